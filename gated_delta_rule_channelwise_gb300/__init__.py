@@ -14,6 +14,9 @@ Public calls (same names as the C ABI without the ``cgdr_`` prefix):
 * :func:`prefill_noalloc` -- prefill with the library's static scratch instead of a workspace.
 * :func:`prefill_workspace_size`, :func:`workspace_status`, :func:`validate`, :func:`status_string`.
 * :func:`prefill_path_for` -- which prefill kernel a call runs.
+* the operators around the delta rule (``include/cgdr_serve.h``, :mod:`.serve`): :func:`conv_prefill`,
+  :func:`conv_decode`, :func:`scan_prefill`, :func:`scan_decode`, :func:`cache_plan`, :func:`cache_append`,
+  :func:`cache_attend`.
 
 The prefill kernel is chosen per call (``path=``, one of the ``PREFILL_*``
 codes; ``PREFILL_AUTO`` by default): the choice travels in the argument
@@ -28,7 +31,8 @@ import threading
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcgdr.so")
 
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS, ERR_RANGE = range(9)
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS, ERR_RANGE, \
+    ERR_CAPACITY = range(10)
 F32, BF16 = 0, 1
 GATE_CHANNEL, GATE_GDN = 0, 1
 PREFILL_AUTO, PREFILL_PER_HEAD, PREFILL_CLUSTER, PREFILL_SIMT, PREFILL_RECURRENT, PREFILL_COOP = range(6)
@@ -84,7 +88,7 @@ def lib():
                 raise RuntimeError("libcgdr.so is not built (%s); run gated_delta_rule_channelwise_gb300.build.build()"
                                    % LIB_PATH)
             L = ctypes.CDLL(LIB_PATH)
-            for name, res, args in _SIGNATURES:
+            for name, res, args in _SIGNATURES + SIGNATURES:
                 fn = getattr(L, name)
                 fn.restype = res
                 fn.argtypes = args
@@ -293,6 +297,11 @@ def validate(A: CgdrArgs, for_prefill: bool) -> int:
     return int(lib().cgdr_validate(ctypes.byref(A), 1 if for_prefill else 0))
 
 
+from .serve import (CachePlan, SIGNATURES, cache_append, cache_attend, cache_attend_workspace_size,  # noqa: E402
+                    cache_plan, conv_decode, conv_prefill, scan_decode, scan_prefill, scan_workspace_size)
+
 __all__ = ["decode", "prefill", "prefill_noalloc", "prefill_workspace_size", "workspace_status", "validate",
            "status_string", "make_args", "prefill_path_for",
+           "conv_prefill", "conv_decode", "scan_prefill", "scan_decode", "scan_workspace_size", "CachePlan",
+           "cache_plan", "cache_append", "cache_attend", "cache_attend_workspace_size",
            "CgdrArgs", "CgdrError", "lib", "LIB_PATH"]

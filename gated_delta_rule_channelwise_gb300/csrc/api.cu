@@ -211,8 +211,9 @@ const char *cgdr_status_string(int s) {
         case CGDR_ERR_WORKSPACE: return "CGDR_ERR_WORKSPACE: workspace too small";
         case CGDR_ERR_CUDA: return "CGDR_ERR_CUDA: a CUDA call or kernel launch failed";
         case CGDR_ERR_TIMEOUT: return "CGDR_ERR_TIMEOUT: a bounded device wait gave up";
-        case CGDR_ERR_BOUNDS: return "CGDR_ERR_BOUNDS: a debug build's device index check failed";
+        case CGDR_ERR_BOUNDS: return "CGDR_ERR_BOUNDS: a device index check failed";
         case CGDR_ERR_RANGE: return "CGDR_ERR_RANGE: an fp16 tensor-core operand left the fp16 range";
+        case CGDR_ERR_CAPACITY: return "CGDR_ERR_CAPACITY: lengths beyond the free pages, the block table or the host's bounds";
         default: return "unknown cgdr status";
     }
 }

@@ -1,0 +1,498 @@
+// Attention over the 8-bit paged cache (cgdr_cache_attend).
+//
+// For single tokens the cache's bytes are the time: 2 D bytes a token and head are read once.  A
+// row tile is the 16 rows of an mma.sync m16n8k16 product -- (query token, query head of the group)
+// pairs that share one key-value head -- and a warp takes 16 cached tokens at a time, all of D: a
+// 16-token piece never crosses a page, is contiguous in the cache, and streams through the warp's
+// own ring of shared-memory stages by cp.async, so the four warps of a block never wait for one
+// another until they join their softmax states at the end.  tcgen05 has no use here: its smallest
+// tile has 64 rows, and one 16-row tile fed at the memory's rate leaves the mma.sync pipe two
+// thirds idle.
+//
+// int8 -> fp16 is exact and takes no conversion instruction: the byte with its sign bit flipped,
+// placed under the exponent byte 0x64, is the fp16 number 1024 + 128 + value, and one packed
+// subtraction leaves the value.  The order of d within a product is free as long as both operands
+// share it, so a lane reads contiguous bytes: for q.k lane l (j = l % 4) has bytes j D/4 .. of key
+// l / 4; for p.v it has bytes (l / 4) D/8 .. of values 2j, 2j+1, 2j+8, 2j+9.
+//
+// The scales stay out of the products: k's multiplies the score; v's becomes part of the exponent,
+// p' = 2^(s + log2 vs - M), with its own running maximum M of s + log2 vs, so that p' lies in (0, 1]
+// whatever the scales are and fits fp16; the denominator adds p' / vs.  A further 2^15 keeps small
+// p' out of fp16's subnormal range (they lose their relative accuracy below 2^-29 of the largest).
+//
+// bf16 queries are scaled by a power of two per row to magnitudes below 2 and are then exact in fp16
+// down to 2^-14 of the row's largest (beyond that their error is below 2^-25 of it).  fp32 queries
+// and their probabilities are carried as two fp16 parts.
+#include "serve.cuh"
+
+#include <cuda_fp16.h>
+
+namespace cgdr {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kRows = 16;                             // rows of a tile
+constexpr int kStep = 16;                             // cached tokens of a warp's step
+constexpr int kStages = 4;
+constexpr int kMaxSplit = 4096;                       // cached tokens of a block: its pages' numbers and scales are staged
+
+struct AttendParams {
+    int B, n, Hq, Hkv, G, page, width, num_pages, max_q, max_kv;
+    int split, splits;                                // tokens of a split, splits
+    float scale;
+    const void *q;
+    void *o;
+    int64_t q_st, q_sh, o_st, o_sh, eq, eo, e_table;
+    const int8_t *kc, *vc;
+    const float *ks, *vs;
+    const int32_t *table;
+    int64_t table_sb;
+    const int32_t *kv_lens, *cu;
+    float *part;                                      // [n * Hq][splits][D + 2]: M, l, o; null: one split
+    int *status;
+};
+
+__device__ __forceinline__ void report(int *status, int code) {
+    if (status != nullptr) atomicExch(status, code);
+}
+
+__device__ __forceinline__ void mma_f16_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+constexpr int kMaxKv = 1 << 27;                       // splits of one request stay within the grid's limit
+// Two sign-flipped int8 in bytes 0 and 2 above exponent bytes -> their values as fp16.
+__device__ __forceinline__ uint32_t less_bias(uint32_t x) {
+    const uint32_t bias = 0x64806480u;                // 1152
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&bias));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t low_pair(uint32_t w) { return less_bias(__byte_perm(w, 0x64646464u, 0x4140)); }
+__device__ __forceinline__ uint32_t high_pair(uint32_t w) { return less_bias(__byte_perm(w, 0x64646464u, 0x4342)); }
+
+// What a block keeps of its split's pages.
+struct PageInfo {
+    int page;                                         // -1: outside the cache
+    float k;                                          // k's scale
+    float lv, iv;                                     // log2 and reciprocal of v's scale; 0 and 1 where it is (as good as) 0
+    bool zero_v;
+};
+
+template <int D, typename T>
+struct AttendShape {
+    static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;              // fp16 parts of q and p
+    static constexpr int STAGE = 2 * kStep * D;                       // k and v bytes of a step
+    static constexpr int RING = kWarps * kStages * STAGE;
+    static constexpr int JOIN = kWarps * kRows * (D + 2) * 4;         // the warps' softmax states, in the ring's place
+    static constexpr int BYTES = RING > JOIN ? RING : JOIN;
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_attend_kernel(const AttendParams p) {
+    using Sh = AttendShape<D, T>;
+    constexpr int PARTS = Sh::PARTS, KS = D / 16, NT = D / 8;         // k steps of q.k, column tiles of p.v
+    extern __shared__ __align__(16) unsigned char smem[];
+    PageInfo *info = reinterpret_cast<PageInfo *>(smem + Sh::BYTES);  // [split / page + 1]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+    const int split = blockIdx.y, b = blockIdx.z, hk = blockIdx.x % p.Hkv, row0 = blockIdx.x / p.Hkv * kRows;
+
+    const int2 span = seq_span(p.cu, b, p.n);
+    const int kv_len = max(p.kv_lens[b], 0);
+    int q_len = span.y - span.x, kv = kv_len;
+    const int most = (int)min((int64_t)p.max_kv, (int64_t)p.width * p.page);
+    if (q_len > p.max_q || kv > most) {
+        if (tid == 0) report(p.status, (int)CGDR_ERR_CAPACITY);
+        kv = min(kv, most);
+        q_len = min(q_len, p.max_q);
+    }
+    const int rows = q_len * p.G;
+    if (row0 >= rows) return;
+    const int behind = kv_len - (span.y - span.x);                     // position of the request's query token 0
+    const int last_row = min(row0 + kRows, rows) - 1;
+    const int begin = split * p.split;
+    const int end = min(min(begin + p.split, kv), behind + last_row / p.G + 1);       // what some row of the tile sees
+    const int steps = end > begin ? (end - begin + kStep - 1) / kStep : 0;
+
+    for (int i = tid; i * p.page < end - begin; i += 32 * kWarps) {
+        PageInfo f;
+        const int64_t at = b * p.table_sb + (begin / p.page + i);
+        f.page = in_bounds(at, p.e_table, p.status, nullptr) ? p.table[at] : -1;
+        f.k = 0.f; f.lv = 0.f; f.iv = 1.f; f.zero_v = true;
+        if (f.page < 0 || f.page >= p.num_pages) {
+            f.page = -1;
+            report(p.status, (int)CGDR_ERR_BOUNDS);
+        } else {
+            f.k = p.ks[(int64_t)f.page * p.Hkv + hk];
+            const float v = p.vs[(int64_t)f.page * p.Hkv + hk];
+            f.zero_v = v < 0x1p-100f;                 // false for a NaN, which then spreads as it has to
+            if (!f.zero_v) { f.lv = log2f(v); f.iv = 1.f / v; }
+        }
+        info[i] = f;
+    }
+
+    // this lane's two rows of the tile, and their queries as A operands
+    int q_tok[2], seen[2];
+    float row_scale[2];
+    uint32_t qa[PARTS][KS][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = row0 + g + 8 * r;
+        const bool ok = row < rows;
+        q_tok[r] = row / p.G;
+        seen[r] = ok ? behind + q_tok[r] + 1 : 0;     // positions below this one
+        float f[D / 4];
+        const int64_t off = (int64_t)(span.x + q_tok[r]) * p.q_st + (int64_t)(hk * p.G + row % p.G) * p.q_sh + j * (D / 4);
+#pragma unroll
+        for (int v = 0; v < D / 4 / Vec<T>::n; ++v) {
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (ok && range_in_bounds(off + v * Vec<T>::n, Vec<T>::n, p.eq, p.status, nullptr))
+                raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + off) + v);
+            Vec<T>::unpack(raw, f + v * Vec<T>::n);
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(f[e]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^ex <= top < 2^(ex + 1), or four times that at the type's end; rows of (almost) nothing stay as they are
+        const int ex = top > 0x1p-100f && top < INFINITY ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+        row_scale[r] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale * kLog2e;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float x = f[4 * s + 2 * c] * down, y = f[4 * s + 2 * c + 1] * down;
+                const uint32_t hi = half2_bits(x, y);
+                qa[0][s][2 * c + r] = hi;
+                if (PARTS == 2) {
+                    const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                    qa[PARTS - 1][s][2 * c + r] = half2_bits(x - back.x, y - back.y);
+                }
+            }
+    }
+    __syncthreads();                                  // the page infos
+
+    unsigned char *ring = smem + warp * kStages * Sh::STAGE;
+    const uint32_t ring_s = smem_u32(ring);
+    auto issue = [&](int step, int stage) {           // copies of a step's 16 keys and 16 values
+        if (step < steps) {
+            const int at = step * kStep;
+            const int page = info[at / p.page].page;
+            if (page >= 0) {
+                const int64_t src = ((int64_t)page * p.Hkv + hk) * p.page * D + (int64_t)(at % p.page) * D;
+#pragma unroll
+                for (int c = 0; c < kStep * D / 16 / 32; ++c) {
+                    const int e = (c * 32 + lane) * 16;
+                    cp_async16(ring_s + stage * Sh::STAGE + e, p.kc + src + e, true);
+                    cp_async16(ring_s + stage * Sh::STAGE + kStep * D + e, p.vc + src + e, true);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+
+    float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) issue(warp + s * kWarps, s);
+    int stage = 0;
+    for (int step = warp; step < steps; step += kWarps) {
+        issue(step + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();                                 // every lane's copies have landed
+        const unsigned char *kb = ring + stage * Sh::STAGE, *vb = kb + kStep * D;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        const PageInfo f = info[step * kStep / p.page];
+        if (f.page < 0) continue;
+        const int at = begin + step * kStep;
+
+        float s[2][4];                                // scores: keys 2j, 2j+1 (+8) for rows g, g+8
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+            uint32_t w[D / 16];                       // bytes j D/4 .. (j+1) D/4 of key g + 8 t
+            const unsigned char *src = kb + (g + 8 * t) * D + j * (D / 4);
+            if (D >= 64) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 r = *reinterpret_cast<const uint4 *>(src + 16 * c);
+                    w[4 * c] = r.x; w[4 * c + 1] = r.y; w[4 * c + 2] = r.z; w[4 * c + 3] = r.w;
+                }
+            } else {
+                const uint2 r = *reinterpret_cast<const uint2 *>(src);
+                w[0] = r.x; w[1] = r.y;
+            }
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+                const uint32_t x = w[c] ^ 0x80808080u, b0 = low_pair(x), b1 = high_pair(x);
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(s[t], qa[part][c], b0, b1);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = e >> 1, pos = at + 8 * t + 2 * j + (e & 1);
+                const float x = fmaf(s[t][e] * f.k, row_scale[r], f.lv);
+                s[t][e] = pos < seen[r] && pos < kv ? x : -INFINITY;
+            }
+        float base[2], shrink[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float m = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = fmaxf(m, M[r]);
+            base[r] = m == -INFINITY ? 0.f : m;       // nothing seen yet: every exponential is 2^-inf = 0
+            shrink[r] = ex2(M[r] - base[r]);
+            M[r] = m;
+        }
+        if (__any_sync(0xffffffffu, shrink[0] != 1.f || shrink[1] != 1.f)) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) l[r] *= shrink[r];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                acc[i][0] *= shrink[0]; acc[i][1] *= shrink[0];
+                acc[i][2] *= shrink[1]; acc[i][3] *= shrink[1];
+            }
+        }
+        uint32_t pa[PARTS][4];                        // p' 2^15 as the A operand
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float x = ex2(s[t][2 * r] - base[r] + 15.f), y = ex2(s[t][2 * r + 1] - base[r] + 15.f);
+                l[r] = fmaf(x + y, f.iv, l[r]);
+                const uint32_t hi = half2_bits(x, y);
+                pa[0][2 * t + r] = f.zero_v ? 0u : hi;
+                if (PARTS == 2) {
+                    const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                    pa[PARTS - 1][2 * t + r] = f.zero_v ? 0u : half2_bits(x - back.x, y - back.y);
+                }
+            }
+        // p.v: column n = l / 4 of tile i is d = (l / 4) D/8 + i
+        constexpr int VB = D / 8;                     // bytes of a lane per value: 16, 8 or 4
+        uint32_t v[4][VB / 4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const unsigned char *src = vb + (2 * j + (t & 1) + 8 * (t >> 1)) * D + g * VB;
+            if (VB == 16) {
+                const uint4 r = *reinterpret_cast<const uint4 *>(src);
+                v[t][0] = r.x; v[t][VB / 4 > 1 ? 1 : 0] = r.y; v[t][VB / 4 > 2 ? 2 : 0] = r.z; v[t][VB / 4 > 3 ? 3 : 0] = r.w;
+            } else if (VB == 8) {
+                const uint2 r = *reinterpret_cast<const uint2 *>(src);
+                v[t][0] = r.x; v[t][VB / 4 > 1 ? 1 : 0] = r.y;
+            } else {
+                v[t][0] = *reinterpret_cast<const uint32_t *>(src);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < VB / 4; ++c) {
+            // bytes 0, 1 (2, 3) of both values of a pair, interleaved
+            const uint32_t x01 = __byte_perm(v[0][c], v[1][c], 0x5140) ^ 0x80808080u, x23 = __byte_perm(v[0][c], v[1][c], 0x7362) ^ 0x80808080u;
+            const uint32_t y01 = __byte_perm(v[2][c], v[3][c], 0x5140) ^ 0x80808080u, y23 = __byte_perm(v[2][c], v[3][c], 0x7362) ^ 0x80808080u;
+            const uint32_t b0[4] = {low_pair(x01), high_pair(x01), low_pair(x23), high_pair(x23)};
+            const uint32_t b1[4] = {low_pair(y01), high_pair(y01), low_pair(y23), high_pair(y23)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(acc[4 * c + i], pa[part], b0[i], b1[i]);
+        }
+        __syncwarp();                                 // the stage is read before it is filled again
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+
+    // join the four warps: [warp][row][M, l, o...] in the ring's place
+    float *join = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        float *to = join + (warp * kRows + g + 8 * r) * (D + 2);
+        if (j == 0) { to[0] = M[r]; to[1] = l[r]; }
+    }
+    // column 2 j + e of tile i stands for d = (2 j + e) D/8 + i
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            join[(warp * kRows + g + 8 * (e >> 1)) * (D + 2) + 2 + (2 * j + (e & 1)) * (D / 8) + i] = acc[i][e];
+    __syncthreads();
+    for (int e = tid; e < kRows * D; e += 32 * kWarps) {
+        const int r = e / D, d = e % D, row = row0 + r;
+        if (row >= rows) continue;
+        const float *from = join + r * (D + 2);
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, from[w * kRows * (D + 2)]);
+        const float at = m == -INFINITY ? 0.f : m;
+        float sum = 0.f, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2(from[w * kRows * (D + 2)] - at);
+            sum = fmaf(f, from[w * kRows * (D + 2) + 1], sum);
+            o = fmaf(f, from[w * kRows * (D + 2) + 2 + d], o);
+        }
+        const int tok = span.x + row / p.G, head = hk * p.G + row % p.G;
+        if (p.part != nullptr) {
+            float *part = p.part + (((int64_t)tok * p.Hq + head) * p.splits + split) * (D + 2);
+            part[2 + d] = o;
+            if (d == 0) { part[0] = m; part[1] = sum; }
+        } else {
+            const int64_t off = (int64_t)tok * p.o_st + (int64_t)head * p.o_sh + d;
+            const float y = sum == 0.f ? 0.f : o / sum;
+            if (in_bounds(off, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off] = Cvt<T>::from_f(y);
+        }
+    }
+}
+
+// Joins the splits of a row: a warp a row, four values of d (or D/32) a lane.
+template <int D, typename T>
+__global__ void __launch_bounds__(128) cache_join_kernel(const AttendParams p) {
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= (int64_t)p.n * p.Hq) return;
+    const int tok = (int)(row / p.Hq), head = (int)(row % p.Hq);
+    int lo = 0, hi = p.B;                             // the request: the first b with cu[b + 1] > tok
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu[mid + 1] > tok) hi = mid;
+        else lo = mid + 1;
+    }
+    if (lo >= p.B) return;
+    const int2 span = seq_span(p.cu, lo, p.n);
+    if (tok < span.x || tok - span.x >= p.max_q) return;
+    const float *part = p.part + row * p.splits * (D + 2);
+    const int most = (int)min((int64_t)p.max_kv, (int64_t)p.width * p.page);
+    const int used = max(0, min(p.splits, (min(p.kv_lens[lo], most) + p.split - 1) / p.split));
+    float m = -INFINITY;
+    for (int s = lane; s < used; s += 32) m = fmaxf(m, part[(int64_t)s * (D + 2)]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float at = m == -INFINITY ? 0.f : m;
+    float sum = 0.f, o[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+    for (int s = 0; s < used; ++s) {
+        const float *from = part + (int64_t)s * (D + 2);
+        const float f = ex2(from[0] - at);
+        sum = fmaf(f, from[1], sum);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, from[2 + lane + 32 * e], o[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+        const int64_t off = (int64_t)tok * p.o_st + (int64_t)head * p.o_sh + lane + 32 * e;
+        const float y = sum == 0.f ? 0.f : o[e] / sum;
+        if (in_bounds(off, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off] = Cvt<T>::from_f(y);
+    }
+}
+
+// Cached tokens of a split: enough blocks for every SM to hold its three, several times over where
+// lengths differ, but no split below 256 tokens, where joining would cost as much as it saves.
+int split_of(const cgdr_attend_args &a) {
+    const int64_t sms = device_sms() > 0 ? device_sms() : 152;       // sizes workspaces without a device, too
+    const int G = a.Hq / a.Hkv;
+    const int64_t tiles = (int64_t)a.B * a.Hkv * (((int64_t)a.max_q * G + kRows - 1) / kRows);
+    const int64_t kv = a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page;
+    int64_t split = kv * tiles / (4 * 3 * sms) + 1;
+    split = split < 256 ? 256 : split > kMaxSplit ? kMaxSplit : split;
+    return (int)((split + 127) / 128 * 128);          // whole pages
+}
+int splits_of(const cgdr_attend_args &a, int split) {
+    const int64_t kv = a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page;
+    return (int)((kv + split - 1) / split);
+}
+
+template <int D, typename T>
+cgdr_status launch_attend(const AttendParams &p, cudaStream_t s) {
+    using Sh = AttendShape<D, T>;
+    static SmemOnce smem_once;
+    constexpr int kMost = Sh::BYTES + (kMaxSplit / 16 + 1) * (int)sizeof(PageInfo);
+    if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_kernel<D, T>), kMost)) return CGDR_ERR_CUDA;
+    const int bytes = Sh::BYTES + (p.split / p.page + 1) * (int)sizeof(PageInfo);
+    const int64_t tiles = ((int64_t)p.max_q * p.G + kRows - 1) / kRows * p.Hkv;
+    cache_attend_kernel<D, T><<<dim3((unsigned)tiles, p.splits > 0 ? p.splits : 1, p.B), 32 * kWarps, bytes, s>>>(p);
+    if (p.part != nullptr) {
+        if (cudaPeekAtLastError() != cudaSuccess) return launched();
+        cache_join_kernel<D, T><<<(unsigned)(((int64_t)p.n * p.Hq + 3) / 4), 128, 0, s>>>(p);
+    }
+    return launched();
+}
+
+template <typename T>
+cgdr_status launch_dim(const AttendParams &p, int D, cudaStream_t s) {
+    return D == 128 ? launch_attend<128, T>(p, s) : D == 64 ? launch_attend<64, T>(p, s) : launch_attend<32, T>(p, s);
+}
+
+cgdr_status check(const cgdr_attend_args *a) {
+    if (!a) return CGDR_ERR_INVALID_ARG;
+    if (a->B < 0 || a->n < 0 || a->Hq <= 0 || a->Hkv <= 0 || a->Hq % a->Hkv != 0 || a->width < 0 || a->num_pages < 0 ||
+        a->max_q < 0 || a->max_kv < 0)
+        return CGDR_ERR_INVALID_ARG;
+    if (!dtype_ok(a->dtype) || !page_ok(a->page) || (a->D != 32 && a->D != 64 && a->D != 128)) return CGDR_ERR_UNSUPPORTED;
+    if (a->B > 65535 || a->n > kMaxTokens || a->max_kv > kMaxKv) return CGDR_ERR_UNSUPPORTED;
+    if (((int64_t)a->max_q * (a->Hq / a->Hkv) + kRows) * a->Hkv > INT32_MAX) return CGDR_ERR_UNSUPPORTED;
+    if (a->B == 0 || a->n == 0 || a->max_q == 0) return CGDR_OK;
+    if (!a->q || !a->o || !a->kv_lens || !a->cu) return CGDR_ERR_INVALID_ARG;
+    if (a->max_kv > 0 && a->width > 0 && (!a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale || !a->block_table))
+        return CGDR_ERR_INVALID_ARG;
+    if (a->table_sb < (a->B > 1 ? a->width : 0)) return CGDR_ERR_INVALID_ARG;
+    if (!aligned_to(a->q, 16) || !aligned_to(a->o, esize(a->dtype)) || !aligned_to(a->k_cache, 16) || !aligned_to(a->v_cache, 16) ||
+        !aligned_to(a->k_scale, 4) || !aligned_to(a->v_scale, 4) || !aligned_to(a->block_table, 4) ||
+        !aligned_to(a->kv_lens, 4) || !aligned_to(a->cu, 4) || !aligned_to(a->status, 4))
+        return CGDR_ERR_ALIGNMENT;
+    const int esz = esize(a->dtype);
+    if (!row_stride_ok(a->q_st, esz) || !row_stride_ok(a->q_sh, esz) || a->o_st < 0 || a->o_sh < 0) return CGDR_ERR_ALIGNMENT;
+    return CGDR_OK;
+}
+
+size_t workspace_of(const cgdr_attend_args &a) {
+    const int splits = splits_of(a, split_of(a));
+    return splits > 1 ? (size_t)a.n * a.Hq * splits * (a.D + 2) * sizeof(float) : 0;
+}
+
+}  // namespace
+}  // namespace cgdr
+
+extern "C" {
+
+size_t cgdr_cache_attend_workspace_size(const cgdr_attend_args *a) {
+    using namespace cgdr;
+    return check(a) != CGDR_OK || a->B == 0 || a->n == 0 || a->max_q == 0 ? 0 : workspace_of(*a);
+}
+
+cgdr_status cgdr_cache_attend(const cgdr_attend_args *a, void *ws, size_t ws_bytes, void *stream) {
+    using namespace cgdr;
+    const cgdr_status st = check(a);
+    if (st != CGDR_OK || a->B == 0 || a->n == 0 || a->max_q == 0) return st;
+    const size_t need = workspace_of(*a);
+    if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned_to(ws, 16))) return CGDR_ERR_WORKSPACE;
+    AttendParams p{};
+    p.B = a->B; p.n = a->n; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = a->Hq / a->Hkv; p.page = a->page; p.width = a->width;
+    p.num_pages = a->num_pages; p.max_q = a->max_q; p.max_kv = a->max_kv;
+    p.split = split_of(*a); p.splits = splits_of(*a, p.split);
+    p.scale = a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->D);
+    p.q = a->q; p.q_st = a->q_st; p.q_sh = a->q_sh; p.o = a->o; p.o_st = a->o_st; p.o_sh = a->o_sh;
+    p.eq = extent3(a->n, a->q_st, a->Hq, a->q_sh, a->D); p.eo = extent3(a->n, a->o_st, a->Hq, a->o_sh, a->D);
+    p.kc = a->k_cache; p.vc = a->v_cache; p.ks = a->k_scale; p.vs = a->v_scale;
+    p.table = a->block_table; p.table_sb = a->table_sb; p.e_table = (a->B - 1) * a->table_sb + a->width;
+    p.kv_lens = a->kv_lens; p.cu = a->cu; p.status = a->status;
+    p.part = need > 0 ? static_cast<float *>(ws) : nullptr;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return a->dtype == CGDR_BF16 ? launch_dim<__nv_bfloat16>(p, a->D, s) : launch_dim<float>(p, a->D, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,448 @@
+"""The operators around the delta rule: causal convolution, selective scan, 8-bit paged cache.
+
+Python side of ``include/cgdr_serve.h``: each call checks types and shapes, packs the argument
+block of its C entry point and runs it on the current CUDA stream (or ``stream``).  As for
+:func:`~gated_delta_rule_channelwise_gb300.decode`, every step runs in the library's kernels and
+there is no CPU fallback.  Outputs that are not given, and workspaces, come from torch's caching
+allocator; with ``stream`` they are allocated on that stream.
+
+* :func:`conv_prefill`, :func:`conv_decode` -- short causal convolution with its state.
+* :func:`scan_prefill`, :func:`scan_decode` -- selective state space scan.
+* :func:`cache_plan` -- block tables and slots of a step, from the requests' lengths.
+* :func:`cache_append` -- quantise new keys and values into the 8-bit cache.
+* :func:`cache_attend` -- attention of the newest tokens over that cache.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+import struct
+
+import torch
+
+from . import BF16, F32, _check, _need_cuda, lib
+
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+class Block:
+    """An argument block: (field, struct code) pairs in the order of the C struct.
+
+    Packing with ``struct`` costs a tenth of filling a ``ctypes.Structure``, which matters for calls of
+    a few microseconds.  ``@`` gives C's own alignment; the last code aligns the size to 8 bytes.
+    """
+
+    def __init__(self, *fields):
+        self.fields = fields
+        self._struct = struct.Struct("@" + "".join(code for _, code in fields) + "0q")
+        self.pack, self.size = self._struct.pack, self._struct.size
+
+    def offset(self, name):
+        code = ""
+        for field, c in self.fields:
+            code += c
+            if field == name:
+                return struct.calcsize("@" + code) - struct.calcsize("@" + c)
+        raise KeyError(name)
+
+
+def _i(names):
+    return [(n, "i") for n in names.split()]
+
+
+def _p(names):
+    return [(n, "P") for n in names.split()]
+
+
+def _strided(name, *strides):
+    return [(name, "P")] + [(name + "_" + s, "q") for s in strides]
+
+
+CONV = Block(*_i("B T C W dtype silu n_tokens reserved"), *_strided("x", "sb", "st"), *_strided("o", "sb", "st"),
+             *_p("weight bias state cu status"))
+SCAN = Block(*_i("B T C N G dtype o_dtype softplus n_tokens reserved"), *_strided("x", "sb", "st"),
+             *_strided("dt", "sb", "st"), *_strided("z", "sb", "st"), *_strided("Bm", "sb", "st"),
+             *_strided("Cm", "sb", "st"), *_strided("o", "sb", "st"), *_p("A_log D dt_bias state cu status"))
+PLAN = Block(*_i("B width page n_tokens F num_pages"), *_p("block_table"), ("table_sb", "q"),
+             *_p("seq_lens new_lens free_pages free_count free_count_out kv_lens cu requests positions slots status"))
+APPEND = Block(*_i("n Hkv D page dtype num_pages"), *_strided("k", "st", "sh"), *_strided("v", "st", "sh"),
+               *_p("slots k_cache v_cache k_scale v_scale status"))
+ATTEND = Block(*_i("B n Hq Hkv D page width dtype num_pages max_q max_kv"), ("scale", "f"), *_strided("q", "st", "sh"),
+               *_strided("o", "st", "sh"), *_p("k_cache v_cache k_scale v_scale block_table"), ("table_sb", "q"),
+               *_p("kv_lens cu status"))
+
+
+def _on(stream, fn, *args, **kw):
+    """fn with ``stream`` as the current one: what it allocates belongs to that stream, too."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _handle():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _code(t, name):
+    try:
+        return _CODES[t.dtype]
+    except KeyError:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype)) from None
+
+
+def _typed(dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+
+
+def _shaped(t, shape, name):
+    if t is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def _dense(t, shape, name):
+    _shaped(t, shape, name)
+    if t is not None and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _address(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _status_word(status):
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda):
+        raise TypeError("status must be an int32 CUDA tensor")
+    return _address(status)
+
+
+def _rows(t, name, packed):
+    """(pointer, batch stride, token stride) of [B, T, C], or of packed [n, C]."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError("%s: innermost dimension must be contiguous" % name)
+    return (t.data_ptr(), 0, st[0]) if packed else (t.data_ptr(), st[0], st[1])
+
+
+def _grouped(t, name, packed):
+    """The same for [B, T, G, N] or packed [n, G, N], whose groups have to be dense."""
+    st = t.stride()
+    if (st[-1] != 1 and t.shape[-1] > 1) or (t.shape[-2] > 1 and st[-2] != t.shape[-1]):
+        raise ValueError("%s: the last two dimensions must be contiguous" % name)
+    return (t.data_ptr(), 0, st[0]) if packed else (t.data_ptr(), st[0], st[1])
+
+
+def _heads(t, name):
+    """(pointer, token stride, head stride) of [n, H, D]."""
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
+        raise ValueError("%s: innermost dimension must be contiguous" % name)
+    return t.data_ptr(), st[0], st[1]
+
+
+def _sequences(x, state, cu, name):
+    """(B, T, packed tokens) of dense [B, T, ...] or packed [n, ...] rows with offsets."""
+    if cu is None:
+        return x.shape[0], x.shape[1], 0
+    B = cu.numel() - 1
+    if cu.dtype != torch.int32 or not cu.is_contiguous() or cu.dim() != 1 or B < 0:
+        raise TypeError("cu_seqlens must be a dense int32 tensor of B + 1 offsets")
+    if state.shape[0] != B:
+        raise ValueError("state has %d sequences, cu_seqlens %d" % (state.shape[0], B))
+    return B, 0, x.shape[0]
+
+
+# --------------------------------------------------------------------------- convolution
+
+
+def _conv(x, weight, state, o, bias, silu, cu, status, packed, where):
+    _need_cuda(x, weight, state, o, bias, cu)
+    if o is None:
+        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    B, T, n = _sequences(x, state, cu, "x")
+    C = x.shape[-1]
+    W = weight.shape[-1]
+    _typed(torch.float32, weight=weight, bias=bias)
+    _typed(x.dtype, state=state, o=o)
+    _shaped(o, x.shape, "o")
+    _dense(weight, (C, W), "weight")
+    _dense(bias, (C,), "bias")
+    _dense(state, (B, W - 1, C), "state")
+    block = CONV.pack(B, T, C, W, _code(x, "x"), 1 if silu else 0, n, 0, *_rows(x, "x", packed), *_rows(o, "o", packed),
+                      weight.data_ptr(), _address(bias), state.data_ptr(), _address(cu), _status_word(status))
+    _check(lib().cgdr_conv(block, _handle()), where)
+    return o
+
+
+def conv_prefill(x, weight, state, o=None, *, bias=None, silu=True, cu_seqlens=None, status=None, stream=None):
+    """Short causal convolution over prompts: ``x [B,T,C]``, or packed ``[n,C]`` with
+    ``cu_seqlens [B+1]`` (int32, on the device).  ``weight [C,W]`` fp32 (W = 2, 3 or 4, the last
+    column meets the current token), ``bias [C]`` fp32, SiLU unless ``silu=False``.  ``state [B,W-1,C]``
+    in x's dtype holds the rows before x and is updated in place (zeros start a sequence).
+    x and o may be strided in batch and tokens; rows are 16-byte aligned.  Returns o, like x."""
+    if stream is not None:
+        return _on(stream, conv_prefill, x, weight, state, o, bias=bias, silu=silu, cu_seqlens=cu_seqlens, status=status)
+    if x.dim() != (3 if cu_seqlens is None else 2):
+        raise ValueError("x must be [B, T, C], or packed [n, C] with cu_seqlens")
+    return _conv(x, weight, state, o, bias, silu, cu_seqlens, status, cu_seqlens is not None, "cgdr_conv")
+
+
+def conv_decode(x, weight, state, o=None, *, bias=None, silu=True, status=None, stream=None):
+    """One token of :func:`conv_prefill` for every sequence: ``x [B,C]``."""
+    if stream is not None:
+        return _on(stream, conv_decode, x, weight, state, o, bias=bias, silu=silu, status=status)
+    if x.dim() != 2:
+        raise ValueError("x must be [B, C]")
+    if o is None:
+        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _conv(x.unsqueeze(1), weight, state, o.unsqueeze(1), bias, silu, None, status, False, "cgdr_conv")
+    return o
+
+
+# --------------------------------------------------------------------------- scan
+
+
+def _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, cu, workspace, status, where):
+    _need_cuda(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, cu, workspace)
+    packed = cu is not None
+    if o is None:
+        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    B, T, n = _sequences(x, state, cu, "x")
+    C, (G, N) = x.shape[-1], Bm.shape[-2:]
+    _typed(torch.float32, A_log=A_log, state=state, D=D, dt_bias=dt_bias)
+    _typed(x.dtype, dt=dt, z=z, Bm=Bm, Cm=Cm)
+    for name, t in (("dt", dt), ("z", z), ("o", o)):
+        _shaped(t, x.shape, name)
+    for name, t in (("Bm", Bm), ("Cm", Cm)):
+        _shaped(t, (*x.shape[:-1], G, N), name)
+    _dense(A_log, (C, N), "A_log")
+    _dense(state, (B, C, N), "state")
+    _dense(D, (C,), "D")
+    _dense(dt_bias, (C,), "dt_bias")
+    block = SCAN.pack(B, T, C, N, G, _code(x, "x"), _code(o, "o"), 1 if softplus else 0, n, 0,
+                      *_rows(x, "x", packed), *_rows(dt, "dt", packed), *(_rows(z, "z", packed) if z is not None else (0, 0, 0)),
+                      *_grouped(Bm, "Bm", packed), *_grouped(Cm, "Cm", packed), *_rows(o, "o", packed),
+                      A_log.data_ptr(), _address(D), _address(dt_bias), state.data_ptr(), _address(cu), _status_word(status))
+    L = lib()
+    need = 0 if T == 1 and not packed else L.cgdr_scan_workspace_size(block)
+    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _check(L.cgdr_scan(block, workspace.data_ptr() if need else None, need, _handle()), where)
+    return o
+
+
+def scan_prefill(x, dt, A_log, Bm, Cm, state, o=None, *, D=None, z=None, dt_bias=None, softplus=True, cu_seqlens=None,
+                 workspace=None, status=None, stream=None):
+    """Selective state space scan over prompts: ``x, dt, z [B,T,C]``, ``Bm, Cm [B,T,G,N]`` (group g serves
+    channels g C/G .. (g+1) C/G - 1), or the same packed ``[n,C]``, ``[n,G,N]`` with ``cu_seqlens [B+1]``.
+    ``A_log [C,N]``, ``D [C]``, ``dt_bias [C]`` fp32; ``state [B,C,N]`` fp32, updated in place.
+
+    With ``d = softplus(dt + dt_bias)``: ``h = exp(-exp(A_log) d) h + d x Bm``, ``o = Cm.h + D x``, times
+    ``z / (1 + e^-z)`` if z is given.  N is 16, 32, 64 or 128 and C/G a multiple of 8.  Returns o: the given one
+    (fp32 or bf16) or a new one like x.  ``workspace``: a buffer of :func:`scan_workspace_size` bytes or
+    more keeps the call free of allocations."""
+    if stream is not None:
+        return _on(stream, scan_prefill, x, dt, A_log, Bm, Cm, state, o, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
+                   cu_seqlens=cu_seqlens, workspace=workspace, status=status)
+    lead = 1 if cu_seqlens is not None else 2
+    if x.dim() != lead + 1 or Bm.dim() != lead + 2:
+        raise ValueError("x must be [B, T, C] and Bm [B, T, G, N], or packed [n, C] and [n, G, N] with cu_seqlens")
+    return _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, cu_seqlens, workspace, status, "cgdr_scan")
+
+
+def scan_decode(x, dt, A_log, Bm, Cm, state, o=None, *, D=None, z=None, dt_bias=None, softplus=True, status=None,
+                stream=None):
+    """One token of :func:`scan_prefill` for every sequence: ``x, dt, z [B,C]``, ``Bm, Cm [B,G,N]``."""
+    if stream is not None:
+        return _on(stream, scan_decode, x, dt, A_log, Bm, Cm, state, o, D=D, z=z, dt_bias=dt_bias, softplus=softplus,
+                   status=status)
+    if x.dim() != 2 or Bm.dim() != 3:
+        raise ValueError("x must be [B, C] and Bm [B, G, N]")
+    if o is None:
+        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    u = lambda t: None if t is None else t.unsqueeze(1)
+    _scan(u(x), u(dt), A_log, u(Bm), u(Cm), state, u(o), D, u(z), dt_bias, softplus, None, None, status, "cgdr_scan")
+    return o
+
+
+def scan_workspace_size(B, T, C, N, G=1, *, n_tokens=None, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace of a :func:`scan_prefill` of these sizes (``n_tokens``: packed, with T ignored)."""
+    esz = 2 if dtype == torch.bfloat16 else 4
+    fake = 1 << 20                                    # checked for alignment, never read
+    rows = (fake, 0 if n_tokens is not None else C * T, C)
+    groups = (fake, 0 if n_tokens is not None else G * N * T, G * N)
+    block = SCAN.pack(B, T, C, N, G, _CODES[dtype], _CODES[dtype], 1, n_tokens or 0, 0, *rows, *rows, 0, 0, 0, *groups,
+                      *groups, *rows, fake, 0, 0, fake, fake if n_tokens is not None else 0, 0)
+    return lib().cgdr_scan_workspace_size(block)
+
+
+# --------------------------------------------------------------------------- 8-bit cache
+
+
+@dataclasses.dataclass
+class CachePlan:
+    """What :func:`cache_plan` writes: see there."""
+    slots: torch.Tensor         # [n] int64
+    kv_lens: torch.Tensor       # [B] int32
+    cu_seqlens: torch.Tensor    # [B + 1] int32
+    free_count: torch.Tensor    # [1] int32
+    requests: torch.Tensor      # [n] int32
+    positions: torch.Tensor     # [n] int32
+
+    @classmethod
+    def empty(cls, B, n_tokens, device="cuda"):
+        words = torch.empty(2 * B + 2 + 2 * n_tokens, dtype=torch.int32, device=device)
+        kv, cu, count, req, pos = words.split([B, B + 1, 1, n_tokens, n_tokens])
+        return cls(torch.empty(n_tokens, dtype=torch.int64, device=device), kv, cu, count, req, pos)
+
+
+def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens, page, out=None, *, num_pages=None,
+               status=None, stream=None):
+    """Block tables and slots of a step, on the device.  Request b holds ``seq_lens[b]`` cached tokens in
+    the first pages of its row of ``block_table [B,width]`` and gets ``new_lens[b]`` more; the pages it
+    needs come off the top of the stack ``free_pages[:free_count]``, in request order, and are entered into
+    block_table (in place).  All int32.  Returns a :class:`CachePlan` (``out``, or a new one):
+
+    ``cu_seqlens`` prefix sums of new_lens; ``kv_lens = seq_lens + new_lens``; per packed new token its
+    ``requests``, ``positions`` (place in the request) and ``slots`` (int64 ``page_number * page + place in
+    the page``), -1 from the last new token to ``n_tokens``; ``free_count`` pages left.
+
+    If the pages, the table's width or ``n_tokens`` do not suffice nothing is taken: every slot is -1, lengths
+    and free count stay, and ``status`` receives ``ERR_CAPACITY`` (``ERR_INVALID_ARG`` for negative lengths
+    and for free pages outside ``num_pages``, by default any number)."""
+    if stream is not None:
+        return _on(stream, cache_plan, block_table, seq_lens, new_lens, free_pages, free_count, n_tokens, page, out,
+                   num_pages=num_pages, status=status)
+    _need_cuda(block_table, seq_lens, new_lens, free_pages, free_count)
+    _typed(torch.int32, block_table=block_table, seq_lens=seq_lens, new_lens=new_lens, free_pages=free_pages,
+           free_count=free_count)
+    B, width = block_table.shape
+    if out is None:
+        out = CachePlan.empty(B, n_tokens, block_table.device)
+    else:
+        _need_cuda(out.slots, out.kv_lens, out.cu_seqlens, out.free_count, out.requests, out.positions)
+        _typed(torch.int32, kv_lens=out.kv_lens, cu_seqlens=out.cu_seqlens, free_count=out.free_count,
+               requests=out.requests, positions=out.positions)
+        _typed(torch.int64, slots=out.slots)
+        for name, t, size in (("kv_lens", out.kv_lens, B), ("cu_seqlens", out.cu_seqlens, B + 1),
+                              ("free_count", out.free_count, 1), ("slots", out.slots, n_tokens),
+                              ("requests", out.requests, n_tokens), ("positions", out.positions, n_tokens)):
+            _dense(t, (size,), "out." + name)
+    _dense(seq_lens, (B,), "seq_lens")
+    _dense(new_lens, (B,), "new_lens")
+    _dense(free_pages, (free_pages.numel(),), "free_pages")
+    _dense(free_count, (1,), "free_count")
+    sb, sw = block_table.stride()
+    if sw != 1 and width > 1:
+        raise ValueError("block_table: innermost dimension must be contiguous")
+    block = PLAN.pack(B, width, page, n_tokens, free_pages.shape[0], 0x7FFFFFFF if num_pages is None else num_pages,
+                      block_table.data_ptr(), sb, seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+                      free_count.data_ptr(), out.free_count.data_ptr(), out.kv_lens.data_ptr(),
+                      out.cu_seqlens.data_ptr(), out.requests.data_ptr(), out.positions.data_ptr(),
+                      out.slots.data_ptr(), _status_word(status))
+    _check(lib().cgdr_cache_plan(block, _handle()), "cgdr_cache_plan")
+    return out
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale):
+    """(pages, Hkv, page, D) of a cache: int8 [pages, Hkv, page, D] with fp32 scales [pages, Hkv]."""
+    _need_cuda(k_cache, v_cache, k_scale, v_scale)
+    _typed(torch.int8, k_cache=k_cache, v_cache=v_cache)
+    _typed(torch.float32, k_scale=k_scale, v_scale=v_scale)
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError("k_cache must be [pages, Hkv, page, D]")
+    _dense(k_cache, shape, "k_cache")
+    _dense(v_cache, shape, "v_cache")
+    _dense(k_scale, shape[:2], "k_scale")
+    _dense(v_scale, shape[:2], "v_scale")
+    return shape
+
+
+def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, status=None, stream=None):
+    """Quantise ``k, v [n,Hkv,D]`` (fp32 or bf16) into the cache: ``k_cache, v_cache`` int8
+    ``[pages,Hkv,page,D]``, ``k_scale, v_scale`` fp32 ``[pages,Hkv]``, all updated in place.  Token i goes to
+    ``slots[i]`` (int64, as :func:`cache_plan` gives them: tokens of a page consecutive and ascending; below 0:
+    nowhere).  A page's scale of a head is the largest magnitude in it / 127; where new values raise it, what
+    the page holds is rounded to the larger scale.  A token at a page's offset 0 starts the page afresh.  A
+    slot outside the cache is skipped and reported in ``status`` (``ERR_BOUNDS``)."""
+    if stream is not None:
+        return _on(stream, cache_append, k, v, slots, k_cache, v_cache, k_scale, v_scale, status=status)
+    pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    _need_cuda(k, v, slots)
+    _typed(k.dtype, v=v)
+    n = k.shape[0]
+    _shaped(k, (n, Hkv, D), "k")
+    _shaped(v, (n, Hkv, D), "v")
+    _typed(torch.int64, slots=slots)
+    _dense(slots, (n,), "slots")
+    block = APPEND.pack(n, Hkv, D, page, _code(k, "k"), pages, *_heads(k, "k"), *_heads(v, "v"), slots.data_ptr(),
+                        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                        _status_word(status))
+    _check(lib().cgdr_cache_append(block, _handle()), "cgdr_cache_append")
+
+
+def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o=None, *, max_q, max_kv=None,
+                 scale=None, workspace=None, status=None, stream=None):
+    """Attention of the newest tokens over the cache (layout as in :func:`cache_append`).  ``q [n,Hq,D]`` (fp32 or
+    bf16) packs the query tokens of all requests, ``cu_seqlens [B+1]`` says whose they are; they are the last of
+    the ``kv_lens[b]`` cached tokens, each sees the tokens up to itself, and a row that sees nothing is zero.
+    ``block_table [B,width]``, ``kv_lens``, ``cu_seqlens`` int32 as :func:`cache_plan` leaves them.  Query head h
+    reads key-value head h / (Hq/Hkv); ``scale`` defaults to 1/sqrt(D).
+
+    ``max_q`` and ``max_kv`` bound the requests' query and cached tokens on the host (default for max_kv: what
+    the table holds); what exceeds them is cut off and reported in ``status`` (``ERR_CAPACITY``), and pages
+    outside the cache are left out (``ERR_BOUNDS``).  Rows of q past ``cu_seqlens[B]`` are not computed.  Returns
+    o ``[n,Hq,D]``, like q.  ``workspace``: a buffer of :func:`cache_attend_workspace_size` bytes or more keeps
+    the call free of allocations."""
+    if stream is not None:
+        return _on(stream, cache_attend, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o,
+                   max_q=max_q, max_kv=max_kv, scale=scale, workspace=workspace, status=status)
+    pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _need_cuda(q, o, block_table, kv_lens, cu_seqlens, workspace)
+    n, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError("q has head dimension %d, the cache %d" % (Dq, D))
+    _typed(q.dtype, o=o)
+    _shaped(o, q.shape, "o")
+    _typed(torch.int32, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens)
+    B, width = block_table.shape
+    _dense(kv_lens, (B,), "kv_lens")
+    _dense(cu_seqlens, (B + 1,), "cu_seqlens")
+    sb, sw = block_table.stride()
+    if sw != 1 and width > 1:
+        raise ValueError("block_table: innermost dimension must be contiguous")
+    block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _code(q, "q"), pages, max_q, width * page if max_kv is None else max_kv,
+                        0.0 if scale is None else scale, *_heads(q, "q"), *_heads(o, "o"), k_cache.data_ptr(),
+                        v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), sb,
+                        kv_lens.data_ptr(), cu_seqlens.data_ptr(), _status_word(status))
+    L = lib()
+    need = L.cgdr_cache_attend_workspace_size(block)
+    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(L.cgdr_cache_attend(block, workspace.data_ptr() if need else None, need, _handle()), "cgdr_cache_attend")
+    return o
+
+
+def cache_attend_workspace_size(B, n, Hq, Hkv, D, page, width, *, max_q, max_kv=None, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace of a :func:`cache_attend` of these sizes."""
+    fake = 1 << 20                                    # checked for alignment, never read
+    block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _CODES[dtype], 1, max_q, width * page if max_kv is None else max_kv,
+                        0.0, fake, Hq * D, D, fake, Hq * D, D, fake, fake, fake, fake, fake, width, fake, fake, 0)
+    return lib().cgdr_cache_attend_workspace_size(block)
+
+
+#: (name, restype, argtypes) of every symbol include/cgdr_serve.h declares.
+SIGNATURES = [
+    ("cgdr_conv", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_scan_workspace_size", ctypes.c_size_t, [ctypes.c_char_p]),
+    ("cgdr_scan", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    ("cgdr_cache_plan", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_cache_append", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_cache_attend_workspace_size", ctypes.c_size_t, [ctypes.c_char_p]),
+    ("cgdr_cache_attend", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+]

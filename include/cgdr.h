@@ -72,13 +72,17 @@ typedef enum cgdr_status {
     CGDR_ERR_WORKSPACE = 4,     /* workspace smaller than cgdr_prefill_workspace_size() */
     CGDR_ERR_CUDA = 5,          /* a CUDA runtime call or launch failed */
     CGDR_ERR_TIMEOUT = 6,       /* a bounded device-side wait gave up (reported through a status word) */
-    CGDR_ERR_BOUNDS = 7,        /* debug build only: a device-side index check failed (through a status
-                                   word); the access was skipped */
-    CGDR_ERR_RANGE = 8          /* a tensor-core prefill met a value of magnitude above 65504 in one of
+    CGDR_ERR_BOUNDS = 7,        /* a device-side index check failed (through a status word); the access
+                                   was skipped.  The calls of cgdr.h: debug build only; the cache calls
+                                   of cgdr_serve.h check the pages and slots they are given in every build */
+    CGDR_ERR_RANGE = 8,         /* a tensor-core prefill met a value of magnitude above 65504 in one of
                                    its fp16 operands (v, the triangular transform, U, or a
                                    decay-scaled key or query when g > 0 grows them); reported through
                                    the status words, the outputs are then invalid: run that call with
                                    CGDR_PREFILL_SIMT */
+    CGDR_ERR_CAPACITY = 9       /* a cache call of cgdr_serve.h met lengths that the free pages, the block
+                                   table or the bounds given by the host do not hold (through a status
+                                   word) */
 } cgdr_status;
 
 typedef enum cgdr_dtype { CGDR_F32 = 0, CGDR_BF16 = 1 } cgdr_dtype;
