@@ -17,8 +17,6 @@
 namespace cgdr {
 namespace {
 
-constexpr int kCh = 16;                               // channels of a block
-constexpr int kTok = 32;                              // tokens of a tile
 
 struct ScanParams {
     int B, T, C, Cg, G, n, chunk, softplus, o_f32;
@@ -104,6 +102,29 @@ __device__ __forceinline__ float softplus_series(float x) {
     return fmaxf(x, 0.f) + 2.f * s * r;
 }
 
+// Pairs of fp32 in a 64-bit register: one instruction for two multiply-adds (the arithmetic rate
+// is that of two, the issue slot is saved).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // Eight consecutive elements as stored, and as fp32.
 template <typename T> struct Eight;
 template <> struct Eight<__nv_bfloat16> {
@@ -130,81 +151,120 @@ __device__ __forceinline__ void fetch(Eight<T> &v, const void *base, int64_t off
     if (ok && range_in_bounds(off, 8, n, st, nullptr)) v.load(static_cast<const T *>(base) + off);
 }
 
+// A block's shape.  A thread holds four states of each of four neighbouring channels: every value of
+// d, d x, B and C that it reads from shared memory meets four states, which brings the reads (128 bytes
+// a clock of the SM) to the level of the arithmetic; with four states of one channel they are twice
+// the time of everything else.
+template <int N>
+struct ScanShape {
+    static constexpr int LPC = N / 4;                                 // lanes that share four channels
+    static constexpr int CH = N <= 64 ? 1024 / N : 16;                // channels of a block
+    static constexpr int NT = CH / 4 * LPC;                           // 64 threads, 128 for N = 128
+    static constexpr int TT = N == 16 ? 8 : 16;                       // tokens of a tile
+    static constexpr int XV = TT * CH / 8;                            // eight-channel vectors of a tile (at most NT)
+    static constexpr int BV = TT * N / 8, BPT = (BV + NT - 1) / NT;   // eight-state vectors, and of a thread
+    static_assert(XV <= NT, "one vector of x a thread");
+};
+template <int N, bool kEnds>
+struct ScanTile {
+    using Sh = ScanShape<N>;
+    float2 du[Sh::TT][Sh::CH];                                        // d, d x
+    float b[Sh::TT][N], c[kEnds ? 1 : Sh::TT][N];
+    float y[kEnds ? 1 : Sh::TT][4][Sh::CH + 8];                       // four parts of every y, each in banks of its own
+};
+
 // kEnds: the first launch (end states and sums of d of every chunk but a sequence's last).
 template <typename T, int N, bool kEnds>
-__global__ void __launch_bounds__(4 * N) scan_kernel(const ScanParams p) {
-    constexpr int LPC = N / 4;                        // lanes of a channel
-    __shared__ __align__(16) float2 s_du[kTok][kCh];  // d, d x
-    __shared__ __align__(16) float s_B[kTok][N];
-    __shared__ __align__(16) float s_C[kEnds ? 1 : kTok][N];
-    __shared__ __align__(16) float s_y[kEnds ? 1 : kTok][kCh];
-    const int tid = threadIdx.x, ch = tid / LPC, q = tid % LPC;
+__global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kernel(const ScanParams p) {
+    using Sh = ScanShape<N>;
+    constexpr int LPC = Sh::LPC, TT = Sh::TT;
+    __shared__ __align__(16) ScanTile<N, kEnds> sm;
+    const int tid = threadIdx.x, ch = tid / LPC * 4, q = tid % LPC;   // channels ch .. ch + 3, states 4 q .. 4 q + 3
     const Piece pc = find_piece(p, blockIdx.y, kEnds);
     if (pc.b < 0 || (kEnds && pc.k == pc.chunks - 1)) return;
     if (pc.chunks > 1 && pc.slot + pc.chunks > p.slots) return;       // offsets that do not ascend: more tokens than there are
-    const int per = (p.Cg + kCh - 1) / kCh;           // blocks of a group
-    const int g = blockIdx.x / per, cg0 = (blockIdx.x % per) * kCh, c0 = g * p.Cg + cg0;
-    const bool live = cg0 + ch < p.Cg;
+    const int per = (p.Cg + Sh::CH - 1) / Sh::CH;                     // blocks of a group
+    const int g = blockIdx.x / per, cg0 = (blockIdx.x % per) * Sh::CH, c0 = g * p.Cg + cg0;
+    const bool live = cg0 + ch < p.Cg;                                // Cg is a multiple of 8: all four channels or none
     const int c = live ? c0 + ch : c0;
 
-    float A[4], h[4];
-    {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p.A_log + (int64_t)c * N + 4 * q));
-        A[0] = -kLog2e * expf(a.x); A[1] = -kLog2e * expf(a.y); A[2] = -kLog2e * expf(a.z); A[3] = -kLog2e * expf(a.w);
+    float A[4][4];
+    f32x2 h[4][2] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p.A_log + (int64_t)(c + i) * N + 4 * q));
+        A[i][0] = -kLog2e * expf(a.x); A[i][1] = -kLog2e * expf(a.y);
+        A[i][2] = -kLog2e * expf(a.z); A[i][3] = -kLog2e * expf(a.w);
     }
-    auto load4 = [&](const float *src) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
+    // h <- exp(A d) h + in, for the four states of channel i
+    auto step = [&](int i, float d, f32x2 in0, f32x2 in1) {
+        h[i][0] = fma2(pair(ex2(d * A[i][0]), ex2(d * A[i][1])), h[i][0], in0);
+        h[i][1] = fma2(pair(ex2(d * A[i][2]), ex2(d * A[i][3])), h[i][1], in1);
+    };
+    auto load_h = [&](const float *src) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(src + i * N);
+            h[i][0] = v.x; h[i][1] = v.y;
+        }
+    };
+    auto store_h = [&](float *dst) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<ulonglong2 *>(dst + i * N) = make_ulonglong2(h[i][0], h[i][1]);
     };
     float *hs = p.state + ((int64_t)pc.b * p.C + c) * N + 4 * q;
     auto end_of = [&](int k) { return p.ends + ((int64_t)(pc.slot + k) * p.C + c) * N + 4 * q; };
     if (pc.k == 0) {
         // the state of a sequence of several chunks is replaced by its last chunk's block, maybe
         // before this one starts: the first launch leaves a copy in the last chunk's slot
-        if (kEnds || pc.chunks == 1) load4(hs);
-        else load4(end_of(pc.chunks - 1));
-        if (kEnds && live) *reinterpret_cast<float4 *>(end_of(pc.chunks - 1)) = make_float4(h[0], h[1], h[2], h[3]);
-    } else if (kEnds) {
-        h[0] = h[1] = h[2] = h[3] = 0.f;
-    } else {                                          // join the chunks before this one
-        load4(end_of(0));
+        if (kEnds || pc.chunks == 1) load_h(hs);
+        else load_h(end_of(pc.chunks - 1));
+        if (kEnds && live) store_h(end_of(pc.chunks - 1));
+    } else if (!kEnds) {                              // join the chunks before this one
+        load_h(end_of(0));
+#pragma unroll 4
         for (int k = 1; k < pc.k; ++k) {
-            const float d = p.sums[(int64_t)(pc.slot + k) * p.C + c];
-            const float4 e = *reinterpret_cast<const float4 *>(end_of(k));
-            h[0] = fmaf(ex2(d * A[0]), h[0], e.x); h[1] = fmaf(ex2(d * A[1]), h[1], e.y);
-            h[2] = fmaf(ex2(d * A[2]), h[2], e.z); h[3] = fmaf(ex2(d * A[3]), h[3], e.w);
+            const float4 d = *reinterpret_cast<const float4 *>(p.sums + (int64_t)(pc.slot + k) * p.C + c);
+            const float ds[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(end_of(k) + i * N);
+                step(i, ds[i], e.x, e.y);
+            }
         }
     }
 
-    // staging: threads 0 .. 63 take eight channels of a token each, every thread eight states of B and C
-    const int xt = tid >> 1, xc = (tid & 1) * 8;
-    const bool xlive = tid < 2 * kTok && cg0 + xc < p.Cg;
-    const int bt = tid / (N / 8), bn = (tid % (N / 8)) * 8;
-    Eight<T> rx, rd, rz, rb, rc;
+    // staging: eight channels of a token, and eight states of a token's B and C, to a thread
+    const int xt = tid / (Sh::CH / 8), xc = tid % (Sh::CH / 8) * 8;
+    const bool stages = tid < Sh::XV, xlive = stages && cg0 + xc < p.Cg;
+    Eight<T> rx, rd, rz, rb[Sh::BPT], rc[Sh::BPT];
     float bias[8], skip[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         bias[e] = xlive && p.dt_bias != nullptr ? __ldg(p.dt_bias + c0 + xc + e) : 0.f;
-        skip[e] = xlive && p.D != nullptr ? __ldg(p.D + c0 + xc + e) : 0.f;
+        skip[e] = !kEnds && xlive && p.D != nullptr ? __ldg(p.D + c0 + xc + e) : 0.f;
     }
     const bool packed = p.cu != nullptr;
     auto row = [&](int64_t sb, int64_t st, int t) { return (packed ? 0 : pc.b * sb) + (int64_t)t * st; };
     auto load = [&](int first) {
-        const int t = pc.t0 + first + xt, tb = pc.t0 + first + bt;
-        const bool ok = xlive && first + xt < pc.len, okb = first + bt < pc.len;
+        const int t = pc.t0 + first + xt;
+        const bool ok = xlive && first + xt < pc.len;
         fetch<T>(rx, p.x, row(p.x_sb, p.x_st, t) + c0 + xc, ok, p.ex, p.status);
         fetch<T>(rd, p.dt, row(p.dt_sb, p.dt_st, t) + c0 + xc, ok, p.edt, p.status);
-        fetch<T>(rb, p.Bm, row(p.B_sb, p.B_st, tb) + g * N + bn, okb, p.eB, p.status);
-        if (!kEnds) {
-            fetch<T>(rc, p.Cm, row(p.C_sb, p.C_st, tb) + g * N + bn, okb, p.eC, p.status);
-            fetch<T>(rz, p.z, row(p.z_sb, p.z_st, t) + c0 + xc, ok && p.z != nullptr, p.ez, p.status);
+        if (!kEnds) fetch<T>(rz, p.z, row(p.z_sb, p.z_st, t) + c0 + xc, ok && p.z != nullptr, p.ez, p.status);
+#pragma unroll
+        for (int i = 0; i < Sh::BPT; ++i) {
+            const int v = tid + i * Sh::NT, bt = first + v / (N / 8), bn = g * N + v % (N / 8) * 8;
+            const bool okb = v < Sh::BV && bt < pc.len;
+            fetch<T>(rb[i], p.Bm, row(p.B_sb, p.B_st, pc.t0 + bt) + bn, okb, p.eB, p.status);
+            if (!kEnds) fetch<T>(rc[i], p.Cm, row(p.C_sb, p.C_st, pc.t0 + bt) + bn, okb, p.eC, p.status);
         }
     };
     load(0);
-    float total = 0.f;
-    for (int first = 0; first < pc.len; first += kTok) {
-        float dx[8], gate[8];                         // what the tile's outputs need again: D x, and the gate
-        if (tid < 2 * kTok) {
+    float total[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int first = 0; first < pc.len; first += TT) {
+        const Eight<T> px = rx, pz = rz;              // what the tile's outputs need again
+        if (stages) {
             float x[8], d[8];
             rx.get(x);
             rd.get(d);
@@ -214,51 +274,93 @@ __global__ void __launch_bounds__(4 * N) scan_kernel(const ScanParams p) {
                 float v = d[e] + bias[e];
                 if (p.softplus) v = softplus_series(v);
                 if (!ok) v = 0.f;                     // past the end: exp(0) h + 0
-                s_du[xt][xc + e] = make_float2(v, v * x[e]);
-                dx[e] = skip[e] * x[e];
+                d[e] = v;
+                x[e] *= v;
             }
-            if (!kEnds) rz.get(gate);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+                *reinterpret_cast<float4 *>(&sm.du[xt][xc + e]) = make_float4(d[e], x[e], d[e + 1], x[e + 1]);
         }
-        {
-            float f[8];
-            rb.get(f);
-            *reinterpret_cast<float4 *>(&s_B[bt][bn]) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4 *>(&s_B[bt][bn + 4]) = make_float4(f[4], f[5], f[6], f[7]);
-            if (!kEnds) {
-                rc.get(f);
-                *reinterpret_cast<float4 *>(&s_C[bt][bn]) = make_float4(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<float4 *>(&s_C[bt][bn + 4]) = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+        for (int i = 0; i < Sh::BPT; ++i) {
+            const int v = tid + i * Sh::NT;
+            if (v < Sh::BV) {
+                float f[8];
+                rb[i].get(f);
+                float4 *to = reinterpret_cast<float4 *>(&sm.b[v / (N / 8)][v % (N / 8) * 8]);
+                to[0] = make_float4(f[0], f[1], f[2], f[3]);
+                to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                if (!kEnds) {
+                    rc[i].get(f);
+                    to = reinterpret_cast<float4 *>(&sm.c[v / (N / 8)][v % (N / 8) * 8]);
+                    to[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                }
             }
         }
         __syncthreads();
-        load(first + kTok);
+        load(first + TT);
+        // the exponentials and inputs of the tokens are independent of the recurrence, which is one
+        // multiply-add a token: unrolled, they run ahead of it
 #pragma unroll 4
-        for (int t = 0; t < kTok; ++t) {
-            const float2 du = s_du[t][ch];
-            const float4 b = *reinterpret_cast<const float4 *>(&s_B[t][4 * q]);
-            h[0] = fmaf(ex2(du.x * A[0]), h[0], du.y * b.x);
-            h[1] = fmaf(ex2(du.x * A[1]), h[1], du.y * b.y);
-            h[2] = fmaf(ex2(du.x * A[2]), h[2], du.y * b.z);
-            h[3] = fmaf(ex2(du.x * A[3]), h[3], du.y * b.w);
-            if (kEnds) total += du.x;
-            else {
-                const float4 cc = *reinterpret_cast<const float4 *>(&s_C[t][4 * q]);
-                float y = cc.x * h[0];
-                y = fmaf(cc.y, h[1], y);
-                y = fmaf(cc.z, h[2], y);
-                y = fmaf(cc.w, h[3], y);
+        for (int t = 0; t < TT; ++t) {
+            const float4 d01 = *reinterpret_cast<const float4 *>(&sm.du[t][ch]);
+            const float4 d23 = *reinterpret_cast<const float4 *>(&sm.du[t][ch + 2]);
+            const float4 b = *reinterpret_cast<const float4 *>(&sm.b[t][4 * q]);
+            const float d[4] = {d01.x, d01.z, d23.x, d23.z}, u[4] = {d01.y, d01.w, d23.y, d23.w};
 #pragma unroll
-                for (int d = LPC / 2; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
-                if (q == 0) s_y[t][ch] = y;
+            for (int i = 0; i < 4; ++i) step(i, d[i], pair(u[i] * b.x, u[i] * b.y), pair(u[i] * b.z, u[i] * b.w));
+            if (kEnds) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) total[i] += d[i];
+            } else {
+                const ulonglong2 cc = *reinterpret_cast<const ulonglong2 *>(&sm.c[kEnds ? 0 : t][4 * q]);
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 s = split(fma2(cc.y, h[i][1], mul2(cc.x, h[i][0])));
+                    y[i] = s.x + s.y;
+                }
+                // down to four lanes that hold parts of the same y: lanes give away half of their
+                // channels, then half of what is left, then add whole values
+                float *part = &sm.y[kEnds ? 0 : t][q & 3][ch];
+                if (LPC == 4) {
+                    *reinterpret_cast<float4 *>(part) = make_float4(y[0], y[1], y[2], y[3]);
+                } else {
+                    const bool hi4 = q & 4;
+                    float r0 = hi4 ? y[2] : y[0], r1 = hi4 ? y[3] : y[1];
+                    r0 += __shfl_xor_sync(0xffffffffu, hi4 ? y[0] : y[2], 4);
+                    r1 += __shfl_xor_sync(0xffffffffu, hi4 ? y[1] : y[3], 4);
+                    part += hi4 ? 2 : 0;
+                    if (LPC == 8) {
+                        *reinterpret_cast<float2 *>(part) = make_float2(r0, r1);
+                    } else {
+                        const bool hi8 = q & 8;
+                        float r = hi8 ? r1 : r0;
+                        r += __shfl_xor_sync(0xffffffffu, hi8 ? r0 : r1, 8);
+                        if (LPC == 32) r += __shfl_xor_sync(0xffffffffu, r, 16);
+                        if (q < 16) part[hi8 ? 1 : 0] = r;
+                    }
+                }
             }
         }
         __syncthreads();
         if (!kEnds && xlive && first + xt < pc.len) {
-            float y[8];
+            float y[8], x[8], z[8];
+            px.get(x);
+            pz.get(z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = skip[e] * x[e];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    const float4 part = *reinterpret_cast<const float4 *>(&sm.y[kEnds ? 0 : xt][i][xc + e]);
+                    y[e] += part.x; y[e + 1] += part.y; y[e + 2] += part.z; y[e + 3] += part.w;
+                }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                y[e] = s_y[xt][xc + e] + dx[e];
-                if (p.z != nullptr) y[e] *= silu_f(gate[e]);
+                if (p.z != nullptr) y[e] *= silu_f(z[e]);
             }
             const int64_t off = row(p.o_sb, p.o_st, pc.t0 + first + xt) + c0 + xc;
             if (range_in_bounds(off, 8, p.eo, p.status, nullptr)) {
@@ -274,10 +376,11 @@ __global__ void __launch_bounds__(4 * N) scan_kernel(const ScanParams p) {
     }
     if (!live) return;
     if (kEnds) {
-        *reinterpret_cast<float4 *>(end_of(pc.k)) = make_float4(h[0], h[1], h[2], h[3]);
-        if (q == 0) p.sums[(int64_t)(pc.slot + pc.k) * p.C + c] = total;
+        store_h(end_of(pc.k));
+        if (q == 0)
+            *reinterpret_cast<float4 *>(p.sums + (int64_t)(pc.slot + pc.k) * p.C + c) = make_float4(total[0], total[1], total[2], total[3]);
     } else if (pc.k == pc.chunks - 1) {
-        *reinterpret_cast<float4 *>(hs) = make_float4(h[0], h[1], h[2], h[3]);
+        store_h(hs);
     }
 }
 
@@ -332,22 +435,22 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanParam
     }
 }
 
-// Tokens of a chunk: a sequence's whole length where the channels and sequences alone give every
-// SM sub-partition a warp in flight for half the time that two passes would take; else as many
-// chunks as give each two warps.
+// Tokens of a chunk.  One pass keeps every warp busy for the whole sequence, two passes with chunks cost
+// 1.7 times the instructions; so a sequence stays whole where the channels and sequences give at least
+// six warps to an SM, and otherwise the chunks are as many as make that twelve, which is what fits at
+// once (sixteen and twenty-four measured 10 and 3 % slower at 4000 tokens of 4096 channels).
 int chunk_of(const cgdr_scan_args &a) {
     const int64_t sms = device_sms() > 0 ? device_sms() : 152;       // sizes workspaces without a device, too
-    const int64_t blocks = (int64_t)a.G * ((a.C / a.G + kCh - 1) / kCh), warps = blocks * (a.N / 8);
-    const int64_t n = a.cu ? a.n_tokens : (int64_t)a.B * a.T, seqs = a.B;
-    const int64_t longest = a.cu ? a.n_tokens : a.T;
+    const int64_t warps = ((int64_t)a.C * a.N + 511) / 512;          // 16 states to a thread
+    const int64_t n = a.cu ? a.n_tokens : (int64_t)a.B * a.T, longest = a.cu ? a.n_tokens : a.T;
     int64_t chunk = longest;
-    if (warps * seqs < 2 * sms || a.cu) {
-        chunk = n * warps / (8 * sms);
+    if (warps * a.B < 6 * sms || a.cu) {
+        chunk = n * warps / (12 * sms);
         // packed lengths are not known here: sequences up to twice the mean stay whole if there are enough
-        if (warps * seqs >= 2 * sms && chunk < 2 * (n / seqs)) chunk = 2 * (n / seqs);
+        if (warps * a.B >= 6 * sms && chunk < 2 * (n / a.B)) chunk = 2 * (n / a.B);
     }
-    if (chunk < 2 * kTok) chunk = 2 * kTok;
-    chunk = (chunk + kTok - 1) / kTok * kTok;
+    if (chunk < 64) chunk = 64;
+    chunk = (chunk + 15) / 16 * 16;
     return (int)(chunk < longest ? chunk : longest);
 }
 
@@ -367,14 +470,15 @@ cgdr_status launch_scan(const cgdr_scan_args &a, ScanParams &p, cudaStream_t s) 
         scan_step_kernel<T, N><<<(unsigned)((units + per - 1) / per), kStepThreads, 0, s>>>(p);
         return launched();
     }
-    const int blocks = a.G * ((p.Cg + kCh - 1) / kCh);
+    using Sh = ScanShape<N>;
+    const int blocks = a.G * ((p.Cg + Sh::CH - 1) / Sh::CH);
     const int64_t pieces = a.cu ? (int64_t)a.n_tokens / p.chunk + a.B : (int64_t)a.B * ((a.T + p.chunk - 1) / p.chunk);
     if (pieces > 65535) return CGDR_ERR_UNSUPPORTED;
     if (p.slots > 0) {
-        scan_kernel<T, N, true><<<dim3(blocks, p.slots), 4 * N, 0, s>>>(p);
+        scan_kernel<T, N, true><<<dim3(blocks, p.slots), Sh::NT, 0, s>>>(p);
         if (cudaPeekAtLastError() != cudaSuccess) return launched();
     }
-    scan_kernel<T, N, false><<<dim3(blocks, (unsigned)pieces), 4 * N, 0, s>>>(p);
+    scan_kernel<T, N, false><<<dim3(blocks, (unsigned)pieces), Sh::NT, 0, s>>>(p);
     return launched();
 }
 

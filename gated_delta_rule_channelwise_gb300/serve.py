@@ -22,7 +22,9 @@ import torch
 
 from . import BF16, F32, _check, _need_cuda, lib
 
+_F32, _I32 = torch.float32, torch.int32
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_NONE = (0, 0, 0)
 
 
 class Block:
@@ -80,8 +82,32 @@ def _on(stream, fn, *args, **kw):
         return fn(*args, **kw)
 
 
-def _handle():
-    return torch.cuda.current_stream().cuda_stream
+# The handle of a device's current stream, without the Stream object that torch.cuda.current_stream builds
+# (2.9 us on a Grace host, as long as all the checks of a call).
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _refuse(dtypes, shapes, dense):
+    """Raises for what is wrong: (name, tensor, dtype), (name, tensor, shape) and (name, tensor) triples.
+
+    The calls first test everything in one expression and come here only when it fails: naming the fault
+    takes longer than the kernels of a small call."""
+    for name, t, dtype in dtypes:
+        if t is not None and t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    for name, t, shape in shapes:
+        if t is not None and t.shape != tuple(shape):
+            raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+    for name, t in dense:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    raise ValueError("the arguments do not agree")
+
+
+def _fits(t, dtype, shape):
+    """Whether a dense operand, which may be absent, has this type and shape."""
+    return t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous())
 
 
 def _code(t, name):
@@ -91,47 +117,33 @@ def _code(t, name):
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype)) from None
 
 
-def _typed(dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-
-
-def _shaped(t, shape, name):
-    if t is not None and t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
-
-
-def _dense(t, shape, name):
-    _shaped(t, shape, name)
-    if t is not None and not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-
-
 def _address(t):
     return 0 if t is None else t.data_ptr()
 
 
 def _status_word(status):
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda):
+    if status is None:
+        return 0
+    if status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda:
         raise TypeError("status must be an int32 CUDA tensor")
-    return _address(status)
+    return status.data_ptr()
 
 
-def _rows(t, name, packed):
-    """(pointer, batch stride, token stride) of [B, T, C], or of packed [n, C]."""
+def _rows(t, name, step):
+    """(pointer, batch stride, token stride) of [B, T, C] rows; with ``step`` of [B, C] or packed [n, C]: the
+    stride of the first dimension then stands in for both."""
     st = t.stride()
     if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError("%s: innermost dimension must be contiguous" % name)
-    return (t.data_ptr(), 0, st[0]) if packed else (t.data_ptr(), st[0], st[1])
+    return t.data_ptr(), st[0], st[0] if step else st[1]
 
 
-def _grouped(t, name, packed):
-    """The same for [B, T, G, N] or packed [n, G, N], whose groups have to be dense."""
-    st = t.stride()
-    if (st[-1] != 1 and t.shape[-1] > 1) or (t.shape[-2] > 1 and st[-2] != t.shape[-1]):
+def _grouped(t, name, step):
+    """The same for [B, T, G, N], or [B, G, N] and packed [n, G, N], whose groups have to be dense."""
+    st, shape = t.stride(), t.shape
+    if (st[-1] != 1 and shape[-1] > 1) or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError("%s: the last two dimensions must be contiguous" % name)
-    return (t.data_ptr(), 0, st[0]) if packed else (t.data_ptr(), st[0], st[1])
+    return t.data_ptr(), st[0], st[0] if step else st[1]
 
 
 def _heads(t, name):
@@ -142,37 +154,35 @@ def _heads(t, name):
     return t.data_ptr(), st[0], st[1]
 
 
-def _sequences(x, state, cu, name):
-    """(B, T, packed tokens) of dense [B, T, ...] or packed [n, ...] rows with offsets."""
-    if cu is None:
-        return x.shape[0], x.shape[1], 0
+def _sequences(x, state, cu):
+    """Sequences of packed rows with offsets."""
     B = cu.numel() - 1
-    if cu.dtype != torch.int32 or not cu.is_contiguous() or cu.dim() != 1 or B < 0:
+    if cu.dtype != torch.int32 or cu.dim() != 1 or B < 0 or not cu.is_contiguous():
         raise TypeError("cu_seqlens must be a dense int32 tensor of B + 1 offsets")
     if state.shape[0] != B:
         raise ValueError("state has %d sequences, cu_seqlens %d" % (state.shape[0], B))
-    return B, 0, x.shape[0]
+    return B
 
 
 # --------------------------------------------------------------------------- convolution
 
 
-def _conv(x, weight, state, o, bias, silu, cu, status, packed, where):
+def _conv(x, weight, state, o, bias, silu, B, T, cu, status):
+    """x is [B, T, C], or [B, C] / packed [n, C] (T is 1 / 0)."""
     _need_cuda(x, weight, state, o, bias, cu)
     if o is None:
-        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    B, T, n = _sequences(x, state, cu, "x")
-    C = x.shape[-1]
-    W = weight.shape[-1]
-    _typed(torch.float32, weight=weight, bias=bias)
-    _typed(x.dtype, state=state, o=o)
-    _shaped(o, x.shape, "o")
-    _dense(weight, (C, W), "weight")
-    _dense(bias, (C,), "bias")
-    _dense(state, (B, W - 1, C), "state")
-    block = CONV.pack(B, T, C, W, _code(x, "x"), 1 if silu else 0, n, 0, *_rows(x, "x", packed), *_rows(o, "o", packed),
-                      weight.data_ptr(), _address(bias), state.data_ptr(), _address(cu), _status_word(status))
-    _check(lib().cgdr_conv(block, _handle()), where)
+        o = torch.empty_like(x)
+    dtype, shape = x.dtype, x.shape
+    C, W, step = shape[-1], weight.shape[-1], len(shape) == 2
+    if not (o.dtype == dtype and o.shape == shape and _fits(weight, _F32, (C, W)) and _fits(bias, _F32, (C,))
+            and _fits(state, dtype, (B, W - 1, C))):
+        _refuse([("weight", weight, _F32), ("bias", bias, _F32), ("state", state, dtype), ("o", o, dtype)],
+                [("o", o, shape), ("weight", weight, (C, W)), ("bias", bias, (C,)), ("state", state, (B, W - 1, C))],
+                [("weight", weight), ("bias", bias), ("state", state)])
+    block = CONV.pack(B, T, C, W, _code(x, "x"), 1 if silu else 0, 0 if cu is None else shape[0], 0, *_rows(x, "x", step),
+                      *_rows(o, "o", step), weight.data_ptr(), _address(bias), state.data_ptr(), _address(cu),
+                      _status_word(status))
+    _check(lib().cgdr_conv(block, _current(x.get_device())), "cgdr_conv")
     return o
 
 
@@ -186,7 +196,8 @@ def conv_prefill(x, weight, state, o=None, *, bias=None, silu=True, cu_seqlens=N
         return _on(stream, conv_prefill, x, weight, state, o, bias=bias, silu=silu, cu_seqlens=cu_seqlens, status=status)
     if x.dim() != (3 if cu_seqlens is None else 2):
         raise ValueError("x must be [B, T, C], or packed [n, C] with cu_seqlens")
-    return _conv(x, weight, state, o, bias, silu, cu_seqlens, status, cu_seqlens is not None, "cgdr_conv")
+    B, T = x.shape[:2] if cu_seqlens is None else (_sequences(x, state, cu_seqlens), 0)
+    return _conv(x, weight, state, o, bias, silu, B, T, cu_seqlens, status)
 
 
 def conv_decode(x, weight, state, o=None, *, bias=None, silu=True, status=None, stream=None):
@@ -195,41 +206,38 @@ def conv_decode(x, weight, state, o=None, *, bias=None, silu=True, status=None, 
         return _on(stream, conv_decode, x, weight, state, o, bias=bias, silu=silu, status=status)
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
-    if o is None:
-        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _conv(x.unsqueeze(1), weight, state, o.unsqueeze(1), bias, silu, None, status, False, "cgdr_conv")
-    return o
+    return _conv(x, weight, state, o, bias, silu, x.shape[0], 1, None, status)
 
 
 # --------------------------------------------------------------------------- scan
 
 
-def _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, cu, workspace, status, where):
+def _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, B, T, cu, workspace, status):
+    """x is [B, T, C], or [B, C] / packed [n, C] (T is 1 / 0)."""
     _need_cuda(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, cu, workspace)
-    packed = cu is not None
     if o is None:
-        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    B, T, n = _sequences(x, state, cu, "x")
-    C, (G, N) = x.shape[-1], Bm.shape[-2:]
-    _typed(torch.float32, A_log=A_log, state=state, D=D, dt_bias=dt_bias)
-    _typed(x.dtype, dt=dt, z=z, Bm=Bm, Cm=Cm)
-    for name, t in (("dt", dt), ("z", z), ("o", o)):
-        _shaped(t, x.shape, name)
-    for name, t in (("Bm", Bm), ("Cm", Cm)):
-        _shaped(t, (*x.shape[:-1], G, N), name)
-    _dense(A_log, (C, N), "A_log")
-    _dense(state, (B, C, N), "state")
-    _dense(D, (C,), "D")
-    _dense(dt_bias, (C,), "dt_bias")
-    block = SCAN.pack(B, T, C, N, G, _code(x, "x"), _code(o, "o"), 1 if softplus else 0, n, 0,
-                      *_rows(x, "x", packed), *_rows(dt, "dt", packed), *(_rows(z, "z", packed) if z is not None else (0, 0, 0)),
-                      *_grouped(Bm, "Bm", packed), *_grouped(Cm, "Cm", packed), *_rows(o, "o", packed),
-                      A_log.data_ptr(), _address(D), _address(dt_bias), state.data_ptr(), _address(cu), _status_word(status))
+        o = torch.empty_like(x)
+    dtype, shape = x.dtype, x.shape
+    C, (G, N), step = shape[-1], Bm.shape[-2:], len(shape) == 2
+    grouped = (*shape[:-1], G, N)
+    if not (dt.dtype == dtype and dt.shape == shape and o.shape == shape and Bm.dtype == dtype and Bm.shape == grouped
+            and Cm.dtype == dtype and Cm.shape == grouped and (z is None or (z.dtype == dtype and z.shape == shape))
+            and _fits(A_log, _F32, (C, N)) and _fits(state, _F32, (B, C, N)) and _fits(D, _F32, (C,))
+            and _fits(dt_bias, _F32, (C,))):
+        _refuse([("A_log", A_log, _F32), ("state", state, _F32), ("D", D, _F32), ("dt_bias", dt_bias, _F32),
+                 ("dt", dt, dtype), ("z", z, dtype), ("Bm", Bm, dtype), ("Cm", Cm, dtype)],
+                [("dt", dt, shape), ("z", z, shape), ("o", o, shape), ("Bm", Bm, grouped), ("Cm", Cm, grouped),
+                 ("A_log", A_log, (C, N)), ("state", state, (B, C, N)), ("D", D, (C,)), ("dt_bias", dt_bias, (C,))],
+                [("A_log", A_log), ("state", state), ("D", D), ("dt_bias", dt_bias)])
+    block = SCAN.pack(B, T, C, N, G, _code(x, "x"), _code(o, "o"), 1 if softplus else 0, 0 if cu is None else shape[0], 0,
+                      *_rows(x, "x", step), *_rows(dt, "dt", step), *(_rows(z, "z", step) if z is not None else _NONE),
+                      *_grouped(Bm, "Bm", step), *_grouped(Cm, "Cm", step), *_rows(o, "o", step), A_log.data_ptr(),
+                      _address(D), _address(dt_bias), state.data_ptr(), _address(cu), _status_word(status))
     L = lib()
-    need = 0 if T == 1 and not packed else L.cgdr_scan_workspace_size(block)
+    need = 0 if T == 1 else L.cgdr_scan_workspace_size(block)
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _check(L.cgdr_scan(block, workspace.data_ptr() if need else None, need, _handle()), where)
+    _check(L.cgdr_scan(block, workspace.data_ptr() if need else None, need, _current(x.get_device())), "cgdr_scan")
     return o
 
 
@@ -249,7 +257,8 @@ def scan_prefill(x, dt, A_log, Bm, Cm, state, o=None, *, D=None, z=None, dt_bias
     lead = 1 if cu_seqlens is not None else 2
     if x.dim() != lead + 1 or Bm.dim() != lead + 2:
         raise ValueError("x must be [B, T, C] and Bm [B, T, G, N], or packed [n, C] and [n, G, N] with cu_seqlens")
-    return _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, cu_seqlens, workspace, status, "cgdr_scan")
+    B, T = x.shape[:2] if cu_seqlens is None else (_sequences(x, state, cu_seqlens), 0)
+    return _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, B, T, cu_seqlens, workspace, status)
 
 
 def scan_decode(x, dt, A_log, Bm, Cm, state, o=None, *, D=None, z=None, dt_bias=None, softplus=True, status=None,
@@ -260,11 +269,7 @@ def scan_decode(x, dt, A_log, Bm, Cm, state, o=None, *, D=None, z=None, dt_bias=
                    status=status)
     if x.dim() != 2 or Bm.dim() != 3:
         raise ValueError("x must be [B, C] and Bm [B, G, N]")
-    if o is None:
-        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    u = lambda t: None if t is None else t.unsqueeze(1)
-    _scan(u(x), u(dt), A_log, u(Bm), u(Cm), state, u(o), D, u(z), dt_bias, softplus, None, None, status, "cgdr_scan")
-    return o
+    return _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, x.shape[0], 1, None, None, status)
 
 
 def scan_workspace_size(B, T, C, N, G=1, *, n_tokens=None, dtype=torch.bfloat16) -> int:
@@ -316,48 +321,47 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
         return _on(stream, cache_plan, block_table, seq_lens, new_lens, free_pages, free_count, n_tokens, page, out,
                    num_pages=num_pages, status=status)
     _need_cuda(block_table, seq_lens, new_lens, free_pages, free_count)
-    _typed(torch.int32, block_table=block_table, seq_lens=seq_lens, new_lens=new_lens, free_pages=free_pages,
-           free_count=free_count)
     B, width = block_table.shape
+    F = free_pages.numel()
     if out is None:
         out = CachePlan.empty(B, n_tokens, block_table.device)
     else:
         _need_cuda(out.slots, out.kv_lens, out.cu_seqlens, out.free_count, out.requests, out.positions)
-        _typed(torch.int32, kv_lens=out.kv_lens, cu_seqlens=out.cu_seqlens, free_count=out.free_count,
-               requests=out.requests, positions=out.positions)
-        _typed(torch.int64, slots=out.slots)
-        for name, t, size in (("kv_lens", out.kv_lens, B), ("cu_seqlens", out.cu_seqlens, B + 1),
-                              ("free_count", out.free_count, 1), ("slots", out.slots, n_tokens),
-                              ("requests", out.requests, n_tokens), ("positions", out.positions, n_tokens)):
-            _dense(t, (size,), "out." + name)
-    _dense(seq_lens, (B,), "seq_lens")
-    _dense(new_lens, (B,), "new_lens")
-    _dense(free_pages, (free_pages.numel(),), "free_pages")
-    _dense(free_count, (1,), "free_count")
+        written = [("kv_lens", B), ("cu_seqlens", B + 1), ("free_count", 1), ("requests", n_tokens), ("positions", n_tokens),
+                   ("slots", n_tokens)]
+        if not all(_fits(getattr(out, name), torch.int64 if name == "slots" else _I32, (size,)) for name, size in written):
+            named = [("out." + name, getattr(out, name), size) for name, size in written]
+            _refuse([(name, t, _I32) for name, t, _ in named[:-1]] + [("out.slots", out.slots, torch.int64)],
+                    [(name, t, (size,)) for name, t, size in named], [(name, t) for name, t, _ in named])
+    if not (block_table.dtype == _I32 and _fits(seq_lens, _I32, (B,)) and _fits(new_lens, _I32, (B,))
+            and _fits(free_pages, _I32, (F,)) and _fits(free_count, _I32, (1,))):
+        named = [("seq_lens", seq_lens, B), ("new_lens", new_lens, B), ("free_pages", free_pages, F), ("free_count", free_count, 1)]
+        _refuse([("block_table", block_table, _I32)] + [(name, t, _I32) for name, t, _ in named],
+                [(name, t, (size,)) for name, t, size in named], [(name, t) for name, t, _ in named])
     sb, sw = block_table.stride()
     if sw != 1 and width > 1:
         raise ValueError("block_table: innermost dimension must be contiguous")
-    block = PLAN.pack(B, width, page, n_tokens, free_pages.shape[0], 0x7FFFFFFF if num_pages is None else num_pages,
+    block = PLAN.pack(B, width, page, n_tokens, F, 0x7FFFFFFF if num_pages is None else num_pages,
                       block_table.data_ptr(), sb, seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
                       free_count.data_ptr(), out.free_count.data_ptr(), out.kv_lens.data_ptr(),
                       out.cu_seqlens.data_ptr(), out.requests.data_ptr(), out.positions.data_ptr(),
                       out.slots.data_ptr(), _status_word(status))
-    _check(lib().cgdr_cache_plan(block, _handle()), "cgdr_cache_plan")
+    _check(lib().cgdr_cache_plan(block, _current(block_table.get_device())), "cgdr_cache_plan")
     return out
 
 
 def _check_cache(k_cache, v_cache, k_scale, v_scale):
     """(pages, Hkv, page, D) of a cache: int8 [pages, Hkv, page, D] with fp32 scales [pages, Hkv]."""
     _need_cuda(k_cache, v_cache, k_scale, v_scale)
-    _typed(torch.int8, k_cache=k_cache, v_cache=v_cache)
-    _typed(torch.float32, k_scale=k_scale, v_scale=v_scale)
     shape = k_cache.shape
     if len(shape) != 4:
         raise ValueError("k_cache must be [pages, Hkv, page, D]")
-    _dense(k_cache, shape, "k_cache")
-    _dense(v_cache, shape, "v_cache")
-    _dense(k_scale, shape[:2], "k_scale")
-    _dense(v_scale, shape[:2], "v_scale")
+    if not (_fits(k_cache, torch.int8, shape) and _fits(v_cache, torch.int8, shape) and _fits(k_scale, _F32, shape[:2])
+            and _fits(v_scale, _F32, shape[:2])):
+        _refuse([("k_cache", k_cache, torch.int8), ("v_cache", v_cache, torch.int8), ("k_scale", k_scale, _F32),
+                 ("v_scale", v_scale, _F32)],
+                [("v_cache", v_cache, shape), ("k_scale", k_scale, shape[:2]), ("v_scale", v_scale, shape[:2])],
+                [("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale)])
     return shape
 
 
@@ -372,16 +376,15 @@ def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, status=None
         return _on(stream, cache_append, k, v, slots, k_cache, v_cache, k_scale, v_scale, status=status)
     pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
     _need_cuda(k, v, slots)
-    _typed(k.dtype, v=v)
     n = k.shape[0]
-    _shaped(k, (n, Hkv, D), "k")
-    _shaped(v, (n, Hkv, D), "v")
-    _typed(torch.int64, slots=slots)
-    _dense(slots, (n,), "slots")
+    shape = (n, Hkv, D)
+    if not (k.shape == shape and v.shape == shape and v.dtype == k.dtype and _fits(slots, torch.int64, (n,))):
+        _refuse([("v", v, k.dtype), ("slots", slots, torch.int64)], [("k", k, shape), ("v", v, shape), ("slots", slots, (n,))],
+                [("slots", slots)])
     block = APPEND.pack(n, Hkv, D, page, _code(k, "k"), pages, *_heads(k, "k"), *_heads(v, "v"), slots.data_ptr(),
                         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         _status_word(status))
-    _check(lib().cgdr_cache_append(block, _handle()), "cgdr_cache_append")
+    _check(lib().cgdr_cache_append(block, _current(k.get_device())), "cgdr_cache_append")
 
 
 def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o=None, *, max_q, max_kv=None,
@@ -402,17 +405,18 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
                    max_q=max_q, max_kv=max_kv, scale=scale, workspace=workspace, status=status)
     pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        o = torch.empty_like(q)
     _need_cuda(q, o, block_table, kv_lens, cu_seqlens, workspace)
     n, Hq, Dq = q.shape
     if Dq != D:
         raise ValueError("q has head dimension %d, the cache %d" % (Dq, D))
-    _typed(q.dtype, o=o)
-    _shaped(o, q.shape, "o")
-    _typed(torch.int32, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens)
     B, width = block_table.shape
-    _dense(kv_lens, (B,), "kv_lens")
-    _dense(cu_seqlens, (B + 1,), "cu_seqlens")
+    if not (o.dtype == q.dtype and o.shape == q.shape and block_table.dtype == _I32 and _fits(kv_lens, _I32, (B,))
+            and _fits(cu_seqlens, _I32, (B + 1,))):
+        _refuse([("o", o, q.dtype), ("block_table", block_table, _I32), ("kv_lens", kv_lens, _I32),
+                 ("cu_seqlens", cu_seqlens, _I32)],
+                [("o", o, q.shape), ("kv_lens", kv_lens, (B,)), ("cu_seqlens", cu_seqlens, (B + 1,))],
+                [("kv_lens", kv_lens), ("cu_seqlens", cu_seqlens)])
     sb, sw = block_table.stride()
     if sw != 1 and width > 1:
         raise ValueError("block_table: innermost dimension must be contiguous")
@@ -424,7 +428,8 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     need = L.cgdr_cache_attend_workspace_size(block)
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(L.cgdr_cache_attend(block, workspace.data_ptr() if need else None, need, _handle()), "cgdr_cache_attend")
+    _check(L.cgdr_cache_attend(block, workspace.data_ptr() if need else None, need, _current(q.get_device())),
+           "cgdr_cache_attend")
     return o
 
 
