@@ -2,10 +2,12 @@
 //
 // Bound by memory for prompts (k and v read once, a byte an element written) and by the launch for
 // single tokens.  The unit of work is a run: consecutive packed tokens on consecutive slots of one
-// page, for one head, of k or of v.  A block owns the run that begins at its token and with it the page's scale, so
-// nothing is exchanged between blocks; a block whose token begins no run has nothing to do.  The
-// run's largest magnitude has to be known before its first byte: the values are read for it, and
-// again, from L1 or L2, to be rounded.
+// page, for one head, of k or of v.  Whoever has a run has its page's scale, so nothing is exchanged
+// between blocks.  A block finds the runs that begin in its window of tokens: few of them (a prompt)
+// it works on one after the other with all its threads, many (single tokens) a warp each.  The
+// largest magnitude has to be known before the first byte: a thread keeps the first four vectors that it
+// reads (eight cost more in resident blocks than they save) and reads the rest again, from L1 or L2.
+// The quotient is only formed where its rounding is in doubt: x (1 / scale) is within 3e-5 of it.
 #include "serve.cuh"
 
 namespace cgdr {
@@ -14,7 +16,7 @@ namespace {
 constexpr int kAppendThreads = 128;
 
 struct AppendParams {
-    int n, Hkv, D, page, num_pages;
+    int n, Hkv, D, page, num_pages, window;
     const void *x[2];                                 // k, v
     int64_t st[2], sh[2], ex[2];                      // strides and footprints
     const int64_t *slots;
@@ -30,63 +32,74 @@ __device__ __forceinline__ int quantised(float x, float scale) {
     return min(max(__float2int_rn(__fdiv_rn(x, scale)), -127), 127);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
-    constexpr int V = Vec<T>::n;
-    const int i = blockIdx.x, h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
-    const int64_t slot = p.slots[i];
-    const int64_t slots = (int64_t)p.num_pages * p.page;
-    if (slot < 0) return;
-    if (slot >= slots) {
-        if (tid == 0 && p.status != nullptr) atomicExch(p.status, (int)CGDR_ERR_BOUNDS);
-        return;
+// Four values as bytes of round(x / by), |x / by| <= 127.  Adding 1.5 2^23 rounds the product with the
+// reciprocal to the nearest integer, ties to even, in the low bits; product and quotient are rounded
+// from values 127 2^-23 apart at most, so where the product is 1e-4 off a tie the quotient rounds the same.
+__device__ __forceinline__ uint32_t quantised4(const float *f, float by, float inverse, bool sure) {
+    constexpr float kMagic = 12582912.f;
+    uint32_t b[4];
+    bool exact = !sure;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float t = f[c] * inverse, r = t + kMagic;
+        exact |= fabsf(fabsf(t - (r - kMagic)) - 0.5f) < 1e-4f;
+        b[c] = __float_as_uint(r);
     }
+    if (exact) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[c] = (uint32_t)quantised(f[c], by);
+    }
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
+// One run by a warp, or (kBlock) by the block: tokens i .. i + len - 1 into the page of `slot` from its
+// offset on.
+template <typename T, bool kBlock>
+__device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t slot, int len, int h, int which, float *s_max) {
+    constexpr int V = Vec<T>::n, NT = kBlock ? kAppendThreads : 32, kKeep = 4;
+    const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
     const int off = (int)(slot % p.page);
-    if (off > 0 && i > 0 && p.slots[i - 1] == slot - 1) return;       // inside a run
-
-    __shared__ int s_len;
-    __shared__ float s_max[kAppendThreads / 32];
-    if (tid == 0) s_len = min(p.page - off, p.n - i);
-    __syncthreads();
-    // the run's length: up to the first token that is not on the next slot (a page has 128 at most)
-    if (tid < min(p.page - off, p.n - i) && p.slots[i + tid] != slot + tid) atomicMin(&s_len, tid);
-    __syncthreads();
-    const int len = s_len;
-
     const int64_t unit = (slot / p.page) * p.Hkv + h;                 // the page's block of this head
     int8_t *dst = p.cache[which] + unit * p.page * p.D;
     const T *x = static_cast<const T *>(p.x[which]);
     const int per = p.D / V, vecs = len * per;
-    auto vec = [&](int e, float (&f)[V]) {
+    auto vec = [&](int e) {
         const int64_t at = (int64_t)(i + e / per) * p.st[which] + h * p.sh[which] + (e % per) * V;
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (range_in_bounds(at, V, p.ex[which], p.status, nullptr)) r = __ldg(reinterpret_cast<const uint4 *>(x + at));
-        Vec<T>::unpack(r, f);
+        return range_in_bounds(at, V, p.ex[which], p.status, nullptr) ? __ldg(reinterpret_cast<const uint4 *>(x + at))
+                                                                      : make_uint4(0, 0, 0, 0);
     };
+    const float had = off > 0 ? p.scale[which][unit] : 0.f;
 
+    uint4 kept[kKeep];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) kept[k] = tid + k * NT < vecs ? vec(tid + k * NT) : make_uint4(0, 0, 0, 0);
     float top = 0.f;
-    for (int e = tid; e < vecs; e += kAppendThreads) {
+    auto over = [&](const uint4 &r) {
         float f[V];
-        vec(e, f);
+        Vec<T>::unpack(r, f);
 #pragma unroll
         for (int j = 0; j < V; ++j) top = max_nan(top, fabsf(f[j]));
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) over(kept[k]);
+    for (int e = tid + kKeep * NT; e < vecs; e += NT) over(vec(e));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if ((tid & 31) == 0) s_max[tid >> 5] = top;
-    __syncthreads();
+    if (kBlock) {
+        if ((tid & 31) == 0) s_max[tid >> 5] = top;
+        __syncthreads();                              // also: every thread has read the scale that is replaced
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) top = max_nan(top, s_max[w]);
-
-    const float stored = p.scale[which][unit];
-    const float had = off > 0 ? stored : 0.f;
+        for (int w = 0; w < kAppendThreads / 32; ++w) top = max_nan(top, s_max[w]);
+    }
     const float grown = max_nan(had, top * (1.f / 127.f));
     const float by = grown > 0.f ? grown : 1.f;       // nothing but zeros: any divisor gives them
-    __syncthreads();                                  // every thread has read the scale that is replaced
+    const float inverse = __frcp_rn(by);
+    const bool sure = grown > 0x1p-100f && grown < INFINITY;          // and not a NaN: 1 / by is as exact as numbers get
+    if (!kBlock) __syncwarp();
     if (tid == 0) p.scale[which][unit] = grown;
 
     if (grown > had && off > 0) {                     // what the page holds, rounded to the larger scale
-        for (int e = tid; e < off * p.D / 16; e += kAppendThreads) {
+        for (int e = tid; e < off * p.D / 16; e += NT) {
             uint4 r = reinterpret_cast<uint4 *>(dst)[e];
             uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -102,25 +115,67 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
             reinterpret_cast<uint4 *>(dst)[e] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    for (int e = tid; e < vecs; e += kAppendThreads) {
+    auto put = [&](int e, const uint4 &r) {
         float f[V];
-        vec(e, f);
+        Vec<T>::unpack(r, f);
         uint32_t w[V / 4];
 #pragma unroll
-        for (int j = 0; j < V / 4; ++j) {
-            w[j] = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) w[j] |= (uint32_t)(quantised(f[4 * j + c], by) & 0xFF) << (8 * c);
-        }
+        for (int j = 0; j < V / 4; ++j) w[j] = quantised4(f + 4 * j, by, inverse, sure);
         uint32_t *to = reinterpret_cast<uint32_t *>(dst + (int64_t)off * p.D + e * V);
         if (V == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[V / 4 - 1]);
         else *to = w[0];
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+        if (tid + k * NT < vecs) put(tid + k * NT, kept[k]);
+    for (int e = tid + kKeep * NT; e < vecs; e += NT) put(e, vec(e));
+    if (kBlock) __syncthreads();                      // s_max is free again
 }
 
 template <typename T>
-cgdr_status launch_append(const AppendParams &p, cudaStream_t s) {
-    cache_append_kernel<T><<<dim3(p.n, p.Hkv, 2), kAppendThreads, 0, s>>>(p);
+__global__ void __launch_bounds__(kAppendThreads, 6) cache_append_kernel(const AppendParams p) {
+    constexpr int NW = kAppendThreads / 32;
+    __shared__ int s_start[kAppendThreads], s_count;
+    __shared__ float s_max[NW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y, which = blockIdx.z;
+    const int i0 = blockIdx.x * p.window;
+    const int64_t slots = (int64_t)p.num_pages * p.page;
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    if (tid < p.window && i0 + tid < p.n) {
+        const int i = i0 + tid;
+        const int64_t slot = p.slots[i];
+        if (slot >= slots && h == 0 && which == 0 && p.status != nullptr) atomicExch(p.status, (int)CGDR_ERR_BOUNDS);
+        // a run begins where a page does, or where the token before is on another slot
+        if (slot >= 0 && slot < slots && (slot % p.page == 0 || i == 0 || p.slots[i - 1] != slot - 1))
+            s_start[atomicAdd(&s_count, 1)] = i;      // in any order: runs share nothing
+    }
+    __syncthreads();
+    const int runs = s_count;
+    const bool alone = runs < NW;                     // the block on one run at a time
+    for (int r = alone ? 0 : warp; r < runs; r += alone ? 1 : NW) {
+        const int i = s_start[r];
+        const int64_t slot = p.slots[i];
+        const int most = min(p.page - (int)(slot % p.page), p.n - i);
+        int len = most;                               // up to the first token that is not on the next slot
+        for (int t = lane; t < most; t += 32)
+            if (p.slots[i + t] != slot + t) { len = t; break; }
+        len = __reduce_min_sync(0xffffffffu, len);
+        if (alone) append_run<T, true>(p, i, slot, len, h, which, s_max);
+        else append_run<T, false>(p, i, slot, len, h, which, s_max);
+    }
+}
+
+// Tokens of a block's window: one where there are few tokens, so that each has a block; up to 64 (a
+// prompt's window then holds a run or two), as long as there are eight blocks to an SM.
+template <typename T>
+cgdr_status launch_append(AppendParams &p, cudaStream_t s) {
+    const int sms = device_sms();
+    if (sms <= 0) return CGDR_ERR_CUDA;
+    const int64_t units = 2 * (int64_t)p.Hkv;
+    p.window = kAppendThreads / 32;
+    while (p.window < 64 && p.n * units >= 16 * (int64_t)sms * p.window) p.window *= 2;
+    cache_append_kernel<T><<<dim3((p.n + p.window - 1) / p.window, p.Hkv, 2), kAppendThreads, 0, s>>>(p);
     return launched();
 }
 

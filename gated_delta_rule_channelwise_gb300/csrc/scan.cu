@@ -86,52 +86,32 @@ __device__ __forceinline__ Piece find_piece(const ScanParams &p, int item, bool 
 }
 
 // softplus(x) = max(x, 0) + log(1 + t), t = e^-|x|.  With s = t / (2 + t) <= 1/3 the logarithm is
-// 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...); eight terms leave 2e-9 of it, and small results keep
-// their relative accuracy, which a logarithm of 1 + t in fp32 would lose.
-__device__ __forceinline__ float softplus_series(float x) {
-    const float t = ex2(-kLog2e * fabsf(x));
-    const float s = t * rcp(2.f + t), q = s * s;
-    float r = 1.f / 15.f;
-    r = fmaf(r, q, 1.f / 13.f);
-    r = fmaf(r, q, 1.f / 11.f);
-    r = fmaf(r, q, 1.f / 9.f);
-    r = fmaf(r, q, 1.f / 7.f);
-    r = fmaf(r, q, 1.f / 5.f);
-    r = fmaf(r, q, 1.f / 3.f);
-    r = fmaf(r, q, 1.f);
-    return fmaxf(x, 0.f) + 2.f * s * r;
+// 2 atanh(s) = 2 s r(s^2), r(q) = 1 + q/3 + q^2/5 + ...; a polynomial of degree 4 through r's values
+// at the Chebyshev points of [0, 1/9] is within 4e-9 of it.  Small results keep their relative
+// accuracy, which a logarithm of 1 + t in fp32 would lose.
+__device__ __forceinline__ f32x2 softplus_pair(f32x2 v) {
+    const float2 x = split(v);
+    const f32x2 t = pair(ex2(-kLog2e * fabsf(x.x)), ex2(-kLog2e * fabsf(x.y)));
+    const float2 w = split(add2(t, both(2.f)));
+    const f32x2 s = mul2(t, pair(rcp(w.x), rcp(w.y))), q = mul2(s, s);
+    f32x2 r = fma2(q, both(0.14078889787197113f), both(0.13982579112052917f));
+    r = fma2(r, q, both(0.20012298226356506f));
+    r = fma2(r, q, both(0.3333316147327423f));
+    r = fma2(r, q, both(1.f));
+    return fma2(add2(s, s), r, pair(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 
-// Pairs of fp32 in a 64-bit register: one instruction for two multiply-adds (the arithmetic rate
-// is that of two, the issue slot is saved).
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 split(f32x2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 // Eight consecutive elements as stored, and as fp32.
 template <typename T> struct Eight;
 template <> struct Eight<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
     __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&f)[8]) const { Vec<__nv_bfloat16>::unpack(a, f); }
+    __device__ __forceinline__ void get(f32x2 (&f)[4]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
 };
 template <> struct Eight<float> {
     uint4 a, b;
@@ -140,9 +120,11 @@ template <> struct Eight<float> {
         b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        Vec<float>::unpack(a, f);
-        Vec<float>::unpack(b, f + 4);
+    __device__ __forceinline__ void get(f32x2 (&f)[4]) const {
+        f[0] = pair(__uint_as_float(a.x), __uint_as_float(a.y));
+        f[1] = pair(__uint_as_float(a.z), __uint_as_float(a.w));
+        f[2] = pair(__uint_as_float(b.x), __uint_as_float(b.y));
+        f[3] = pair(__uint_as_float(b.z), __uint_as_float(b.w));
     }
 };
 template <typename T>
@@ -168,7 +150,7 @@ struct ScanShape {
 template <int N, bool kEnds>
 struct ScanTile {
     using Sh = ScanShape<N>;
-    float2 du[Sh::TT][Sh::CH];                                        // d, d x
+    float d[Sh::TT][Sh::CH], u[Sh::TT][Sh::CH];                       // d, d x
     float b[Sh::TT][N], c[kEnds ? 1 : Sh::TT][N];
     float y[kEnds ? 1 : Sh::TT][4][Sh::CH + 8];                       // four parts of every y, each in banks of its own
 };
@@ -238,76 +220,96 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
     const int xt = tid / (Sh::CH / 8), xc = tid % (Sh::CH / 8) * 8;
     const bool stages = tid < Sh::XV, xlive = stages && cg0 + xc < p.Cg;
     Eight<T> rx, rd, rz, rb[Sh::BPT], rc[Sh::BPT];
-    float bias[8], skip[8];
+    f32x2 bias[4], skip[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        bias[e] = xlive && p.dt_bias != nullptr ? __ldg(p.dt_bias + c0 + xc + e) : 0.f;
-        skip[e] = !kEnds && xlive && p.D != nullptr ? __ldg(p.D + c0 + xc + e) : 0.f;
+    for (int e = 0; e < 4; ++e) {
+        auto two = [&](const float *v) {
+            return xlive && v != nullptr ? __ldg(reinterpret_cast<const float2 *>(v + c0 + xc) + e) : make_float2(0.f, 0.f);
+        };
+        const float2 b = two(p.dt_bias), d = kEnds ? make_float2(0.f, 0.f) : two(p.D);
+        bias[e] = pair(b.x, b.y);
+        skip[e] = pair(d.x, d.y);
     }
-    const bool packed = p.cu != nullptr;
-    auto row = [&](int64_t sb, int64_t st, int t) { return (packed ? 0 : pc.b * sb) + (int64_t)t * st; };
-    auto load = [&](int first) {
-        const int t = pc.t0 + first + xt;
-        const bool ok = xlive && first + xt < pc.len;
-        fetch<T>(rx, p.x, row(p.x_sb, p.x_st, t) + c0 + xc, ok, p.ex, p.status);
-        fetch<T>(rd, p.dt, row(p.dt_sb, p.dt_st, t) + c0 + xc, ok, p.edt, p.status);
-        if (!kEnds) fetch<T>(rz, p.z, row(p.z_sb, p.z_st, t) + c0 + xc, ok && p.z != nullptr, p.ez, p.status);
+    // offsets of the thread's first rows; tiles are TT rows apart
+    const int64_t at = p.cu != nullptr ? 0 : pc.b, row = pc.t0 + xt;
+    int64_t ox = at * p.x_sb + row * p.x_st + c0 + xc, od = at * p.dt_sb + row * p.dt_st + c0 + xc,
+            oz = at * p.z_sb + row * p.z_st + c0 + xc, oo = at * p.o_sb + row * p.o_st + c0 + xc, ob[Sh::BPT], oc[Sh::BPT];
+#pragma unroll
+    for (int i = 0; i < Sh::BPT; ++i) {
+        const int v = tid + i * Sh::NT, bn = g * N + v % (N / 8) * 8;
+        const int64_t brow = pc.t0 + v / (N / 8);
+        ob[i] = at * p.B_sb + brow * p.B_st + bn;
+        oc[i] = at * p.C_sb + brow * p.C_st + bn;
+    }
+    const bool gated = !kEnds && p.z != nullptr;
+    auto load = [&](int left) {                       // of the tile's tokens on, `left` are left
+        const bool ok = xlive && xt < left;
+        fetch<T>(rx, p.x, ox, ok, p.ex, p.status);
+        fetch<T>(rd, p.dt, od, ok, p.edt, p.status);
+        if (!kEnds) fetch<T>(rz, p.z, oz, ok && gated, p.ez, p.status);
+        ox += TT * p.x_st; od += TT * p.dt_st; oz += TT * p.z_st;
 #pragma unroll
         for (int i = 0; i < Sh::BPT; ++i) {
-            const int v = tid + i * Sh::NT, bt = first + v / (N / 8), bn = g * N + v % (N / 8) * 8;
-            const bool okb = v < Sh::BV && bt < pc.len;
-            fetch<T>(rb[i], p.Bm, row(p.B_sb, p.B_st, pc.t0 + bt) + bn, okb, p.eB, p.status);
-            if (!kEnds) fetch<T>(rc[i], p.Cm, row(p.C_sb, p.C_st, pc.t0 + bt) + bn, okb, p.eC, p.status);
+            const int v = tid + i * Sh::NT;
+            const bool okb = v < Sh::BV && v / (N / 8) < left;
+            fetch<T>(rb[i], p.Bm, ob[i], okb, p.eB, p.status);
+            if (!kEnds) fetch<T>(rc[i], p.Cm, oc[i], okb, p.eC, p.status);
+            ob[i] += TT * p.B_st; oc[i] += TT * p.C_st;
         }
     };
-    load(0);
+    load(pc.len);
     float total[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int first = 0; first < pc.len; first += TT) {
+    for (int left = pc.len; left > 0; left -= TT) {
         const Eight<T> px = rx, pz = rz;              // what the tile's outputs need again
         if (stages) {
-            float x[8], d[8];
+            const bool ok = xlive && xt < left;
+            f32x2 x[4], d[4];
             rx.get(x);
             rd.get(d);
-            const bool ok = xlive && first + xt < pc.len;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float v = d[e] + bias[e];
-                if (p.softplus) v = softplus_series(v);
-                if (!ok) v = 0.f;                     // past the end: exp(0) h + 0
-                d[e] = v;
-                x[e] *= v;
+            for (int e = 0; e < 4; ++e) d[e] = add2(d[e], bias[e]);
+            if (p.softplus) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] = softplus_pair(d[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; e += 2)
-                *reinterpret_cast<float4 *>(&sm.du[xt][xc + e]) = make_float4(d[e], x[e], d[e + 1], x[e + 1]);
+            for (int e = 0; e < 4; ++e) {
+                if (!ok) d[e] = both(0.f);            // past the end: exp(0) h + 0
+                x[e] = mul2(x[e], d[e]);
+            }
+            ulonglong2 *to = reinterpret_cast<ulonglong2 *>(&sm.d[xt][xc]);
+            to[0] = make_ulonglong2(d[0], d[1]);
+            to[1] = make_ulonglong2(d[2], d[3]);
+            to = reinterpret_cast<ulonglong2 *>(&sm.u[xt][xc]);
+            to[0] = make_ulonglong2(x[0], x[1]);
+            to[1] = make_ulonglong2(x[2], x[3]);
         }
 #pragma unroll
         for (int i = 0; i < Sh::BPT; ++i) {
             const int v = tid + i * Sh::NT;
             if (v < Sh::BV) {
-                float f[8];
+                f32x2 f[4];
                 rb[i].get(f);
-                float4 *to = reinterpret_cast<float4 *>(&sm.b[v / (N / 8)][v % (N / 8) * 8]);
-                to[0] = make_float4(f[0], f[1], f[2], f[3]);
-                to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                ulonglong2 *to = reinterpret_cast<ulonglong2 *>(&sm.b[v / (N / 8)][v % (N / 8) * 8]);
+                to[0] = make_ulonglong2(f[0], f[1]);
+                to[1] = make_ulonglong2(f[2], f[3]);
                 if (!kEnds) {
                     rc[i].get(f);
-                    to = reinterpret_cast<float4 *>(&sm.c[v / (N / 8)][v % (N / 8) * 8]);
-                    to[0] = make_float4(f[0], f[1], f[2], f[3]);
-                    to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    to = reinterpret_cast<ulonglong2 *>(&sm.c[v / (N / 8)][v % (N / 8) * 8]);
+                    to[0] = make_ulonglong2(f[0], f[1]);
+                    to[1] = make_ulonglong2(f[2], f[3]);
                 }
             }
         }
         __syncthreads();
-        load(first + TT);
+        load(left - TT);
         // the exponentials and inputs of the tokens are independent of the recurrence, which is one
         // multiply-add a token: unrolled, they run ahead of it
 #pragma unroll 4
         for (int t = 0; t < TT; ++t) {
-            const float4 d01 = *reinterpret_cast<const float4 *>(&sm.du[t][ch]);
-            const float4 d23 = *reinterpret_cast<const float4 *>(&sm.du[t][ch + 2]);
+            const float4 dd = *reinterpret_cast<const float4 *>(&sm.d[t][ch]), uu = *reinterpret_cast<const float4 *>(&sm.u[t][ch]);
             const float4 b = *reinterpret_cast<const float4 *>(&sm.b[t][4 * q]);
-            const float d[4] = {d01.x, d01.z, d23.x, d23.z}, u[4] = {d01.y, d01.w, d23.y, d23.w};
+            const float d[4] = {dd.x, dd.y, dd.z, dd.w}, u[4] = {uu.x, uu.y, uu.z, uu.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) step(i, d[i], pair(u[i] * b.x, u[i] * b.y), pair(u[i] * b.z, u[i] * b.w));
             if (kEnds) {
@@ -345,34 +347,40 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
             }
         }
         __syncthreads();
-        if (!kEnds && xlive && first + xt < pc.len) {
-            float y[8], x[8], z[8];
+        if (!kEnds && xlive && xt < left) {
+            f32x2 y[4], x[4];
             px.get(x);
-            pz.get(z);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = skip[e] * x[e];
+            for (int e = 0; e < 4; ++e) y[e] = mul2(skip[e], x[e]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 part = *reinterpret_cast<const float4 *>(&sm.y[kEnds ? 0 : xt][i][xc + e]);
-                    y[e] += part.x; y[e + 1] += part.y; y[e + 2] += part.z; y[e + 3] += part.w;
-                }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (p.z != nullptr) y[e] *= silu_f(z[e]);
+            for (int i = 0; i < 4; ++i) {
+                const ulonglong2 *part = reinterpret_cast<const ulonglong2 *>(&sm.y[kEnds ? 0 : xt][i][xc]);
+                const ulonglong2 lo = part[0], hi = part[1];
+                y[0] = add2(y[0], lo.x); y[1] = add2(y[1], lo.y);
+                y[2] = add2(y[2], hi.x); y[3] = add2(y[3], hi.y);
             }
-            const int64_t off = row(p.o_sb, p.o_st, pc.t0 + first + xt) + c0 + xc;
-            if (range_in_bounds(off, 8, p.eo, p.status, nullptr)) {
+            if (gated) {
+                f32x2 z[4];
+                pz.get(z);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = mul2(y[e], silu_pair(z[e]));
+                }
+            }
+            if (range_in_bounds(oo, 8, p.eo, p.status, nullptr)) {
                 if (p.o_f32) {
-                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + off);
-                    o[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    o[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    ulonglong2 *o = reinterpret_cast<ulonglong2 *>(static_cast<float *>(p.o) + oo);
+                    o[0] = make_ulonglong2(y[0], y[1]);
+                    o[1] = make_ulonglong2(y[2], y[3]);
                 } else {
-                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + off) = Vec<__nv_bfloat16>::pack(y);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(split(y[e]).x, split(y[e]).y);
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + oo) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
         }
+        oo += TT * p.o_st;
     }
     if (!live) return;
     if (kEnds) {
@@ -414,7 +422,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanParam
     const float x = one(p.x, b * p.x_sb + c, p.ex);
     float d = one(p.dt, b * p.dt_sb + c, p.edt) + (p.dt_bias != nullptr ? __ldg(p.dt_bias + c) : 0.f);
     const float4 bb = quad(p.Bm, b * p.B_sb + g * N + 4 * q, p.eB), cc = quad(p.Cm, b * p.C_sb + g * N + 4 * q, p.eC);
-    if (p.softplus) d = softplus_series(d);
+    if (p.softplus) d = split(softplus_pair(both(d))).x;
     const float u = d * x, s = -kLog2e * d;
     h.x = fmaf(ex2(s * expf(a.x)), h.x, u * bb.x);
     h.y = fmaf(ex2(s * expf(a.y)), h.y, u * bb.y);
@@ -504,7 +512,7 @@ cgdr_status check(const cgdr_scan_args *a) {
     if (!a->x || !a->dt || !a->Bm || !a->Cm || !a->o || !a->A_log || !a->state) return CGDR_ERR_INVALID_ARG;
     if (!aligned_to(a->x, 16) || !aligned_to(a->dt, 16) || !aligned_to(a->z, 16) || !aligned_to(a->Bm, 16) ||
         !aligned_to(a->Cm, 16) || !aligned_to(a->o, 16) || !aligned_to(a->A_log, 16) || !aligned_to(a->state, 16) ||
-        !aligned_to(a->D, 4) || !aligned_to(a->dt_bias, 4) || !aligned_to(a->cu, 4) || !aligned_to(a->status, 4))
+        !aligned_to(a->D, 8) || !aligned_to(a->dt_bias, 8) || !aligned_to(a->cu, 4) || !aligned_to(a->status, 4))
         return CGDR_ERR_ALIGNMENT;
     const int esz = esize(a->dtype), osz = esize(a->o_dtype);
     const bool tok = a->cu || a->T > 1, bat = !a->cu;

@@ -80,8 +80,8 @@ typedef struct cgdr_scan_args {
     const void *Cm; int64_t Cm_sb, Cm_st;       /* [B,T,G,N], groups dense */
     void *o;        int64_t o_sb, o_st;         /* [B,T,C] */
     const float *A_log;                         /* [C,N] dense, 16-byte aligned */
-    const float *D;                             /* [C] or NULL */
-    const float *dt_bias;                       /* [C] or NULL */
+    const float *D;                             /* [C] or NULL, 8-byte aligned */
+    const float *dt_bias;                       /* [C] or NULL, 8-byte aligned */
     float *state;                               /* [B,C,N] dense; in place */
     const int32_t *cu;                          /* [B+1] or NULL */
     int32_t *status;                            /* reserved for the index-checking build */
