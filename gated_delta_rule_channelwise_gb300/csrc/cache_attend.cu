@@ -20,6 +20,12 @@
 // whatever the scales are and fits fp16; the denominator adds p' / vs.  A further 2^15 keeps small
 // p' out of fp16's subnormal range (they lose their relative accuracy below 2^-29 of the largest).
 //
+// Lengths differ, so the work is not cut by request: a unit is (request, row tile, key-value head), its
+// cost the 64-token steps of its cache, and every block takes an equal share of the steps of all
+// units in a row.  A unit that one block has from end to end it writes out; of the others each block
+// leaves a part (maximum, denominator, weighted sum), at most two of them, one for a unit that
+// began before its share and one for a unit that goes on after it, and a second kernel joins a unit's parts.
+//
 // bf16 queries are scaled by a power of two per row to magnitudes below 2 and are then exact in fp16
 // down to 2^-14 of the row's largest (beyond that their error is below 2^-25 of it).  fp32 queries
 // and their probabilities are carried as two fp16 parts.
@@ -34,11 +40,12 @@ constexpr int kWarps = 4;
 constexpr int kRows = 16;                             // rows of a tile
 constexpr int kStep = 16;                             // cached tokens of a warp's step
 constexpr int kStages = 4;
-constexpr int kMaxSplit = 4096;                       // cached tokens of a block: its pages' numbers and scales are staged
+constexpr int kBlockStep = kWarps * kStep;            // cached tokens of a block's step: the scheduling unit
+constexpr int kMinShare = 4;                          // steps of a block's share at least: joining costs about as much
+constexpr int kInfos = 320;                           // pages whose numbers and scales a block holds at a time
 
 struct AttendParams {
-    int B, n, Hq, Hkv, G, page, width, num_pages, max_q, max_kv;
-    int split, splits;                                // tokens of a split, splits
+    int B, n, Hq, Hkv, G, page, shift, width, num_pages, max_q, most;        // most: cached tokens of a request at most
     float scale;
     const void *q;
     void *o;
@@ -48,9 +55,61 @@ struct AttendParams {
     const int32_t *table;
     int64_t table_sb;
     const int32_t *kv_lens, *cu;
-    float *part;                                      // [n * Hq][splits][D + 2]: M, l, o; null: one split
+    float *ml, *part;                                 // parts: [2 grid][kRows][2] maximum and denominator, [2 grid][kRows][D]
+    int blocks;                                       // of the first kernel
     int *status;
 };
+
+// A request as the kernel sees it.
+struct Request {
+    int first, q_len, kv, behind;                     // first query token, tokens, cached tokens, position of query token 0
+    int units, steps;                                 // (row tile, head) pairs, block steps of each
+};
+__device__ __forceinline__ Request request(const AttendParams &p, int b) {
+    const int2 span = seq_span(p.cu, b, p.n);
+    const int len = span.y - span.x, kv = max(p.kv_lens[b], 0);
+    Request r;
+    r.first = span.x;
+    r.q_len = min(len, p.max_q);
+    r.kv = min(kv, p.most);
+    r.behind = kv - len;
+    r.units = (r.q_len * p.G + kRows - 1) / kRows * p.Hkv;
+    r.steps = max((r.kv + kBlockStep - 1) / kBlockStep, 1);           // rows that see nothing are written, too
+    return r;
+}
+__device__ __forceinline__ bool cut(const AttendParams &p, int b) {
+    const int2 span = seq_span(p.cu, b, p.n);
+    return span.y - span.x > p.max_q || p.kv_lens[b] > p.most;
+}
+
+// The steps of all requests, and a block's share of them; worked out by a whole block of NT threads.
+struct Share {
+    int64_t total, size;                              // steps, steps of a block
+};
+template <int NT>
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *s_sum) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = x;
+    __syncthreads();
+    int64_t t = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) t += s_sum[w];
+    return t;
+}
+template <int NT>
+__device__ __forceinline__ Share share_of(const AttendParams &p, int64_t *s_sum) {
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < p.B; b += NT) {
+        const Request r = request(p, b);
+        mine += (int64_t)r.units * r.steps;
+    }
+    Share s;
+    s.total = block_sum<NT>(mine, s_sum);
+    s.size = max((s.total + p.blocks - 1) / p.blocks, (int64_t)kMinShare);
+    return s;
+}
 
 __device__ __forceinline__ void report(int *status, int code) {
     if (status != nullptr) atomicExch(status, code);
@@ -66,7 +125,7 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-constexpr int kMaxKv = 1 << 27;                       // splits of one request stay within the grid's limit
+constexpr int kMaxKv = 1 << 30;                       // positions stay well inside 32 bits
 // Two sign-flipped int8 in bytes 0 and 2 above exponent bytes -> their values as fp16.
 __device__ __forceinline__ uint32_t less_bias(uint32_t x) {
     const uint32_t bias = 0x64806480u;                // 1152
@@ -76,12 +135,12 @@ __device__ __forceinline__ uint32_t less_bias(uint32_t x) {
 __device__ __forceinline__ uint32_t low_pair(uint32_t w) { return less_bias(__byte_perm(w, 0x64646464u, 0x4140)); }
 __device__ __forceinline__ uint32_t high_pair(uint32_t w) { return less_bias(__byte_perm(w, 0x64646464u, 0x4342)); }
 
-// What a block keeps of its split's pages.
+// What a block holds of a page, in 16 bytes.
+constexpr int kZeroV = 1 << 30;                       // flag in `page`: v's scale is (as good as) zero, and so are the values
 struct PageInfo {
     int page;                                         // -1: outside the cache
     float k;                                          // k's scale
-    float lv, iv;                                     // log2 and reciprocal of v's scale; 0 and 1 where it is (as good as) 0
-    bool zero_v;
+    float lv, iv;                                     // log2 and reciprocal of v's scale; 0 and 1 with kZeroV
 };
 
 template <int D, typename T>
@@ -94,47 +153,23 @@ struct AttendShape {
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_attend_kernel(const AttendParams p) {
+struct AttendBlocks {                                 // blocks of an SM: shared memory at D = 128, registers below
+    static constexpr int value = (D == 128 ? 3 : D == 64 ? 4 : 5) - (sizeof(T) == 4 ? 1 : 0);
+};
+
+// One unit's steps [step0, step1), by a whole block.
+template <int D, typename T>
+__device__ __forceinline__ void attend_unit(const AttendParams &p, const Request &rq, int b, int unit, int step0, int step1,
+                                            unsigned char *smem) {
     using Sh = AttendShape<D, T>;
     constexpr int PARTS = Sh::PARTS, KS = D / 16, NT = D / 8;         // k steps of q.k, column tiles of p.v
-    extern __shared__ __align__(16) unsigned char smem[];
-    PageInfo *info = reinterpret_cast<PageInfo *>(smem + Sh::BYTES);  // [split / page + 1]
+    PageInfo *info = reinterpret_cast<PageInfo *>(smem + Sh::BYTES);  // [kInfos + 1]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
-    const int split = blockIdx.y, b = blockIdx.z, hk = blockIdx.x % p.Hkv, row0 = blockIdx.x / p.Hkv * kRows;
-
-    const int2 span = seq_span(p.cu, b, p.n);
-    const int kv_len = max(p.kv_lens[b], 0);
-    int q_len = span.y - span.x, kv = kv_len;
-    const int most = (int)min((int64_t)p.max_kv, (int64_t)p.width * p.page);
-    if (q_len > p.max_q || kv > most) {
-        if (tid == 0) report(p.status, (int)CGDR_ERR_CAPACITY);
-        kv = min(kv, most);
-        q_len = min(q_len, p.max_q);
-    }
-    const int rows = q_len * p.G;
-    if (row0 >= rows) return;
-    const int behind = kv_len - (span.y - span.x);                     // position of the request's query token 0
+    const int hk = unit % p.Hkv, row0 = unit / p.Hkv * kRows, rows = rq.q_len * p.G;
+    const int kv = rq.kv, behind = rq.behind;
     const int last_row = min(row0 + kRows, rows) - 1;
-    const int begin = split * p.split;
-    const int end = min(min(begin + p.split, kv), behind + last_row / p.G + 1);       // what some row of the tile sees
-    const int steps = end > begin ? (end - begin + kStep - 1) / kStep : 0;
-
-    for (int i = tid; i * p.page < end - begin; i += 32 * kWarps) {
-        PageInfo f;
-        const int64_t at = b * p.table_sb + (begin / p.page + i);
-        f.page = in_bounds(at, p.e_table, p.status, nullptr) ? p.table[at] : -1;
-        f.k = 0.f; f.lv = 0.f; f.iv = 1.f; f.zero_v = true;
-        if (f.page < 0 || f.page >= p.num_pages) {
-            f.page = -1;
-            report(p.status, (int)CGDR_ERR_BOUNDS);
-        } else {
-            f.k = p.ks[(int64_t)f.page * p.Hkv + hk];
-            const float v = p.vs[(int64_t)f.page * p.Hkv + hk];
-            f.zero_v = v < 0x1p-100f;                 // false for a NaN, which then spreads as it has to
-            if (!f.zero_v) { f.lv = log2f(v); f.iv = 1.f / v; }
-        }
-        info[i] = f;
-    }
+    const int begin = step0 * kBlockStep;
+    const int end = min(min(step1 * kBlockStep, kv), behind + last_row / p.G + 1);    // what some row of the tile sees
 
     // this lane's two rows of the tile, and their queries as A operands
     int q_tok[2], seen[2];
@@ -147,7 +182,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_att
         q_tok[r] = row / p.G;
         seen[r] = ok ? behind + q_tok[r] + 1 : 0;     // positions below this one
         float f[D / 4];
-        const int64_t off = (int64_t)(span.x + q_tok[r]) * p.q_st + (int64_t)(hk * p.G + row % p.G) * p.q_sh + j * (D / 4);
+        const int64_t off = (int64_t)(rq.first + q_tok[r]) * p.q_st + (int64_t)(hk * p.G + row % p.G) * p.q_sh + j * (D / 4);
 #pragma unroll
         for (int v = 0; v < D / 4 / Vec<T>::n; ++v) {
             uint4 raw = make_uint4(0, 0, 0, 0);
@@ -177,16 +212,39 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_att
                 }
             }
     }
-    __syncthreads();                                  // the page infos
+    float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
     unsigned char *ring = smem + warp * kStages * Sh::STAGE;
     const uint32_t ring_s = smem_u32(ring);
+    const int span = kInfos * p.page;                 // cached tokens whose pages are held at a time
+    for (int from = begin; from < end; from += span) {
+    const int steps = (min(end - from, span) + kStep - 1) / kStep;
+    const int page0 = from >> p.shift;
+    for (int i = tid; i <= ((from + steps * kStep - 1) >> p.shift) - page0; i += 32 * kWarps) {
+        PageInfo f{-1, 0.f, 0.f, 1.f};
+        const int64_t at = b * p.table_sb + page0 + i;
+        const int page = in_bounds(at, p.e_table, p.status, nullptr) ? p.table[at] : -1;
+        if (page < 0 || page >= p.num_pages) {
+            report(p.status, (int)CGDR_ERR_BOUNDS);
+        } else {
+            f.page = page;
+            f.k = p.ks[(int64_t)page * p.Hkv + hk];
+            const float v = p.vs[(int64_t)page * p.Hkv + hk];
+            if (v < 0x1p-100f) f.page |= kZeroV;      // not so for a NaN, which then spreads as it has to
+            else { f.lv = log2f(v); f.iv = 1.f / v; }
+        }
+        info[i] = f;
+    }
+    __syncthreads();
+
     auto issue = [&](int step, int stage) {           // copies of a step's 16 keys and 16 values
         if (step < steps) {
-            const int at = step * kStep;
-            const int page = info[at / p.page].page;
+            const int at = from + step * kStep, page = info[(at >> p.shift) - page0].page;
             if (page >= 0) {
-                const int64_t src = ((int64_t)page * p.Hkv + hk) * p.page * D + (int64_t)(at % p.page) * D;
+                const int64_t src = ((((int64_t)(page & ~kZeroV) * p.Hkv + hk) << p.shift) + (at & (p.page - 1))) * D;
 #pragma unroll
                 for (int c = 0; c < kStep * D / 16 / 32; ++c) {
                     const int e = (c * 32 + lane) * 16;
@@ -197,12 +255,6 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_att
         }
         cp_async_commit();
     };
-
-    float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float acc[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue(warp + s * kWarps, s);
     int stage = 0;
@@ -212,9 +264,10 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_att
         __syncwarp();                                 // every lane's copies have landed
         const unsigned char *kb = ring + stage * Sh::STAGE, *vb = kb + kStep * D;
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        const PageInfo f = info[step * kStep / p.page];
+        const int at = from + step * kStep;
+        const PageInfo f = info[(at >> p.shift) - page0];
         if (f.page < 0) continue;
-        const int at = begin + step * kStep;
+        const bool zero_v = f.page & kZeroV;
 
         float s[2][4];                                // scores: keys 2j, 2j+1 (+8) for rows g, g+8
 #pragma unroll
@@ -275,10 +328,10 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_att
                 const float x = ex2(s[t][2 * r] - base[r] + 15.f), y = ex2(s[t][2 * r + 1] - base[r] + 15.f);
                 l[r] = fmaf(x + y, f.iv, l[r]);
                 const uint32_t hi = half2_bits(x, y);
-                pa[0][2 * t + r] = f.zero_v ? 0u : hi;
+                pa[0][2 * t + r] = zero_v ? 0u : hi;
                 if (PARTS == 2) {
                     const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                    pa[PARTS - 1][2 * t + r] = f.zero_v ? 0u : half2_bits(x - back.x, y - back.y);
+                    pa[PARTS - 1][2 * t + r] = zero_v ? 0u : half2_bits(x - back.x, y - back.y);
                 }
             }
         // p.v: column n = l / 4 of tile i is d = (l / 4) D/8 + i
@@ -312,7 +365,8 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_att
         __syncwarp();                                 // the stage is read before it is filled again
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+    __syncthreads();                                  // infos and stages are free again
+    }
 
     // join the four warps: [warp][row][M, l, o...] in the ring's place
     float *join = reinterpret_cast<float *>(smem);
@@ -345,97 +399,168 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3) cache_att
             sum = fmaf(f, from[w * kRows * (D + 2) + 1], sum);
             o = fmaf(f, from[w * kRows * (D + 2) + 2 + d], o);
         }
-        const int tok = span.x + row / p.G, head = hk * p.G + row % p.G;
-        if (p.part != nullptr) {
-            float *part = p.part + (((int64_t)tok * p.Hq + head) * p.splits + split) * (D + 2);
-            part[2 + d] = o;
-            if (d == 0) { part[0] = m; part[1] = sum; }
+        if (step0 > 0 || step1 < rq.steps) {          // a part: of a unit begun before (0) or going on after (1)
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (step0 > 0 ? 0 : 1);
+            p.part[(slot * kRows + r) * D + d] = o;
+            if (d == 0) *reinterpret_cast<float2 *>(p.ml + (slot * kRows + r) * 2) = make_float2(m, sum);
         } else {
-            const int64_t off = (int64_t)tok * p.o_st + (int64_t)head * p.o_sh + d;
+            const int64_t off = (int64_t)(rq.first + row / p.G) * p.o_st + (int64_t)(hk * p.G + row % p.G) * p.o_sh + d;
             const float y = sum == 0.f ? 0.f : o / sum;
             if (in_bounds(off, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off] = Cvt<T>::from_f(y);
         }
     }
+    __syncthreads();                                  // the ring is free again
 }
 
-// Joins the splits of a row: a warp a row, four values of d (or D/32) a lane.
 template <int D, typename T>
-__global__ void __launch_bounds__(128) cache_join_kernel(const AttendParams p) {
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (int64_t)p.n * p.Hq) return;
-    const int tok = (int)(row / p.Hq), head = (int)(row % p.Hq);
-    int lo = 0, hi = p.B;                             // the request: the first b with cu[b + 1] > tok
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu[mid + 1] > tok) hi = mid;
-        else lo = mid + 1;
+__global__ void __launch_bounds__(32 * kWarps, AttendBlocks<D, T>::value) cache_attend_kernel(const AttendParams p) {
+    constexpr int NT = 32 * kWarps;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ int64_t s_sum[NT / 32];
+    const Share share = share_of<NT>(p, s_sum);
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < p.B; b += NT)
+            if (cut(p, b)) report(p.status, (int)CGDR_ERR_CAPACITY);
+    int64_t left = share.size, at = share.size * blockIdx.x;          // steps to do, from this one of all on
+    if (at >= share.total) return;
+    if (left > share.total - at) left = share.total - at;
+    int b = 0;
+    // the request of the first step: skip whole groups of NT requests, then single ones
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
+        int64_t mine = 0;
+        if (b0 + threadIdx.x < p.B) {
+            const Request r = request(p, b0 + threadIdx.x);
+            mine = (int64_t)r.units * r.steps;
+        }
+        const int64_t group = block_sum<NT>(mine, s_sum);
+        b = b0;
+        if (at < group) break;
+        at -= group;
     }
-    if (lo >= p.B) return;
-    const int2 span = seq_span(p.cu, lo, p.n);
-    if (tok < span.x || tok - span.x >= p.max_q) return;
-    const float *part = p.part + row * p.splits * (D + 2);
-    const int most = (int)min((int64_t)p.max_kv, (int64_t)p.width * p.page);
-    const int used = max(0, min(p.splits, (min(p.kv_lens[lo], most) + p.split - 1) / p.split));
-    float m = -INFINITY;
-    for (int s = lane; s < used; s += 32) m = fmaxf(m, part[(int64_t)s * (D + 2)]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float at = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, o[D / 32];
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-    for (int s = 0; s < used; ++s) {
-        const float *from = part + (int64_t)s * (D + 2);
-        const float f = ex2(from[0] - at);
-        sum = fmaf(f, from[1], sum);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, from[2 + lane + 32 * e], o[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-        const int64_t off = (int64_t)tok * p.o_st + (int64_t)head * p.o_sh + lane + 32 * e;
-        const float y = sum == 0.f ? 0.f : o[e] / sum;
-        if (in_bounds(off, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off] = Cvt<T>::from_f(y);
+    for (; b < p.B && left > 0; ++b) {
+        const Request r = request(p, b);
+        const int64_t all = (int64_t)r.units * r.steps;
+        while (at < all && left > 0) {
+            const int unit = (int)(at / r.steps), step0 = (int)(at % r.steps);
+            const int step1 = (int)min((int64_t)r.steps, step0 + left);
+            attend_unit<D, T>(p, r, b, unit, step0, step1, smem);
+            at += step1 - step0;
+            left -= step1 - step0;
+        }
+        at = at > all ? at - all : 0;
     }
 }
 
-// Cached tokens of a split: enough blocks for every SM to hold its three, several times over where
-// lengths differ, but no split below 256 tokens, where joining would cost as much as it saves.
-int split_of(const cgdr_attend_args &a) {
+// Joins the parts of a unit: four rows to a block, four groups of threads that take every fourth part.
+constexpr int kJoinRows = 4, kJoinGroups = 4;
+template <int D, typename T>
+__global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) cache_join_kernel(const AttendParams p) {
+    constexpr int LANES = kJoinRows * D / 4, NT = LANES * kJoinGroups;
+    __shared__ int64_t s_sum[NT / 32];
+    __shared__ float4 s_o[kJoinGroups][LANES];
+    __shared__ float2 s_ml[kJoinGroups][LANES];
+    const int b = blockIdx.z, unit = blockIdx.x, lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const Request rq = request(p, b);
+    const int r = blockIdx.y * kJoinRows + lane / (D / 4), d = lane % (D / 4) * 4;
+    const int row = unit / p.Hkv * kRows + r, rows = rq.q_len * p.G;
+    if (unit >= rq.units || unit / p.Hkv * kRows + (int)blockIdx.y * kJoinRows >= rows) return;
+    const Share share = share_of<NT>(p, s_sum);
+    int64_t before = 0;
+    for (int i = threadIdx.x; i < b; i += NT) {
+        const Request x = request(p, i);
+        before += (int64_t)x.units * x.steps;
+    }
+    const int64_t at = block_sum<NT>(before, s_sum) + (int64_t)unit * rq.steps;
+    const int64_t first = at / share.size, last = (at + rq.steps - 1) / share.size;
+    if (first == last) return;                        // written out by its one block
+    float m = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int64_t c = first + group; c <= last; c += kJoinGroups) {
+        const int64_t slot = 2 * c + (c == first ? 1 : 0);
+        const float2 ml = *reinterpret_cast<const float2 *>(p.ml + (slot * kRows + r) * 2);
+        const float4 x = *reinterpret_cast<const float4 *>(p.part + (slot * kRows + r) * D + d);
+        const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+        const float keep = ex2(m - base), add = ex2(ml.x - base);
+        sum = fmaf(add, ml.y, sum * keep);
+        o.x = fmaf(add, x.x, o.x * keep); o.y = fmaf(add, x.y, o.y * keep);
+        o.z = fmaf(add, x.z, o.z * keep); o.w = fmaf(add, x.w, o.w * keep);
+        m = top;
+    }
+    s_o[group][lane] = o;
+    s_ml[group][lane] = make_float2(m, sum);
+    __syncthreads();
+    if (group != 0 || row >= rows) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups; ++i) m = fmaxf(m, s_ml[i][lane].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups; ++i) {
+        const float f = ex2(s_ml[i][lane].x - base);
+        const float4 x = s_o[i][lane];
+        sum = fmaf(f, s_ml[i][lane].y, sum);
+        v[0] = fmaf(f, x.x, v[0]); v[1] = fmaf(f, x.y, v[1]); v[2] = fmaf(f, x.z, v[2]); v[3] = fmaf(f, x.w, v[3]);
+    }
+    const int64_t off = (int64_t)(rq.first + row / p.G) * p.o_st + (int64_t)(unit % p.Hkv * p.G + row % p.G) * p.o_sh + d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (in_bounds(off + e, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off + e] = Cvt<T>::from_f(sum == 0.f ? 0.f : v[e] / sum);
+}
+
+// Blocks of the first kernel: all that fit, but no more than shares of kMinShare steps need.
+template <int D, typename T>
+int blocks_of(const cgdr_attend_args &a) {
     const int64_t sms = device_sms() > 0 ? device_sms() : 152;       // sizes workspaces without a device, too
-    const int G = a.Hq / a.Hkv;
-    const int64_t tiles = (int64_t)a.B * a.Hkv * (((int64_t)a.max_q * G + kRows - 1) / kRows);
+    const int64_t units = (int64_t)a.B * a.Hkv * (((int64_t)a.max_q * (a.Hq / a.Hkv) + kRows - 1) / kRows);
     const int64_t kv = a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page;
-    int64_t split = kv * tiles / (4 * 3 * sms) + 1;
-    split = split < 256 ? 256 : split > kMaxSplit ? kMaxSplit : split;
-    return (int)((split + 127) / 128 * 128);          // whole pages
+    const int64_t steps = kv > 0 ? (kv + kBlockStep - 1) / kBlockStep : 1, most = sms * AttendBlocks<D, T>::value;
+    const int64_t need = (units * steps + kMinShare - 1) / kMinShare;
+    return (int)(need < most ? need : most);
 }
-int splits_of(const cgdr_attend_args &a, int split) {
-    const int64_t kv = a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page;
-    return (int)((kv + split - 1) / split);
+template <int D, typename T>
+size_t workspace_for(const cgdr_attend_args &a) {
+    const int blocks = blocks_of<D, T>(a);
+    return blocks > 1 ? (size_t)2 * blocks * kRows * (D + 2) * sizeof(float) : 0;
 }
 
 template <int D, typename T>
-cgdr_status launch_attend(const AttendParams &p, cudaStream_t s) {
+cgdr_status launch_attend(const cgdr_attend_args &a, AttendParams &p, float *ws, cudaStream_t s) {
     using Sh = AttendShape<D, T>;
     static SmemOnce smem_once;
-    constexpr int kMost = Sh::BYTES + (kMaxSplit / 16 + 1) * (int)sizeof(PageInfo);
-    if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_kernel<D, T>), kMost)) return CGDR_ERR_CUDA;
-    const int bytes = Sh::BYTES + (p.split / p.page + 1) * (int)sizeof(PageInfo);
-    const int64_t tiles = ((int64_t)p.max_q * p.G + kRows - 1) / kRows * p.Hkv;
-    cache_attend_kernel<D, T><<<dim3((unsigned)tiles, p.splits > 0 ? p.splits : 1, p.B), 32 * kWarps, bytes, s>>>(p);
-    if (p.part != nullptr) {
+    constexpr int kBytes = Sh::BYTES + (kInfos + 1) * (int)sizeof(PageInfo);
+    if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_kernel<D, T>), kBytes)) return CGDR_ERR_CUDA;
+    p.blocks = blocks_of<D, T>(a);
+    p.part = ws;
+    p.ml = ws + (size_t)2 * p.blocks * kRows * D;
+    cache_attend_kernel<D, T><<<p.blocks, 32 * kWarps, kBytes, s>>>(p);
+    if (p.blocks > 1) {
         if (cudaPeekAtLastError() != cudaSuccess) return launched();
-        cache_join_kernel<D, T><<<(unsigned)(((int64_t)p.n * p.Hq + 3) / 4), 128, 0, s>>>(p);
+        const int64_t tiles = ((int64_t)a.max_q * p.G + kRows - 1) / kRows;
+        const int64_t rows = (int64_t)a.max_q * p.G < kRows ? (int64_t)a.max_q * p.G : kRows;
+        cache_join_kernel<D, T><<<dim3((unsigned)(tiles * a.Hkv), (unsigned)((rows + kJoinRows - 1) / kJoinRows), a.B),
+                                  kJoinRows * kJoinGroups * D / 4, 0, s>>>(p);
     }
     return launched();
 }
 
-template <typename T>
-cgdr_status launch_dim(const AttendParams &p, int D, cudaStream_t s) {
-    return D == 128 ? launch_attend<128, T>(p, s) : D == 64 ? launch_attend<64, T>(p, s) : launch_attend<32, T>(p, s);
+#define CGDR_ATTEND_CASES(CALL) \
+    if (a.dtype == CGDR_BF16) \
+        return a.D == 128 ? CALL(128, __nv_bfloat16) : a.D == 64 ? CALL(64, __nv_bfloat16) : CALL(32, __nv_bfloat16); \
+    return a.D == 128 ? CALL(128, float) : a.D == 64 ? CALL(64, float) : CALL(32, float);
+size_t workspace_of(const cgdr_attend_args &a) {
+#define CGDR_CALL(D, T) workspace_for<D, T>(a)
+    CGDR_ATTEND_CASES(CGDR_CALL)
+#undef CGDR_CALL
 }
+cgdr_status launch_of(const cgdr_attend_args &a, AttendParams &p, float *ws, cudaStream_t s) {
+#define CGDR_CALL(D, T) launch_attend<D, T>(a, p, ws, s)
+    CGDR_ATTEND_CASES(CGDR_CALL)
+#undef CGDR_CALL
+}
+#undef CGDR_ATTEND_CASES
 
 cgdr_status check(const cgdr_attend_args *a) {
     if (!a) return CGDR_ERR_INVALID_ARG;
@@ -443,7 +568,7 @@ cgdr_status check(const cgdr_attend_args *a) {
         a->max_q < 0 || a->max_kv < 0)
         return CGDR_ERR_INVALID_ARG;
     if (!dtype_ok(a->dtype) || !page_ok(a->page) || (a->D != 32 && a->D != 64 && a->D != 128)) return CGDR_ERR_UNSUPPORTED;
-    if (a->B > 65535 || a->n > kMaxTokens || a->max_kv > kMaxKv) return CGDR_ERR_UNSUPPORTED;
+    if (a->B > 65535 || a->n > kMaxTokens || a->max_kv > kMaxKv || a->num_pages > kZeroV) return CGDR_ERR_UNSUPPORTED;
     if (((int64_t)a->max_q * (a->Hq / a->Hkv) + kRows) * a->Hkv > INT32_MAX) return CGDR_ERR_UNSUPPORTED;
     if (a->B == 0 || a->n == 0 || a->max_q == 0) return CGDR_OK;
     if (!a->q || !a->o || !a->kv_lens || !a->cu) return CGDR_ERR_INVALID_ARG;
@@ -457,11 +582,6 @@ cgdr_status check(const cgdr_attend_args *a) {
     const int esz = esize(a->dtype);
     if (!row_stride_ok(a->q_st, esz) || !row_stride_ok(a->q_sh, esz) || a->o_st < 0 || a->o_sh < 0) return CGDR_ERR_ALIGNMENT;
     return CGDR_OK;
-}
-
-size_t workspace_of(const cgdr_attend_args &a) {
-    const int splits = splits_of(a, split_of(a));
-    return splits > 1 ? (size_t)a.n * a.Hq * splits * (a.D + 2) * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -481,18 +601,16 @@ cgdr_status cgdr_cache_attend(const cgdr_attend_args *a, void *ws, size_t ws_byt
     const size_t need = workspace_of(*a);
     if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned_to(ws, 16))) return CGDR_ERR_WORKSPACE;
     AttendParams p{};
-    p.B = a->B; p.n = a->n; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = a->Hq / a->Hkv; p.page = a->page; p.width = a->width;
-    p.num_pages = a->num_pages; p.max_q = a->max_q; p.max_kv = a->max_kv;
-    p.split = split_of(*a); p.splits = splits_of(*a, p.split);
+    p.B = a->B; p.n = a->n; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = a->Hq / a->Hkv; p.page = a->page; p.shift = __builtin_ctz(a->page); p.width = a->width;
+    p.num_pages = a->num_pages; p.max_q = a->max_q;
+    p.most = (int)(a->max_kv < (int64_t)a->width * a->page ? a->max_kv : (int64_t)a->width * a->page);
     p.scale = a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->D);
     p.q = a->q; p.q_st = a->q_st; p.q_sh = a->q_sh; p.o = a->o; p.o_st = a->o_st; p.o_sh = a->o_sh;
     p.eq = extent3(a->n, a->q_st, a->Hq, a->q_sh, a->D); p.eo = extent3(a->n, a->o_st, a->Hq, a->o_sh, a->D);
     p.kc = a->k_cache; p.vc = a->v_cache; p.ks = a->k_scale; p.vs = a->v_scale;
     p.table = a->block_table; p.table_sb = a->table_sb; p.e_table = (a->B - 1) * a->table_sb + a->width;
     p.kv_lens = a->kv_lens; p.cu = a->cu; p.status = a->status;
-    p.part = need > 0 ? static_cast<float *>(ws) : nullptr;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return a->dtype == CGDR_BF16 ? launch_dim<__nv_bfloat16>(p, a->D, s) : launch_dim<float>(p, a->D, s);
+    return launch_of(*a, p, static_cast<float *>(ws), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
