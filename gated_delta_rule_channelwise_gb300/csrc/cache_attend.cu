@@ -1,24 +1,26 @@
 // Attention over the 8-bit paged cache (cgdr_cache_attend).
 //
-// For single tokens the cache's bytes are the time: 2 D bytes a token and head are read once.  A
-// row tile is the 16 rows of an mma.sync m16n8k16 product -- (query token, query head of the group)
-// pairs that share one key-value head -- and a warp takes 16 cached tokens at a time, all of D: a
-// 16-token piece never crosses a page, is contiguous in the cache, and streams through the warp's
-// own ring of shared-memory stages by cp.async, so the four warps of a block never wait for one
-// another until they join their softmax states at the end.  tcgen05 has no use here: its smallest
-// tile has 64 rows, and one 16-row tile fed at the memory's rate leaves the mma.sync pipe two
-// thirds idle.
+// For single tokens the cache's bytes are the time: 2 D bytes a token and head are read once.  A warp
+// takes 16 cached tokens at a time, all of D: a 16-token piece never crosses a page, is contiguous in
+// the cache, and streams through the warp's own ring of shared-memory stages by cp.async, so the
+// four warps of a block never wait for one another until they join their softmax states at the end.
+// The tokens are the 16 rows of the mma.sync m16n8k16 products and the columns are queries: (query
+// token, query head of the group) pairs that share one key-value head, eight or sixteen to a tile.
+// Both products are taken transposed, s^T = k q^T and o^T = v^T p^T, so eight queries cost half of
+// what sixteen do, in products and in registers; a p^T tile changes from result to operand by two
+// 8 x 8 transpositions (movmatrix).  tcgen05 has no use here: its smallest tile has 64 rows.
 //
 // int8 -> fp16 is exact and takes no conversion instruction: the byte with its sign bit flipped,
 // placed under the exponent byte 0x64, is the fp16 number 1024 + 128 + value, and one packed
 // subtraction leaves the value.  The order of d within a product is free as long as both operands
-// share it, so a lane reads contiguous bytes: for q.k lane l (j = l % 4) has bytes j D/4 .. of key
-// l / 4; for p.v it has bytes (l / 4) D/8 .. of values 2j, 2j+1, 2j+8, 2j+9.
+// share it, so a lane reads contiguous bytes: of keys g = l / 4 and g + 8 its D/4 bytes from (l % 4) D/4
+// on; of values 2j, 2j+1, 2j+8, 2j+9 (j = l % 4) its D/8 bytes from g D/8 on.
 //
 // The scales stay out of the products: k's multiplies the score; v's becomes part of the exponent,
 // p' = 2^(s + log2 vs - M), with its own running maximum M of s + log2 vs, so that p' lies in (0, 1]
 // whatever the scales are and fits fp16; the denominator adds p' / vs.  A further 2^15 keeps small
 // p' out of fp16's subnormal range (they lose their relative accuracy below 2^-29 of the largest).
+// M is only looked for, over the lanes, when some score passes it: a vote a step instead of shuffles.
 //
 // Lengths differ, so the work is not cut by request: a unit is (request, row tile, key-value head), its
 // cost the 64-token steps of its cache, and every block takes an equal share of the steps of all
@@ -37,15 +39,17 @@ namespace cgdr {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kRows = 16;                             // rows of a tile
+constexpr int kRows = 16;                             // rows of a tile at most
 constexpr int kStep = 16;                             // cached tokens of a warp's step
-constexpr int kStages = 4;
+constexpr int kStages = 3;
+constexpr float kLowest = -3e38f;                     // below every score: M before there is one
 constexpr int kBlockStep = kWarps * kStep;            // cached tokens of a block's step: the scheduling unit
 constexpr int kMinShare = 4;                          // steps of a block's share at least: joining costs about as much
 constexpr int kInfos = 320;                           // pages whose numbers and scales a block holds at a time
 
 struct AttendParams {
-    int B, n, Hq, Hkv, G, page, shift, width, num_pages, max_q, most;        // most: cached tokens of a request at most
+    int B, n, Hq, Hkv, G, tile, page, shift, width, num_pages, max_q, most;  // tile: rows of a tile, 8 or 16;
+                                                       // most: cached tokens of a request at most
     float scale;
     const void *q;
     void *o;
@@ -73,7 +77,7 @@ __device__ __forceinline__ Request request(const AttendParams &p, int b) {
     r.q_len = min(len, p.max_q);
     r.kv = min(kv, p.most);
     r.behind = kv - len;
-    r.units = (r.q_len * p.G + kRows - 1) / kRows * p.Hkv;
+    r.units = (r.q_len * p.G + p.tile - 1) / p.tile * p.Hkv;
     r.steps = max((r.kv + kBlockStep - 1) / kBlockStep, 1);           // rows that see nothing are written, too
     return r;
 }
@@ -143,46 +147,57 @@ struct PageInfo {
     float lv, iv;                                     // log2 and reciprocal of v's scale; 0 and 1 with kZeroV
 };
 
-template <int D, typename T>
-struct AttendShape {
+template <int D, int NQ, typename T>
+struct AttendShape {                                                  // NQ: tiles of eight queries, 1 or 2
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;              // fp16 parts of q and p
     static constexpr int STAGE = 2 * kStep * D;                       // k and v bytes of a step
     static constexpr int RING = kWarps * kStages * STAGE;
-    static constexpr int JOIN = kWarps * kRows * (D + 2) * 4;         // the warps' softmax states, in the ring's place
+    static constexpr int JOIN = kWarps * 8 * NQ * (D + 4) * 4;        // the warps' softmax states, in the ring's place
     static constexpr int BYTES = RING > JOIN ? RING : JOIN;
+    static constexpr int BLOCKS = (D == 128 ? 5 : 6) - NQ - (sizeof(T) == 4 ? 1 : 0); // of an SM, by shared memory and registers
 };
 
-template <int D, typename T>
-struct AttendBlocks {                                 // blocks of an SM: shared memory at D = 128, registers below
-    static constexpr int value = (D == 128 ? 3 : D == 64 ? 4 : 5) - (sizeof(T) == 4 ? 1 : 0);
-};
+// Four values of a row of o from a weighted sum and its denominator; a row that saw nothing is zero.
+template <typename T>
+__device__ __forceinline__ void put_row(const AttendParams &p, int tok, int head, int d, const float (&o)[4], float sum) {
+    const int64_t off = (int64_t)tok * p.o_st + (int64_t)head * p.o_sh + d;
+    const float by = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (in_bounds(off + e, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off + e] = Cvt<T>::from_f(sum == 0.f ? 0.f : o[e] * by);
+}
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {          // an 8 x 8 tile of fp16 over the warp
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
 // One unit's steps [step0, step1), by a whole block.
-template <int D, typename T>
+template <int D, int NQ, typename T>
 __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request &rq, int b, int unit, int step0, int step1,
                                             unsigned char *smem) {
-    using Sh = AttendShape<D, T>;
-    constexpr int PARTS = Sh::PARTS, KS = D / 16, NT = D / 8;         // k steps of q.k, column tiles of p.v
+    using Sh = AttendShape<D, NQ, T>;
+    constexpr int PARTS = Sh::PARTS, KS = D / 16, MT = D / 16, R = 8 * NQ;            // k steps of k q^T, row tiles of v^T p^T
     PageInfo *info = reinterpret_cast<PageInfo *>(smem + Sh::BYTES);  // [kInfos + 1]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
-    const int hk = unit % p.Hkv, row0 = unit / p.Hkv * kRows, rows = rq.q_len * p.G;
+    const int hk = unit % p.Hkv, row0 = unit / p.Hkv * R, rows = rq.q_len * p.G;
     const int kv = rq.kv, behind = rq.behind;
-    const int last_row = min(row0 + kRows, rows) - 1;
+    const int last_row = min(row0 + R, rows) - 1;
     const int begin = step0 * kBlockStep;
     const int end = min(min(step1 * kBlockStep, kv), behind + last_row / p.G + 1);    // what some row of the tile sees
+    const int all_see = min(kv, behind + row0 / p.G + 1);             // what every row sees
 
-    // this lane's two rows of the tile, and their queries as A operands
-    int q_tok[2], seen[2];
-    float row_scale[2];
-    uint32_t qa[PARTS][KS][4];
+    // query g of each tile as B operands, and what belongs to the queries 2 j, 2 j + 1 of this lane's results
+    int seen[NQ][2];
+    float row_scale[NQ][2];
+    uint32_t qb[PARTS][NQ][KS][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = row0 + g + 8 * r;
+    for (int n = 0; n < NQ; ++n) {
+        const int row = row0 + 8 * n + g;
         const bool ok = row < rows;
-        q_tok[r] = row / p.G;
-        seen[r] = ok ? behind + q_tok[r] + 1 : 0;     // positions below this one
         float f[D / 4];
-        const int64_t off = (int64_t)(rq.first + q_tok[r]) * p.q_st + (int64_t)(hk * p.G + row % p.G) * p.q_sh + j * (D / 4);
+        const int64_t off = (int64_t)(rq.first + row / p.G) * p.q_st + (int64_t)(hk * p.G + row % p.G) * p.q_sh + j * (D / 4);
 #pragma unroll
         for (int v = 0; v < D / 4 / Vec<T>::n; ++v) {
             uint4 raw = make_uint4(0, 0, 0, 0);
@@ -198,24 +213,35 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
         // 2^ex <= top < 2^(ex + 1), or four times that at the type's end; rows of (almost) nothing stay as they are
         const int ex = top > 0x1p-100f && top < INFINITY ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
         const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        row_scale[r] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale * kLog2e;
+        const float scale = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale * kLog2e;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int mine = row0 + 8 * n + 2 * j + e;
+            row_scale[n][e] = __shfl_sync(0xffffffffu, scale, 4 * (2 * j + e));
+            seen[n][e] = mine < rows ? min(behind + mine / p.G + 1, kv) : 0;          // positions below this one
+        }
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const float x = f[4 * s + 2 * c] * down, y = f[4 * s + 2 * c + 1] * down;
                 const uint32_t hi = half2_bits(x, y);
-                qa[0][s][2 * c + r] = hi;
+                qb[0][n][s][c] = hi;
                 if (PARTS == 2) {
                     const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                    qa[PARTS - 1][s][2 * c + r] = half2_bits(x - back.x, y - back.y);
+                    qb[PARTS - 1][n][s][c] = half2_bits(x - back.x, y - back.y);
                 }
             }
     }
-    float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float acc[NT][4];
+    float M[NQ][2], l[NQ][2];
+    float acc[MT][NQ][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int n = 0; n < NQ; ++n) {
+        M[n][0] = M[n][1] = kLowest;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+    }
 
     unsigned char *ring = smem + warp * kStages * Sh::STAGE;
     const uint32_t ring_s = smem_u32(ring);
@@ -267,74 +293,91 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
         const int at = from + step * kStep;
         const PageInfo f = info[(at >> p.shift) - page0];
         if (f.page < 0) continue;
-        const bool zero_v = f.page & kZeroV;
 
-        float s[2][4];                                // scores: keys 2j, 2j+1 (+8) for rows g, g+8
+        // scores: tokens g (0, 1) and g + 8 (2, 3) for queries 2 j, 2 j + 1
+        float s[NQ][4];
+        {
+            uint32_t w[2][D / 16];                    // bytes j D/4 .. (j+1) D/4 of keys g, g + 8
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-            uint32_t w[D / 16];                       // bytes j D/4 .. (j+1) D/4 of key g + 8 t
-            const unsigned char *src = kb + (g + 8 * t) * D + j * (D / 4);
-            if (D >= 64) {
+            for (int t = 0; t < 2; ++t) {
+                const unsigned char *src = kb + (g + 8 * t) * D + j * (D / 4);
+                if (D >= 64) {
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const uint4 r = *reinterpret_cast<const uint4 *>(src + 16 * c);
-                    w[4 * c] = r.x; w[4 * c + 1] = r.y; w[4 * c + 2] = r.z; w[4 * c + 3] = r.w;
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint4 r = *reinterpret_cast<const uint4 *>(src + 16 * c);
+                        w[t][4 * c] = r.x; w[t][4 * c + 1] = r.y; w[t][4 * c + 2] = r.z; w[t][4 * c + 3] = r.w;
+                    }
+                } else {
+                    const uint2 r = *reinterpret_cast<const uint2 *>(src);
+                    w[t][0] = r.x; w[t][1] = r.y;
                 }
-            } else {
-                const uint2 r = *reinterpret_cast<const uint2 *>(src);
-                w[0] = r.x; w[1] = r.y;
             }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
-                const uint32_t x = w[c] ^ 0x80808080u, b0 = low_pair(x), b1 = high_pair(x);
+                const uint32_t x = w[0][c] ^ 0x80808080u, y = w[1][c] ^ 0x80808080u;
+                const uint32_t a[4] = {low_pair(x), low_pair(y), high_pair(x), high_pair(y)};
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(s[t], qa[part][c], b0, b1);
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(s[n], a, qb[part][n][c][0], qb[part][n][c][1]);
             }
         }
+        // exponents against the present M; NaN compares false and goes through
+        float c[NQ][2], t[NQ][4];
+        bool more = false;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int r = e >> 1, pos = at + 8 * t + 2 * j + (e & 1);
-                const float x = fmaf(s[t][e] * f.k, row_scale[r], f.lv);
-                s[t][e] = pos < seen[r] && pos < kv ? x : -INFINITY;
+                const int q = e & 1;
+                if (e < 2) c[n][q] = f.k * row_scale[n][q];
+                if (at + kStep > all_see && at + g + (e >> 1) * 8 >= seen[n][q]) s[n][e] = -INFINITY;
+                else s[n][e] = fmaf(s[n][e], c[n][q], f.lv);
+                more |= s[n][e] > M[n][q];
             }
-        float base[2], shrink[2];
+        if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float m = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            m = fmaxf(m, M[r]);
-            base[r] = m == -INFINITY ? 0.f : m;       // nothing seen yet: every exponential is 2^-inf = 0
-            shrink[r] = ex2(M[r] - base[r]);
-            M[r] = m;
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float m = fmaxf(M[n][q], fmaxf(s[n][q], s[n][q + 2]));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    const float shrink = ex2(M[n][q] - m);
+                    M[n][q] = m;
+                    l[n][q] *= shrink;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) { acc[i][n][q] *= shrink; acc[i][n][q + 2] *= shrink; }
+                }
         }
-        if (__any_sync(0xffffffffu, shrink[0] != 1.f || shrink[1] != 1.f)) {
+        uint32_t pb[PARTS][NQ][2];                    // p' 2^15 as the B operand
 #pragma unroll
-            for (int r = 0; r < 2; ++r) l[r] *= shrink[r];
+        for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                acc[i][0] *= shrink[0]; acc[i][1] *= shrink[0];
-                acc[i][2] *= shrink[1]; acc[i][3] *= shrink[1];
-            }
-        }
-        uint32_t pa[PARTS][4];                        // p' 2^15 as the A operand
+            for (int e = 0; e < 4; ++e) t[n][e] = ex2(s[n][e] - (M[n][e & 1] - 15.f));
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int q = 0; q < 2; ++q) l[n][q] = fmaf(t[n][q] + t[n][q + 2], f.iv, l[n][q]);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float x = ex2(s[t][2 * r] - base[r] + 15.f), y = ex2(s[t][2 * r + 1] - base[r] + 15.f);
-                l[r] = fmaf(x + y, f.iv, l[r]);
+            for (int h = 0; h < 2; ++h) {
+                const float x = t[n][2 * h], y = t[n][2 * h + 1];
                 const uint32_t hi = half2_bits(x, y);
-                pa[0][2 * t + r] = zero_v ? 0u : hi;
+                pb[0][n][h] = transposed(hi);
                 if (PARTS == 2) {
                     const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                    pa[PARTS - 1][2 * t + r] = zero_v ? 0u : half2_bits(x - back.x, y - back.y);
+                    pb[PARTS - 1][n][h] = transposed(half2_bits(x - back.x, y - back.y));
                 }
             }
-        // p.v: column n = l / 4 of tile i is d = (l / 4) D/8 + i
+        }
+        if (f.page & kZeroV) {                        // whatever the bytes are, the values are zero
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) pb[part][n][0] = pb[part][n][1] = 0u;
+        }
+        // v^T p^T: row g (g + 8) of tile i is d = g D/8 + 2 i (+ 1)
         constexpr int VB = D / 8;                     // bytes of a lane per value: 16, 8 or 4
         uint32_t v[4][VB / 4];
 #pragma unroll
@@ -351,69 +394,70 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
             }
         }
 #pragma unroll
-        for (int c = 0; c < VB / 4; ++c) {
-            // bytes 0, 1 (2, 3) of both values of a pair, interleaved
-            const uint32_t x01 = __byte_perm(v[0][c], v[1][c], 0x5140) ^ 0x80808080u, x23 = __byte_perm(v[0][c], v[1][c], 0x7362) ^ 0x80808080u;
-            const uint32_t y01 = __byte_perm(v[2][c], v[3][c], 0x5140) ^ 0x80808080u, y23 = __byte_perm(v[2][c], v[3][c], 0x7362) ^ 0x80808080u;
-            const uint32_t b0[4] = {low_pair(x01), high_pair(x01), low_pair(x23), high_pair(x23)};
-            const uint32_t b1[4] = {low_pair(y01), high_pair(y01), low_pair(y23), high_pair(y23)};
+        for (int c = 0; c < VB / 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int h = 0; h < 2; ++h) {             // bytes 0, 1 (2, 3) of both values of a pair, interleaved
+                const uint32_t sel = h ? 0x7362 : 0x5140;
+                const uint32_t x = __byte_perm(v[0][c], v[1][c], sel) ^ 0x80808080u, y = __byte_perm(v[2][c], v[3][c], sel) ^ 0x80808080u;
+                const uint32_t a[4] = {low_pair(x), high_pair(x), low_pair(y), high_pair(y)};
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(acc[4 * c + i], pa[part], b0[i], b1[i]);
-        }
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(acc[2 * c + h][n], a, pb[part][n][0], pb[part][n][1]);
+            }
         __syncwarp();                                 // the stage is read before it is filled again
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();                                  // infos and stages are free again
     }
 
-    // join the four warps: [warp][row][M, l, o...] in the ring's place
+    // join the four warps: [warp][row][M, l, -, -, o...] in the ring's place
     float *join = reinterpret_cast<float *>(smem);
+    constexpr int W = D + 4;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        float *to = join + (warp * kRows + g + 8 * r) * (D + 2);
-        if (j == 0) { to[0] = M[r]; to[1] = l[r]; }
-    }
-    // column 2 j + e of tile i stands for d = (2 j + e) D/8 + i
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+        for (int q = 0; q < 2; ++q) {
+            float sum = l[n][q];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            float *to = join + (warp * R + 8 * n + 2 * j + q) * W;
+            if (g == 0) *reinterpret_cast<float2 *>(to) = make_float2(M[n][q], sum);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            join[(warp * kRows + g + 8 * (e >> 1)) * (D + 2) + 2 + (2 * j + (e & 1)) * (D / 8) + i] = acc[i][e];
+            for (int i = 0; i < MT; ++i)
+                *reinterpret_cast<float2 *>(to + 4 + g * (D / 8) + 2 * i) = make_float2(acc[i][n][q], acc[i][n][q + 2]);
+        }
     __syncthreads();
-    for (int e = tid; e < kRows * D; e += 32 * kWarps) {
-        const int r = e / D, d = e % D, row = row0 + r;
+    for (int e = tid; e < R * D / 4; e += 32 * kWarps) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4, row = row0 + r;
         if (row >= rows) continue;
-        const float *from = join + r * (D + 2);
-        float m = -INFINITY;
+        const float *from = join + r * W;
+        float m = kLowest;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, from[w * kRows * (D + 2)]);
-        const float at = m == -INFINITY ? 0.f : m;
-        float sum = 0.f, o = 0.f;
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, from[w * R * W]);
+        float sum = 0.f;
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(from[w * kRows * (D + 2)] - at);
-            sum = fmaf(f, from[w * kRows * (D + 2) + 1], sum);
-            o = fmaf(f, from[w * kRows * (D + 2) + 2 + d], o);
+            const float f = ex2(from[w * R * W] - m);
+            const float4 x = *reinterpret_cast<const float4 *>(from + w * R * W + 4 + d);
+            sum = fmaf(f, from[w * R * W + 1], sum);
+            o[0] = fmaf(f, x.x, o[0]); o[1] = fmaf(f, x.y, o[1]); o[2] = fmaf(f, x.z, o[2]); o[3] = fmaf(f, x.w, o[3]);
         }
         if (step0 > 0 || step1 < rq.steps) {          // a part: of a unit begun before (0) or going on after (1)
             const int64_t slot = 2 * (int64_t)blockIdx.x + (step0 > 0 ? 0 : 1);
-            p.part[(slot * kRows + r) * D + d] = o;
-            if (d == 0) *reinterpret_cast<float2 *>(p.ml + (slot * kRows + r) * 2) = make_float2(m, sum);
+            *reinterpret_cast<float4 *>(p.part + (slot * R + r) * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+            if (d == 0) *reinterpret_cast<float2 *>(p.ml + (slot * R + r) * 2) = make_float2(m, sum);
         } else {
-            const int64_t off = (int64_t)(rq.first + row / p.G) * p.o_st + (int64_t)(hk * p.G + row % p.G) * p.o_sh + d;
-            const float y = sum == 0.f ? 0.f : o / sum;
-            if (in_bounds(off, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off] = Cvt<T>::from_f(y);
+            put_row<T>(p, rq.first + row / p.G, hk * p.G + row % p.G, d, o, sum);
         }
     }
     __syncthreads();                                  // the ring is free again
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(32 * kWarps, AttendBlocks<D, T>::value) cache_attend_kernel(const AttendParams p) {
+template <int D, int NQ, typename T>
+__global__ void __launch_bounds__(32 * kWarps, AttendShape<D, NQ, T>::BLOCKS) cache_attend_kernel(const AttendParams p) {
     constexpr int NT = 32 * kWarps;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int64_t s_sum[NT / 32];
@@ -443,7 +487,7 @@ __global__ void __launch_bounds__(32 * kWarps, AttendBlocks<D, T>::value) cache_
         while (at < all && left > 0) {
             const int unit = (int)(at / r.steps), step0 = (int)(at % r.steps);
             const int step1 = (int)min((int64_t)r.steps, step0 + left);
-            attend_unit<D, T>(p, r, b, unit, step0, step1, smem);
+            attend_unit<D, NQ, T>(p, r, b, unit, step0, step1, smem);
             at += step1 - step0;
             left -= step1 - step0;
         }
@@ -462,8 +506,8 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) cache_join_ke
     const int b = blockIdx.z, unit = blockIdx.x, lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const Request rq = request(p, b);
     const int r = blockIdx.y * kJoinRows + lane / (D / 4), d = lane % (D / 4) * 4;
-    const int row = unit / p.Hkv * kRows + r, rows = rq.q_len * p.G;
-    if (unit >= rq.units || unit / p.Hkv * kRows + (int)blockIdx.y * kJoinRows >= rows) return;
+    const int row = unit / p.Hkv * p.tile + r, rows = rq.q_len * p.G;
+    if (unit >= rq.units || unit / p.Hkv * p.tile + (int)blockIdx.y * kJoinRows >= rows) return;
     const Share share = share_of<NT>(p, s_sum);
     int64_t before = 0;
     for (int i = threadIdx.x; i < b; i += NT) {
@@ -473,15 +517,14 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) cache_join_ke
     const int64_t at = block_sum<NT>(before, s_sum) + (int64_t)unit * rq.steps;
     const int64_t first = at / share.size, last = (at + rq.steps - 1) / share.size;
     if (first == last) return;                        // written out by its one block
-    float m = -INFINITY, sum = 0.f;
+    float m = kLowest, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int64_t c = first + group; c <= last; c += kJoinGroups) {
         const int64_t slot = 2 * c + (c == first ? 1 : 0);
-        const float2 ml = *reinterpret_cast<const float2 *>(p.ml + (slot * kRows + r) * 2);
-        const float4 x = *reinterpret_cast<const float4 *>(p.part + (slot * kRows + r) * D + d);
-        const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
-        const float keep = ex2(m - base), add = ex2(ml.x - base);
+        const float2 ml = *reinterpret_cast<const float2 *>(p.ml + (slot * p.tile + r) * 2);
+        const float4 x = *reinterpret_cast<const float4 *>(p.part + (slot * p.tile + r) * D + d);
+        const float top = fmaxf(m, ml.x), keep = ex2(m - top), add = ex2(ml.x - top);
         sum = fmaf(add, ml.y, sum * keep);
         o.x = fmaf(add, x.x, o.x * keep); o.y = fmaf(add, x.y, o.y * keep);
         o.z = fmaf(add, x.z, o.z * keep); o.w = fmaf(add, x.w, o.w * keep);
@@ -491,55 +534,57 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) cache_join_ke
     s_ml[group][lane] = make_float2(m, sum);
     __syncthreads();
     if (group != 0 || row >= rows) return;
-    m = -INFINITY;
+    m = kLowest;
 #pragma unroll
     for (int i = 0; i < kJoinGroups; ++i) m = fmaxf(m, s_ml[i][lane].x);
-    const float base = m == -INFINITY ? 0.f : m;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kJoinGroups; ++i) {
-        const float f = ex2(s_ml[i][lane].x - base);
+        const float f = ex2(s_ml[i][lane].x - m);
         const float4 x = s_o[i][lane];
         sum = fmaf(f, s_ml[i][lane].y, sum);
         v[0] = fmaf(f, x.x, v[0]); v[1] = fmaf(f, x.y, v[1]); v[2] = fmaf(f, x.z, v[2]); v[3] = fmaf(f, x.w, v[3]);
     }
-    const int64_t off = (int64_t)(rq.first + row / p.G) * p.o_st + (int64_t)(unit % p.Hkv * p.G + row % p.G) * p.o_sh + d;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (in_bounds(off + e, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off + e] = Cvt<T>::from_f(sum == 0.f ? 0.f : v[e] / sum);
+    put_row<T>(p, rq.first + row / p.G, unit % p.Hkv * p.G + row % p.G, d, v, sum);
 }
 
+// Rows of a tile: eight where that holds all of a request's.
+int tile_of(const cgdr_attend_args &a) {
+    const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
+    return rows <= 8 ? 8 : 16;
+}
+int64_t most_of(const cgdr_attend_args &a) {
+    return a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page;
+}
 // Blocks of the first kernel: all that fit, but no more than shares of kMinShare steps need.
-template <int D, typename T>
+template <int D, int NQ, typename T>
 int blocks_of(const cgdr_attend_args &a) {
     const int64_t sms = device_sms() > 0 ? device_sms() : 152;       // sizes workspaces without a device, too
-    const int64_t units = (int64_t)a.B * a.Hkv * (((int64_t)a.max_q * (a.Hq / a.Hkv) + kRows - 1) / kRows);
-    const int64_t kv = a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page;
-    const int64_t steps = kv > 0 ? (kv + kBlockStep - 1) / kBlockStep : 1, most = sms * AttendBlocks<D, T>::value;
-    const int64_t need = (units * steps + kMinShare - 1) / kMinShare;
+    const int64_t tiles = ((int64_t)a.max_q * (a.Hq / a.Hkv) + 8 * NQ - 1) / (8 * NQ), kv = most_of(a);
+    const int64_t steps = kv > 0 ? (kv + kBlockStep - 1) / kBlockStep : 1, most = sms * AttendShape<D, NQ, T>::BLOCKS;
+    const int64_t need = ((int64_t)a.B * a.Hkv * tiles * steps + kMinShare - 1) / kMinShare;
     return (int)(need < most ? need : most);
 }
-template <int D, typename T>
+template <int D, int NQ, typename T>
 size_t workspace_for(const cgdr_attend_args &a) {
-    const int blocks = blocks_of<D, T>(a);
-    return blocks > 1 ? (size_t)2 * blocks * kRows * (D + 2) * sizeof(float) : 0;
+    const int blocks = blocks_of<D, NQ, T>(a);
+    return blocks > 1 ? (size_t)2 * blocks * 8 * NQ * (D + 2) * sizeof(float) : 0;
 }
 
-template <int D, typename T>
+template <int D, int NQ, typename T>
 cgdr_status launch_attend(const cgdr_attend_args &a, AttendParams &p, float *ws, cudaStream_t s) {
-    using Sh = AttendShape<D, T>;
+    using Sh = AttendShape<D, NQ, T>;
     static SmemOnce smem_once;
     constexpr int kBytes = Sh::BYTES + (kInfos + 1) * (int)sizeof(PageInfo);
-    if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_kernel<D, T>), kBytes)) return CGDR_ERR_CUDA;
-    p.blocks = blocks_of<D, T>(a);
+    if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_kernel<D, NQ, T>), kBytes)) return CGDR_ERR_CUDA;
+    p.blocks = blocks_of<D, NQ, T>(a);
     p.part = ws;
-    p.ml = ws + (size_t)2 * p.blocks * kRows * D;
-    cache_attend_kernel<D, T><<<p.blocks, 32 * kWarps, kBytes, s>>>(p);
+    p.ml = ws + (size_t)2 * p.blocks * p.tile * D;
+    cache_attend_kernel<D, NQ, T><<<p.blocks, 32 * kWarps, kBytes, s>>>(p);
     if (p.blocks > 1) {
         if (cudaPeekAtLastError() != cudaSuccess) return launched();
-        const int64_t tiles = ((int64_t)a.max_q * p.G + kRows - 1) / kRows;
-        const int64_t rows = (int64_t)a.max_q * p.G < kRows ? (int64_t)a.max_q * p.G : kRows;
+        const int64_t all = (int64_t)a.max_q * p.G, tiles = (all + p.tile - 1) / p.tile, rows = all < p.tile ? all : p.tile;
         cache_join_kernel<D, T><<<dim3((unsigned)(tiles * a.Hkv), (unsigned)((rows + kJoinRows - 1) / kJoinRows), a.B),
                                   kJoinRows * kJoinGroups * D / 4, 0, s>>>(p);
     }
@@ -547,16 +592,19 @@ cgdr_status launch_attend(const cgdr_attend_args &a, AttendParams &p, float *ws,
 }
 
 #define CGDR_ATTEND_CASES(CALL) \
-    if (a.dtype == CGDR_BF16) \
-        return a.D == 128 ? CALL(128, __nv_bfloat16) : a.D == 64 ? CALL(64, __nv_bfloat16) : CALL(32, __nv_bfloat16); \
-    return a.D == 128 ? CALL(128, float) : a.D == 64 ? CALL(64, float) : CALL(32, float);
+    if (a.dtype == CGDR_BF16) { \
+        if (tile_of(a) == 8) return a.D == 128 ? CALL(128, 1, __nv_bfloat16) : a.D == 64 ? CALL(64, 1, __nv_bfloat16) : CALL(32, 1, __nv_bfloat16); \
+        return a.D == 128 ? CALL(128, 2, __nv_bfloat16) : a.D == 64 ? CALL(64, 2, __nv_bfloat16) : CALL(32, 2, __nv_bfloat16); \
+    } \
+    if (tile_of(a) == 8) return a.D == 128 ? CALL(128, 1, float) : a.D == 64 ? CALL(64, 1, float) : CALL(32, 1, float); \
+    return a.D == 128 ? CALL(128, 2, float) : a.D == 64 ? CALL(64, 2, float) : CALL(32, 2, float);
 size_t workspace_of(const cgdr_attend_args &a) {
-#define CGDR_CALL(D, T) workspace_for<D, T>(a)
+#define CGDR_CALL(D, NQ, T) workspace_for<D, NQ, T>(a)
     CGDR_ATTEND_CASES(CGDR_CALL)
 #undef CGDR_CALL
 }
 cgdr_status launch_of(const cgdr_attend_args &a, AttendParams &p, float *ws, cudaStream_t s) {
-#define CGDR_CALL(D, T) launch_attend<D, T>(a, p, ws, s)
+#define CGDR_CALL(D, NQ, T) launch_attend<D, NQ, T>(a, p, ws, s)
     CGDR_ATTEND_CASES(CGDR_CALL)
 #undef CGDR_CALL
 }
@@ -603,7 +651,7 @@ cgdr_status cgdr_cache_attend(const cgdr_attend_args *a, void *ws, size_t ws_byt
     AttendParams p{};
     p.B = a->B; p.n = a->n; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = a->Hq / a->Hkv; p.page = a->page; p.shift = __builtin_ctz(a->page); p.width = a->width;
     p.num_pages = a->num_pages; p.max_q = a->max_q;
-    p.most = (int)(a->max_kv < (int64_t)a->width * a->page ? a->max_kv : (int64_t)a->width * a->page);
+    p.most = (int)most_of(*a); p.tile = tile_of(*a);
     p.scale = a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->D);
     p.q = a->q; p.q_st = a->q_st; p.q_sh = a->q_sh; p.o = a->o; p.o_st = a->o_st; p.o_sh = a->o_sh;
     p.eq = extent3(a->n, a->q_st, a->Hq, a->q_sh, a->D); p.eo = extent3(a->n, a->o_st, a->Hq, a->o_sh, a->D);
