@@ -18,12 +18,13 @@
 //
 // The scales stay out of the products: k's multiplies the score; v's becomes part of the exponent,
 // p' = 2^(s + log2 vs - M), with its own running maximum M of s + log2 vs, so that p' lies in (0, 1]
-// whatever the scales are and fits fp16; the denominator adds p' / vs.  A further 2^15 keeps small
-// p' out of fp16's subnormal range (they lose their relative accuracy below 2^-29 of the largest).
-// M is only looked for, over the lanes, when some score passes it: a vote a step instead of shuffles.
+// whatever the scales are and fits fp16; the denominator adds p' / vs.  M follows the maximum loosely:
+// it is only looked for, over the lanes, when some score passes it by more than 2^7, which after the
+// first step is rare, and a vote otherwise.  p' is carried times 2^8: it stays below 2^15 even so,
+// and keeps fp16's relative accuracy down to 2^-22 of the largest (2^-33 of it is where it ends).
 //
 // Lengths differ, so the work is not cut by request: a unit is (request, row tile, key-value head), its
-// cost the 64-token steps of its cache, and every block takes an equal share of the steps of all
+// cost the 128-token steps of its cache, and every block takes an equal share of the steps of all
 // units in a row.  A unit that one block has from end to end it writes out; of the others each block
 // leaves a part (maximum, denominator, weighted sum), at most two of them, one for a unit that
 // began before its share and one for a unit that goes on after it, and a second kernel joins a unit's parts.
@@ -38,13 +39,20 @@
 namespace cgdr {
 namespace {
 
+#ifndef AB
+#define AB 4
+#endif
+#ifndef MMAV
+#define MMAV
+#endif
 constexpr int kWarps = 4;
 constexpr int kRows = 16;                             // rows of a tile at most
-constexpr int kStep = 16;                             // cached tokens of a warp's step
-constexpr int kStages = 3;
+constexpr int kHalf = 16, kStep = 2 * kHalf;          // cached tokens of a product's tile, and of a warp's step
+constexpr int kStages = 2;
 constexpr float kLowest = -3e38f;                     // below every score: M before there is one
+constexpr float kUp = 8.f, kMost = 15.f;              // p' is carried times 2^kUp and stays below 2^kMost
 constexpr int kBlockStep = kWarps * kStep;            // cached tokens of a block's step: the scheduling unit
-constexpr int kMinShare = 4;                          // steps of a block's share at least: joining costs about as much
+constexpr int kMinShare = 2;                          // steps of a block's share at least: joining costs about as much
 constexpr int kInfos = 320;                           // pages whose numbers and scales a block holds at a time
 
 struct AttendParams {
@@ -120,7 +128,7 @@ __device__ __forceinline__ void report(int *status, int code) {
 }
 
 __device__ __forceinline__ void mma_f16_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm MMAV(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -140,11 +148,11 @@ __device__ __forceinline__ uint32_t low_pair(uint32_t w) { return less_bias(__by
 __device__ __forceinline__ uint32_t high_pair(uint32_t w) { return less_bias(__byte_perm(w, 0x64646464u, 0x4342)); }
 
 // What a block holds of a page, in 16 bytes.
-constexpr int kZeroV = 1 << 30;                       // flag in `page`: v's scale is (as good as) zero, and so are the values
 struct PageInfo {
     int page;                                         // -1: outside the cache
     float k;                                          // k's scale
-    float lv, iv;                                     // log2 and reciprocal of v's scale; 0 and 1 with kZeroV
+    float lv, iv;                                     // log2 and reciprocal of v's scale; 0 and -1 where that is (as good
+                                                      // as) zero, and so are the values
 };
 
 template <int D, int NQ, typename T>
@@ -154,7 +162,7 @@ struct AttendShape {                                                  // NQ: til
     static constexpr int RING = kWarps * kStages * STAGE;
     static constexpr int JOIN = kWarps * 8 * NQ * (D + 4) * 4;        // the warps' softmax states, in the ring's place
     static constexpr int BYTES = RING > JOIN ? RING : JOIN;
-    static constexpr int BLOCKS = (D == 128 ? 5 : 6) - NQ - (sizeof(T) == 4 ? 1 : 0); // of an SM, by shared memory and registers
+    static constexpr int BLOCKS = (D == 128 ? AB : 6) - NQ - (sizeof(T) == 4 ? 1 : 0); // of an SM, by shared memory and registers
 };
 
 // Four values of a row of o from a weighted sum and its denominator; a row that saw nothing is zero.
@@ -169,9 +177,17 @@ __device__ __forceinline__ void put_row(const AttendParams &p, int tok, int head
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {          // an 8 x 8 tile of fp16 over the warp
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+
+// Where a 16-byte piece of a 128-byte line of a stage is kept: its number xor this.  A quarter of a warp
+// reads the keys of two tokens (every other piece of two lines) or the values of four pairs (two pieces
+// of every other line): without it those meet the same banks two and four times.
+template <int D>
+__device__ __forceinline__ int k_swizzle(int line) { return D == 128 ? line & 1 : 0; }
+template <int D>
+__device__ __forceinline__ int v_swizzle(int line) { return D == 128 ? line & 6 : D == 64 ? (line & 3) << 1 : 0; }
 
 // One unit's steps [step0, step1), by a whole block.
 template <int D, int NQ, typename T>
@@ -188,23 +204,99 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
     const int end = min(min(step1 * kBlockStep, kv), behind + last_row / p.G + 1);    // what some row of the tile sees
     const int all_see = min(kv, behind + row0 / p.G + 1);             // what every row sees
 
+    // the queries' bytes first: they arrive while the pages are looked up
+    uint4 raw[NQ][D / 4 / Vec<T>::n];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int row = row0 + 8 * n + g;
+        const int64_t off = (int64_t)(rq.first + row / p.G) * p.q_st + (int64_t)(hk * p.G + row % p.G) * p.q_sh + j * (D / 4);
+#pragma unroll
+        for (int v = 0; v < D / 4 / Vec<T>::n; ++v) {
+            raw[n][v] = make_uint4(0, 0, 0, 0);
+            if (row < rows && range_in_bounds(off + v * Vec<T>::n, Vec<T>::n, p.eq, p.status, nullptr))
+                raw[n][v] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + off) + v);
+        }
+    }
+    unsigned char *ring = smem + warp * kStages * Sh::STAGE;
+    const uint32_t ring_s = smem_u32(ring);
+    const int span = kInfos * p.page;                  // cached tokens whose pages are held at a time
+    // the pages of `span` tokens from `from` on, and the copies of the warp's first steps among them
+    int steps = 0, page0 = 0, from = begin;
+    auto issue = [&](int step, int stage) {           // copies of a step's 16 keys and 16 values
+        if (step < steps) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int at = from + step * kStep + u * kHalf, page = info[(at >> p.shift) - page0].page;
+                if (page >= 0) {
+                    const int64_t src = ((((int64_t)page * p.Hkv + hk) << p.shift) + (at & (p.page - 1))) * D + lane * 16;
+                    const uint32_t dst = ring_s + stage * Sh::STAGE + 2 * u * kHalf * D;
+#pragma unroll
+                    for (int c = 0; c < kHalf * D / 16 / 32; ++c) {
+                        const int line = 4 * c + (lane >> 3), piece = lane & 7;
+                        cp_async16(dst + line * 128 + (piece ^ k_swizzle<D>(line)) * 16, p.kc + src + c * 512, true);
+                        cp_async16(dst + kHalf * D + line * 128 + (piece ^ v_swizzle<D>(line)) * 16, p.vc + src + c * 512, true);
+                    }
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    // Page numbers first, so that the copies can start; the scales are on their way meanwhile, and what is
+    // made of them follows with ready().
+    constexpr int kOf = (kInfos + 32 * kWarps) / (32 * kWarps);       // pages of a thread
+    int last = 0;
+    float ks[kOf], vs[kOf];
+    auto open = [&]() {
+        steps = (max(min(end - from, span), 0) + kStep - 1) / kStep;
+        page0 = from >> p.shift;
+        last = ((from + steps * kStep - 1) >> p.shift) - page0;
+#pragma unroll
+        for (int r = 0; r < kOf; ++r) {
+            const int i = tid + r * 32 * kWarps;
+            ks[r] = 0.f;
+            vs[r] = 0.f;
+            if (i <= last) {
+                const int64_t at = b * p.table_sb + page0 + i;
+                const bool held = (page0 + i) << p.shift < end;      // the last step may reach past the request's pages
+                int page = held && in_bounds(at, p.e_table, p.status, nullptr) ? p.table[at] : -1;
+                if (page < 0 || page >= p.num_pages) {
+                    if (held) report(p.status, (int)CGDR_ERR_BOUNDS);
+                    page = -1;
+                } else {
+                    ks[r] = __ldg(p.ks + (int64_t)page * p.Hkv + hk);
+                    vs[r] = __ldg(p.vs + (int64_t)page * p.Hkv + hk);
+                }
+                info[i].page = page;
+            }
+        }
+        __syncthreads();
+        issue(warp, 0);
+        issue(warp + kWarps, 1);
+    };
+    auto ready = [&]() {
+#pragma unroll
+        for (int r = 0; r < kOf; ++r) {
+            const int i = tid + r * 32 * kWarps;
+            if (i <= last) {
+                const bool zero = vs[r] < 0x1p-100f;  // not so for a NaN, which then spreads as it has to
+                info[i].k = ks[r];
+                info[i].lv = zero ? 0.f : log2f(vs[r]);
+                info[i].iv = zero ? -1.f : 1.f / vs[r];
+            }
+        }
+        __syncthreads();
+    };
+    open();
+
     // query g of each tile as B operands, and what belongs to the queries 2 j, 2 j + 1 of this lane's results
     int seen[NQ][2];
     float row_scale[NQ][2];
     uint32_t qb[PARTS][NQ][KS][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        const int row = row0 + 8 * n + g;
-        const bool ok = row < rows;
         float f[D / 4];
-        const int64_t off = (int64_t)(rq.first + row / p.G) * p.q_st + (int64_t)(hk * p.G + row % p.G) * p.q_sh + j * (D / 4);
 #pragma unroll
-        for (int v = 0; v < D / 4 / Vec<T>::n; ++v) {
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (ok && range_in_bounds(off + v * Vec<T>::n, Vec<T>::n, p.eq, p.status, nullptr))
-                raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + off) + v);
-            Vec<T>::unpack(raw, f + v * Vec<T>::n);
-        }
+        for (int v = 0; v < D / 4 / Vec<T>::n; ++v) Vec<T>::unpack(raw[n][v], f + v * Vec<T>::n);
         float top = 0.f;
 #pragma unroll
         for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(f[e]));
@@ -243,77 +335,43 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
         for (int i = 0; i < MT; ++i) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
     }
 
-    unsigned char *ring = smem + warp * kStages * Sh::STAGE;
-    const uint32_t ring_s = smem_u32(ring);
-    const int span = kInfos * p.page;                 // cached tokens whose pages are held at a time
-    for (int from = begin; from < end; from += span) {
-    const int steps = (min(end - from, span) + kStep - 1) / kStep;
-    const int page0 = from >> p.shift;
-    for (int i = tid; i <= ((from + steps * kStep - 1) >> p.shift) - page0; i += 32 * kWarps) {
-        PageInfo f{-1, 0.f, 0.f, 1.f};
-        const int64_t at = b * p.table_sb + page0 + i;
-        const int page = in_bounds(at, p.e_table, p.status, nullptr) ? p.table[at] : -1;
-        if (page < 0 || page >= p.num_pages) {
-            report(p.status, (int)CGDR_ERR_BOUNDS);
-        } else {
-            f.page = page;
-            f.k = p.ks[(int64_t)page * p.Hkv + hk];
-            const float v = p.vs[(int64_t)page * p.Hkv + hk];
-            if (v < 0x1p-100f) f.page |= kZeroV;      // not so for a NaN, which then spreads as it has to
-            else { f.lv = log2f(v); f.iv = 1.f / v; }
-        }
-        info[i] = f;
-    }
-    __syncthreads();
-
-    auto issue = [&](int step, int stage) {           // copies of a step's 16 keys and 16 values
-        if (step < steps) {
-            const int at = from + step * kStep, page = info[(at >> p.shift) - page0].page;
-            if (page >= 0) {
-                const int64_t src = ((((int64_t)(page & ~kZeroV) * p.Hkv + hk) << p.shift) + (at & (p.page - 1))) * D;
-#pragma unroll
-                for (int c = 0; c < kStep * D / 16 / 32; ++c) {
-                    const int e = (c * 32 + lane) * 16;
-                    cp_async16(ring_s + stage * Sh::STAGE + e, p.kc + src + e, true);
-                    cp_async16(ring_s + stage * Sh::STAGE + kStep * D + e, p.vc + src + e, true);
-                }
-            }
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue(warp + s * kWarps, s);
+    ready();
+    while (true) {
     int stage = 0;
     for (int step = warp; step < steps; step += kWarps) {
-        issue(step + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncwarp();                                 // every lane's copies have landed
-        const unsigned char *kb = ring + stage * Sh::STAGE, *vb = kb + kStep * D;
-        stage = stage == kStages - 1 ? 0 : stage + 1;
-        const int at = from + step * kStep;
-        const PageInfo f = info[(at >> p.shift) - page0];
-        if (f.page < 0) continue;
+        const unsigned char *bytes = ring + stage * Sh::STAGE;
+        PageInfo f[2];
+        int at[2];                                    // of what lies outside the cache: a position that no row sees
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            at[u] = from + step * kStep + u * kHalf;
+            f[u] = info[(at[u] >> p.shift) - page0];
+            if (f[u].page < 0) at[u] = INT32_MAX - kHalf;
+        }
 
-        // scores: tokens g (0, 1) and g + 8 (2, 3) for queries 2 j, 2 j + 1
-        float s[NQ][4];
-        {
+        // scores: tokens g (0, 1) and g + 8 (2, 3) of each half for queries 2 j, 2 j + 1
+        float s[2][NQ][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
             uint32_t w[2][D / 16];                    // bytes j D/4 .. (j+1) D/4 of keys g, g + 8
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const unsigned char *src = kb + (g + 8 * t) * D + j * (D / 4);
+                const unsigned char *src = bytes + (2 * u * kHalf + g + 8 * t) * D;
                 if (D >= 64) {
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
-                        const uint4 r = *reinterpret_cast<const uint4 *>(src + 16 * c);
+                        const uint4 r = *reinterpret_cast<const uint4 *>(src + (((D / 64) * j + c) ^ k_swizzle<D>(g)) * 16);
                         w[t][4 * c] = r.x; w[t][4 * c + 1] = r.y; w[t][4 * c + 2] = r.z; w[t][4 * c + 3] = r.w;
                     }
                 } else {
-                    const uint2 r = *reinterpret_cast<const uint2 *>(src);
+                    const uint2 r = *reinterpret_cast<const uint2 *>(src + 8 * j);
                     w[t][0] = r.x; w[t][1] = r.y;
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            for (int n = 0; n < NQ; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
 #pragma unroll
             for (int c = 0; c < KS; ++c) {
                 const uint32_t x = w[0][c] ^ 0x80808080u, y = w[1][c] ^ 0x80808080u;
@@ -321,28 +379,48 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(s[n], a, qb[part][n][c][0], qb[part][n][c][1]);
+                    for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(s[u][n], a, qb[part][n][c][0], qb[part][n][c][1]);
             }
         }
-        // exponents against the present M; NaN compares false and goes through
-        float c[NQ][2], t[NQ][4];
-        bool more = false;
+        // p' = 2^d, d = s + log2 vs - (M - kUp); a NaN compares false and goes through
+        float d[2][NQ][4];
+        auto exponents = [&]() {
+            bool more = false;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+            for (int u = 0; u < 2; ++u) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int q = e & 1;
-                if (e < 2) c[n][q] = f.k * row_scale[n][q];
-                if (at + kStep > all_see && at + g + (e >> 1) * 8 >= seen[n][q]) s[n][e] = -INFINITY;
-                else s[n][e] = fmaf(s[n][e], c[n][q], f.lv);
-                more |= s[n][e] > M[n][q];
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float c = f[u].k * row_scale[n][q], base = f[u].lv - (M[n][q] - kUp);
+#pragma unroll
+                        for (int e = q; e < 4; e += 2) d[u][n][e] = fmaf(s[u][n][e], c, base);
+                    }
+                if (at[u] + kHalf > all_see) {
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (at[u] + g + (e >> 1) * 8 >= seen[n][e & 1]) d[u][n][e] = -INFINITY;
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) more |= d[u][n][e] > kMost;
             }
-        if (__any_sync(0xffffffffu, more)) {
+            return more;
+        };
+        if (__any_sync(0xffffffffu, exponents())) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    float m = fmaxf(M[n][q], fmaxf(s[n][q], s[n][q + 2]));
+                    float m = M[n][q];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int e = q; e < 4; e += 2)
+                            if (at[u] + g + (e >> 1) * 8 < seen[n][q]) m = fmaxf(m, fmaf(s[u][n][e], f[u].k * row_scale[n][q], f[u].lv));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -352,63 +430,77 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
 #pragma unroll
                     for (int i = 0; i < MT; ++i) { acc[i][n][q] *= shrink; acc[i][n][q + 2] *= shrink; }
                 }
+            exponents();
         }
-        uint32_t pb[PARTS][NQ][2];                    // p' 2^15 as the B operand
+        uint32_t pb[2][PARTS][NQ][2];                 // p' 2^kUp as B operands
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[n][e] = ex2(s[n][e] - (M[n][e & 1] - 15.f));
+            for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) l[n][q] = fmaf(t[n][q] + t[n][q + 2], f.iv, l[n][q]);
+                for (int e = 0; e < 4; ++e) d[u][n][e] = ex2(d[u][n][e]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float x = t[n][2 * h], y = t[n][2 * h + 1];
-                const uint32_t hi = half2_bits(x, y);
-                pb[0][n][h] = transposed(hi);
-                if (PARTS == 2) {
-                    const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                    pb[PARTS - 1][n][h] = transposed(half2_bits(x - back.x, y - back.y));
+                for (int q = 0; q < 2; ++q) l[n][q] = fmaf(d[u][n][q] + d[u][n][q + 2], fabsf(f[u].iv), l[n][q]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float x = d[u][n][2 * h], y = d[u][n][2 * h + 1];
+                    const uint32_t hi = half2_bits(x, y);
+                    pb[u][0][n][h] = transposed(hi);
+                    if (PARTS == 2) {
+                        const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                        pb[u][PARTS - 1][n][h] = transposed(half2_bits(x - back.x, y - back.y));
+                    }
                 }
             }
-        }
-        if (f.page & kZeroV) {                        // whatever the bytes are, the values are zero
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) pb[part][n][0] = pb[part][n][1] = 0u;
-        }
-        // v^T p^T: row g (g + 8) of tile i is d = g D/8 + 2 i (+ 1)
-        constexpr int VB = D / 8;                     // bytes of a lane per value: 16, 8 or 4
-        uint32_t v[4][VB / 4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const unsigned char *src = vb + (2 * j + (t & 1) + 8 * (t >> 1)) * D + g * VB;
-            if (VB == 16) {
-                const uint4 r = *reinterpret_cast<const uint4 *>(src);
-                v[t][0] = r.x; v[t][VB / 4 > 1 ? 1 : 0] = r.y; v[t][VB / 4 > 2 ? 2 : 0] = r.z; v[t][VB / 4 > 3 ? 3 : 0] = r.w;
-            } else if (VB == 8) {
-                const uint2 r = *reinterpret_cast<const uint2 *>(src);
-                v[t][0] = r.x; v[t][VB / 4 > 1 ? 1 : 0] = r.y;
-            } else {
-                v[t][0] = *reinterpret_cast<const uint32_t *>(src);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < VB / 4; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {             // bytes 0, 1 (2, 3) of both values of a pair, interleaved
-                const uint32_t sel = h ? 0x7362 : 0x5140;
-                const uint32_t x = __byte_perm(v[0][c], v[1][c], sel) ^ 0x80808080u, y = __byte_perm(v[2][c], v[3][c], sel) ^ 0x80808080u;
-                const uint32_t a[4] = {low_pair(x), high_pair(x), low_pair(y), high_pair(y)};
+            if (f[u].iv < 0.f) {                      // whatever the bytes are, the values are zero
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(acc[2 * c + h][n], a, pb[part][n][0], pb[part][n][1]);
+                    for (int part = 0; part < PARTS; ++part) pb[u][part][n][0] = pb[u][part][n][1] = 0u;
             }
+        }
+        // v^T p^T: row g (g + 8) of tile i is d = g D/8 + 2 i (+ 1)
+        constexpr int VB = D / 8;                     // bytes of a lane per value: 16, 8 or 4
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t v[4][VB / 4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int row = 2 * j + (t & 1) + 8 * (t >> 1), at16 = row * D + g * VB;
+                const unsigned char *src = bytes + (2 * u + 1) * kHalf * D + (at16 ^ (v_swizzle<D>(at16 >> 7) * 16));
+                if (VB == 16) {
+                    const uint4 r = *reinterpret_cast<const uint4 *>(src);
+                    v[t][0] = r.x; v[t][VB / 4 > 1 ? 1 : 0] = r.y; v[t][VB / 4 > 2 ? 2 : 0] = r.z; v[t][VB / 4 > 3 ? 3 : 0] = r.w;
+                } else if (VB == 8) {
+                    const uint2 r = *reinterpret_cast<const uint2 *>(src);
+                    v[t][0] = r.x; v[t][VB / 4 > 1 ? 1 : 0] = r.y;
+                } else {
+                    v[t][0] = *reinterpret_cast<const uint32_t *>(src);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < VB / 4; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {         // bytes 0, 1 (2, 3) of both values of a pair, interleaved
+                    const uint32_t sel = h ? 0x7362 : 0x5140;
+                    const uint32_t x = __byte_perm(v[0][c], v[1][c], sel) ^ 0x80808080u, y = __byte_perm(v[2][c], v[3][c], sel) ^ 0x80808080u;
+                    const uint32_t a[4] = {low_pair(x), high_pair(x), low_pair(y), high_pair(y)};
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part) mma_f16_16x8x16(acc[2 * c + h][n], a, pb[u][part][n][0], pb[u][part][n][1]);
+                }
+        }
         __syncwarp();                                 // the stage is read before it is filled again
+        issue(step + 2 * kWarps, stage);
+        stage ^= 1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();                                  // infos and stages are free again
+    from += span;
+    if (from >= end) break;
+    open();
+    ready();
     }
 
     // join the four warps: [warp][row][M, l, -, -, o...] in the ring's place
@@ -459,28 +551,48 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
 template <int D, int NQ, typename T>
 __global__ void __launch_bounds__(32 * kWarps, AttendShape<D, NQ, T>::BLOCKS) cache_attend_kernel(const AttendParams p) {
     constexpr int NT = 32 * kWarps;
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int64_t s_sum[NT / 32];
+    extern __shared__ __align__(128) unsigned char smem[];              // copies of 512 bytes: misaligned to a line, each takes two
+    __shared__ int64_t s_sum[NT / 32], s_at;
+    __shared__ int s_b;
     const Share share = share_of<NT>(p, s_sum);
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.B; b += NT)
-            if (cut(p, b)) report(p.status, (int)CGDR_ERR_CAPACITY);
     int64_t left = share.size, at = share.size * blockIdx.x;          // steps to do, from this one of all on
-    if (at >= share.total) return;
     if (left > share.total - at) left = share.total - at;
-    int b = 0;
-    // the request of the first step: skip whole groups of NT requests, then single ones
-    for (int b0 = 0; b0 < p.B; b0 += NT) {
+    // the request of the first step, and the step in it: by prefix sums over groups of NT requests
+    if (threadIdx.x == 0) s_b = p.B;
+    for (int b0 = 0; left > 0 && b0 < p.B; b0 += NT) {
         int64_t mine = 0;
         if (b0 + threadIdx.x < p.B) {
             const Request r = request(p, b0 + threadIdx.x);
             mine = (int64_t)r.units * r.steps;
         }
-        const int64_t group = block_sum<NT>(mine, s_sum);
-        b = b0;
-        if (at < group) break;
+        int64_t upto = mine;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        __syncthreads();
+        if (lane == 31) s_sum[warp] = upto;
+        __syncthreads();
+        int64_t group = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < warp) upto += s_sum[w];
+            group += s_sum[w];
+        }
+        if (at < group) {
+            if (at < upto && at >= upto - mine) {
+                s_b = b0 + threadIdx.x;
+                s_at = at - (upto - mine);
+            }
+            break;
+        }
         at -= group;
     }
+    __syncthreads();
+    int b = s_b;
+    at = b < p.B ? s_at : 0;
     for (; b < p.B && left > 0; ++b) {
         const Request r = request(p, b);
         const int64_t all = (int64_t)r.units * r.steps;
@@ -493,7 +605,15 @@ __global__ void __launch_bounds__(32 * kWarps, AttendShape<D, NQ, T>::BLOCKS) ca
         }
         at = at > all ? at - all : 0;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < p.B; i += NT)
+            if (cut(p, i)) report(p.status, (int)CGDR_ERR_CAPACITY);
 }
+
+// Waits for the first kernel, whose end this one overlaps.  Every thread does before it returns, so that
+// what follows in the stream finds both kernels done.
+__device__ __forceinline__ void joined() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Joins the parts of a unit: four rows to a block, four groups of threads that take every fourth part.
 constexpr int kJoinRows = 4, kJoinGroups = 4;
@@ -507,7 +627,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) cache_join_ke
     const Request rq = request(p, b);
     const int r = blockIdx.y * kJoinRows + lane / (D / 4), d = lane % (D / 4) * 4;
     const int row = unit / p.Hkv * p.tile + r, rows = rq.q_len * p.G;
-    if (unit >= rq.units || unit / p.Hkv * p.tile + (int)blockIdx.y * kJoinRows >= rows) return;
+    if (unit >= rq.units || unit / p.Hkv * p.tile + (int)blockIdx.y * kJoinRows >= rows) return joined();
     const Share share = share_of<NT>(p, s_sum);
     int64_t before = 0;
     for (int i = threadIdx.x; i < b; i += NT) {
@@ -516,6 +636,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) cache_join_ke
     }
     const int64_t at = block_sum<NT>(before, s_sum) + (int64_t)unit * rq.steps;
     const int64_t first = at / share.size, last = (at + rq.steps - 1) / share.size;
+    joined();
     if (first == last) return;                        // written out by its one block
     float m = kLowest, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -585,8 +706,17 @@ cgdr_status launch_attend(const cgdr_attend_args &a, AttendParams &p, float *ws,
     if (p.blocks > 1) {
         if (cudaPeekAtLastError() != cudaSuccess) return launched();
         const int64_t all = (int64_t)a.max_q * p.G, tiles = (all + p.tile - 1) / p.tile, rows = all < p.tile ? all : p.tile;
-        cache_join_kernel<D, T><<<dim3((unsigned)(tiles * a.Hkv), (unsigned)((rows + kJoinRows - 1) / kJoinRows), a.B),
-                                  kJoinRows * kJoinGroups * D / 4, 0, s>>>(p);
+        // begins while the first kernel ends, finds its unit, and waits for that kernel's parts
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3((unsigned)(tiles * a.Hkv), (unsigned)((rows + kJoinRows - 1) / kJoinRows), a.B);
+        c.blockDim = dim3(kJoinRows * kJoinGroups * D / 4);
+        c.stream = s;
+        cudaLaunchAttribute early{};
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        c.attrs = &early;
+        c.numAttrs = 1;
+        if (cudaLaunchKernelEx(&c, cache_join_kernel<D, T>, p) != cudaSuccess) return launched();
     }
     return launched();
 }
@@ -616,7 +746,7 @@ cgdr_status check(const cgdr_attend_args *a) {
         a->max_q < 0 || a->max_kv < 0)
         return CGDR_ERR_INVALID_ARG;
     if (!dtype_ok(a->dtype) || !page_ok(a->page) || (a->D != 32 && a->D != 64 && a->D != 128)) return CGDR_ERR_UNSUPPORTED;
-    if (a->B > 65535 || a->n > kMaxTokens || a->max_kv > kMaxKv || a->num_pages > kZeroV) return CGDR_ERR_UNSUPPORTED;
+    if (a->B > 65535 || a->n > kMaxTokens || a->max_kv > kMaxKv) return CGDR_ERR_UNSUPPORTED;
     if (((int64_t)a->max_q * (a->Hq / a->Hkv) + kRows) * a->Hkv > INT32_MAX) return CGDR_ERR_UNSUPPORTED;
     if (a->B == 0 || a->n == 0 || a->max_q == 0) return CGDR_OK;
     if (!a->q || !a->o || !a->kv_lens || !a->cu) return CGDR_ERR_INVALID_ARG;
