@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libcgdr.so")
 OBJDIR_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libcgdr_debug.so")
 SOURCES = ["api.cu", "decode.cu", "prefill_simt.cu", "prefill_tc05.cu", "prefill_cluster.cu",
-           "conv.cu", "scan.cu", "cache_plan.cu", "cache_append.cu", "cache_attend.cu"]
+           "conv.cu", "scan.cu", "cache_plan.cu", "cache_append.cu", "cache_attend.cu",
+           "cache_attend_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -32,67 +32,18 @@
 // bf16 queries are scaled by a power of two per row to magnitudes below 2 and are then exact in fp16
 // down to 2^-14 of the row's largest (beyond that their error is below 2^-25 of it).  fp32 queries
 // and their probabilities are carried as two fp16 parts.
-#include "serve.cuh"
-
-#include <cuda_fp16.h>
+#include "cache_attend.cuh"
 
 namespace cgdr {
 namespace {
 
-#ifndef AB
-#define AB 4
-#endif
-#ifndef MMAV
-#define MMAV
-#endif
 constexpr int kWarps = 4;
 constexpr int kRows = 16;                             // rows of a tile at most
 constexpr int kHalf = 16, kStep = 2 * kHalf;          // cached tokens of a product's tile, and of a warp's step
 constexpr int kStages = 2;
-constexpr float kLowest = -3e38f;                     // below every score: M before there is one
-constexpr float kUp = 8.f, kMost = 15.f;              // p' is carried times 2^kUp and stays below 2^kMost
-constexpr int kBlockStep = kWarps * kStep;            // cached tokens of a block's step: the scheduling unit
+static_assert(kBlockStep == kWarps * kStep, "a block's step");
 constexpr int kMinShare = 2;                          // steps of a block's share at least: joining costs about as much
 constexpr int kInfos = 320;                           // pages whose numbers and scales a block holds at a time
-
-struct AttendParams {
-    int B, n, Hq, Hkv, G, tile, page, shift, width, num_pages, max_q, most;  // tile: rows of a tile, 8 or 16;
-                                                       // most: cached tokens of a request at most
-    float scale;
-    const void *q;
-    void *o;
-    int64_t q_st, q_sh, o_st, o_sh, eq, eo, e_table;
-    const int8_t *kc, *vc;
-    const float *ks, *vs;
-    const int32_t *table;
-    int64_t table_sb;
-    const int32_t *kv_lens, *cu;
-    float *ml, *part;                                 // parts: [2 grid][kRows][2] maximum and denominator, [2 grid][kRows][D]
-    int blocks;                                       // of the first kernel
-    int *status;
-};
-
-// A request as the kernel sees it.
-struct Request {
-    int first, q_len, kv, behind;                     // first query token, tokens, cached tokens, position of query token 0
-    int units, steps;                                 // (row tile, head) pairs, block steps of each
-};
-__device__ __forceinline__ Request request(const AttendParams &p, int b) {
-    const int2 span = seq_span(p.cu, b, p.n);
-    const int len = span.y - span.x, kv = max(p.kv_lens[b], 0);
-    Request r;
-    r.first = span.x;
-    r.q_len = min(len, p.max_q);
-    r.kv = min(kv, p.most);
-    r.behind = kv - len;
-    r.units = (r.q_len * p.G + p.tile - 1) / p.tile * p.Hkv;
-    r.steps = max((r.kv + kBlockStep - 1) / kBlockStep, 1);           // rows that see nothing are written, too
-    return r;
-}
-__device__ __forceinline__ bool cut(const AttendParams &p, int b) {
-    const int2 span = seq_span(p.cu, b, p.n);
-    return span.y - span.x > p.max_q || p.kv_lens[b] > p.most;
-}
 
 // The steps of all requests, and a block's share of them; worked out by a whole block of NT threads.
 struct Share {
@@ -123,29 +74,13 @@ __device__ __forceinline__ Share share_of(const AttendParams &p, int64_t *s_sum)
     return s;
 }
 
-__device__ __forceinline__ void report(int *status, int code) {
-    if (status != nullptr) atomicExch(status, code);
-}
-
 __device__ __forceinline__ void mma_f16_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm MMAV(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 constexpr int kMaxKv = 1 << 30;                       // positions stay well inside 32 bits
-// Two sign-flipped int8 in bytes 0 and 2 above exponent bytes -> their values as fp16.
-__device__ __forceinline__ uint32_t less_bias(uint32_t x) {
-    const uint32_t bias = 0x64806480u;                // 1152
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&bias));
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t low_pair(uint32_t w) { return less_bias(__byte_perm(w, 0x64646464u, 0x4140)); }
-__device__ __forceinline__ uint32_t high_pair(uint32_t w) { return less_bias(__byte_perm(w, 0x64646464u, 0x4342)); }
 
 // What a block holds of a page, in 16 bytes.
 struct PageInfo {
@@ -162,18 +97,8 @@ struct AttendShape {                                                  // NQ: til
     static constexpr int RING = kWarps * kStages * STAGE;
     static constexpr int JOIN = kWarps * 8 * NQ * (D + 4) * 4;        // the warps' softmax states, in the ring's place
     static constexpr int BYTES = RING > JOIN ? RING : JOIN;
-    static constexpr int BLOCKS = (D == 128 ? AB : 6) - NQ - (sizeof(T) == 4 ? 1 : 0); // of an SM, by shared memory and registers
+    static constexpr int BLOCKS = (D == 128 ? 4 : 6) - NQ - (sizeof(T) == 4 ? 1 : 0); // of an SM, by shared memory and registers
 };
-
-// Four values of a row of o from a weighted sum and its denominator; a row that saw nothing is zero.
-template <typename T>
-__device__ __forceinline__ void put_row(const AttendParams &p, int tok, int head, int d, const float (&o)[4], float sum) {
-    const int64_t off = (int64_t)tok * p.o_st + (int64_t)head * p.o_sh + d;
-    const float by = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (in_bounds(off + e, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off + e] = Cvt<T>::from_f(sum == 0.f ? 0.f : o[e] * by);
-}
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {          // an 8 x 8 tile of fp16 over the warp
     uint32_t y;
@@ -769,14 +694,15 @@ extern "C" {
 
 size_t cgdr_cache_attend_workspace_size(const cgdr_attend_args *a) {
     using namespace cgdr;
-    return check(a) != CGDR_OK || a->B == 0 || a->n == 0 || a->max_q == 0 ? 0 : workspace_of(*a);
+    return check(a) != CGDR_OK || a->B == 0 || a->n == 0 || a->max_q == 0 || attend_prompt_supported(*a) ? 0 : workspace_of(*a);
 }
 
 cgdr_status cgdr_cache_attend(const cgdr_attend_args *a, void *ws, size_t ws_bytes, void *stream) {
     using namespace cgdr;
     const cgdr_status st = check(a);
     if (st != CGDR_OK || a->B == 0 || a->n == 0 || a->max_q == 0) return st;
-    const size_t need = workspace_of(*a);
+    const bool prompt = attend_prompt_supported(*a);
+    const size_t need = prompt ? 0 : workspace_of(*a);
     if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned_to(ws, 16))) return CGDR_ERR_WORKSPACE;
     AttendParams p{};
     p.B = a->B; p.n = a->n; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = a->Hq / a->Hkv; p.page = a->page; p.shift = __builtin_ctz(a->page); p.width = a->width;
@@ -788,7 +714,8 @@ cgdr_status cgdr_cache_attend(const cgdr_attend_args *a, void *ws, size_t ws_byt
     p.kc = a->k_cache; p.vc = a->v_cache; p.ks = a->k_scale; p.vs = a->v_scale;
     p.table = a->block_table; p.table_sb = a->table_sb; p.e_table = (a->B - 1) * a->table_sb + a->width;
     p.kv_lens = a->kv_lens; p.cu = a->cu; p.status = a->status;
-    return launch_of(*a, p, static_cast<float *>(ws), static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return prompt ? launch_attend_prompt(*a, p, s) : launch_of(*a, p, static_cast<float *>(ws), s);
 }
 
 }  // extern "C"

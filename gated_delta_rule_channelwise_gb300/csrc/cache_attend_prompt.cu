@@ -1,0 +1,428 @@
+// Attention over the 8-bit paged cache for many query rows (prompts): bf16 queries, D = 128.
+//
+// The same mathematics and number formats as cache_attend.cu, on tcgen05: a block takes 256 rows
+// ((query token, head of the group) pairs of one request and key-value head) as two tiles of 128, and
+// walks over the cache 64 tokens at a time.
+//   - Four warps bring in k and v bytes by cp.async, two steps ahead, and turn them into fp16 tiles once for
+//     both row tiles: k as it lies, v transposed on the way by stmatrix (rows d, columns tokens).
+//   - One thread issues the products: s = q k^T into tensor memory, and o += p v with p from tensor memory.
+//     s of the next step is under way while p of this one is formed.
+//   - Four warps for each row tile, a thread a row, read s, form p' = 2^(s + log2 vs - M + kUp), and put it
+//     back as fp16.  o stays in tensor memory; it is rescaled when a row's maximum has grown by
+//     more than 2^7, which after the first steps is rare.
+// 64 tokens by 256 rows are 4.2 M multiply-adds (1,024 tensor-core cycles) against 16,384 exponentials (512
+// cycles of that unit) and about 900 issue cycles of the four schedulers for softmax and conversions: the
+// tile is as wide as tensor memory allows (two o, two s and two p take 448 of 512 columns), because
+// every row shares the conversions.
+#include "cache_attend.cuh"
+#include "tc05.cuh"
+
+namespace cgdr {
+namespace {
+
+using namespace tc05;
+
+constexpr int D = 128;
+constexpr int kTile = 128;                            // rows of a tile
+constexpr int kTok = 64;                              // cached tokens of a step
+constexpr int kGroups = kTok / 16;                    // a group of 16 tokens lies in one page
+constexpr int kSoft = 128;                            // softmax threads of a tile
+constexpr int kLoad = 128;                            // loading threads
+constexpr int kThreads = 2 * kSoft + kLoad + 32;      // and the warp that issues the products
+constexpr int kRaw = 2 * kTok * D;                    // k and v bytes of a step
+constexpr int kRawStages = 3;
+#ifndef POLLS
+#define POLLS (1u << 18)
+#endif
+constexpr uint32_t kPolls = POLLS;                    // of a wait, before it gives up
+
+constexpr int kQBytes = kTile * D * 2, kKBytes = kTok * D * 2, kVBytes = D * kTok * 2;
+constexpr int kOffQ = 0, kOffK = 2 * kQBytes, kOffV = kOffK + 2 * kKBytes, kOffRaw = kOffV + 2 * kVBytes;
+constexpr int kOffScale = kOffRaw + kRawStages * kRaw;                // float4 [4][kGroups]: ring of four steps
+constexpr int kOffBar = kOffScale + 4 * kGroups * 16;
+enum Bar { kQFull, kKFull, kKFree = kKFull + 2, kVFull = kKFree + 2, kVFree = kVFull + 2, kSFull = kVFree + 2, kSFree = kSFull + 2,
+           kPFull = kSFree + 2, kPvDone = kPFull + 2, kDrain = kPvDone + 2, kBars };
+constexpr int kBytes = kOffBar + kBars * 8 + 1024;    // and the room to align to 1024 bytes
+
+constexpr int kTmemO = 0, kTmemS = 2 * D, kTmemP = kTmemS + 2 * kTok, kTmemCols = 512;
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Where a 16-byte piece of a token's 128 bytes is kept among them: its number xor this.
+__device__ __forceinline__ int raw_swizzle(int token) { return ((token & 1) << 2) | ((token >> 1) & 3); }
+
+__device__ __forceinline__ void stmatrix_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const AttendParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_stop;                   // a wait gave up: everybody leaves
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int b = blockIdx.z, hk = blockIdx.y, row0 = (int)(gridDim.x - 1 - blockIdx.x) * 2 * kTile;      // the longest rows first
+    const Request rq = request(p, b);
+    const int rows = rq.q_len * p.G, kv = rq.kv, behind = rq.behind;
+    if (row0 >= rows) return;
+    const int tiles = rows - row0 > kTile ? 2 : 1, last_row = min(row0 + 2 * kTile, rows) - 1;
+    const int end = min(kv, behind + last_row / p.G + 1);             // what the last row sees
+    const int steps = end > 0 ? (end + kTok - 1) / kTok : 0;
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+    auto bar = [&](int i) { return base + kOffBar + 8 * i; };
+    if (tid == 0) {
+        s_stop = 0;
+        mbar_init(bar(kQFull), tiles * kSoft);
+        mbar_init(bar(kDrain), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kKFull + i), kLoad);
+            mbar_init(bar(kVFull + i), kLoad);
+            mbar_init(bar(kKFree + i), 1);
+            mbar_init(bar(kVFree + i), 1);
+            mbar_init(bar(kSFull + i), 2);            // the products, and the thread that issued them (for what it has seen)
+            mbar_init(bar(kSFree + i), kSoft);
+            mbar_init(bar(kPFull + i), kSoft);
+            mbar_init(bar(kPvDone + i), 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kThreads / 32 - 1) tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = s_tmem;
+
+    // false: this wait, or another thread's, gave up
+    auto wait = [&](int which, uint32_t parity) -> bool {
+        for (uint32_t it = 0; it < kPolls; ++it) {
+            if (mbar_try_wait(bar(which), parity)) return true;
+            if (s_stop) return false;
+        }
+        s_stop = 1;
+        report(p.status, (int)CGDR_ERR_TIMEOUT);
+        return false;
+    };
+
+    if (warp < 2 * kSoft / 32) {
+        // ---------------------------------------------------------------- softmax: a thread a row
+        const int tile = warp / (kSoft / 32), r = tid % kSoft, row = row0 + tile * kTile + r;
+        if (tile < tiles) {
+            const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+            const int tok = rq.first + row / p.G, head = hk * p.G + row % p.G;
+            const bool ok = row < rows;
+            const int seen = ok ? min(behind + row / p.G + 1, kv) : 0;
+            const int all_see = row0 + (tile + 1) * kTile <= rows ? min(kv, behind + (row0 + tile * kTile) / p.G + 1) : 0;
+            float scale;
+            {
+                // the row in fp16, scaled by a power of two to magnitudes below 2 (4 at the type's end)
+                const int64_t off = (int64_t)tok * p.q_st + (int64_t)head * p.q_sh;
+                uint4 raw[D / 8];
+                float top = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    raw[c] = make_uint4(0, 0, 0, 0);
+                    if (ok && range_in_bounds(off + 8 * c, 8, p.eq, p.status, nullptr))
+                        raw[c] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off) + c);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    float f[8];
+                    Vec<__nv_bfloat16>::unpack(raw[c], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+                }
+                const int ex = top > 0x1p-100f && top < INFINITY ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
+                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                scale = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale * kLog2e;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    float f[8];
+                    Vec<__nv_bfloat16>::unpack(raw[c], f);
+                    sts128(base + kOffQ + tile * kQBytes + sw_off16(kTile, r, 8 * c), half2_bits(f[0] * down, f[1] * down),
+                           half2_bits(f[2] * down, f[3] * down), half2_bits(f[4] * down, f[5] * down), half2_bits(f[6] * down, f[7] * down));
+                }
+                fence_smem_to_async();
+                arrive(bar(kQFull));
+            }
+            float M = kLowest, l = 0.f;
+            bool go = true;
+            const uint32_t t_s = tmem + lanes + kTmemS + tile * kTok, t_p = tmem + lanes + kTmemP + tile * (kTok / 2),
+                           t_o = tmem + lanes + kTmemO + tile * D;
+            for (int i = 0; i < steps && go; ++i) {
+                go = __all_sync(0xffffffffu, wait(kSFull + tile, i & 1));
+                if (!go) break;
+                fence_after_sync();
+                float x[kTok];
+                tmem_ld32(t_s, *reinterpret_cast<float (*)[32]>(x));
+                tmem_ld32(t_s + 32, *reinterpret_cast<float (*)[32]>(x + 32));
+                fence_before_sync();
+                arrive(bar(kSFree + tile));
+                // x <- exponents s + log2 vs; their largest
+                float iv[kGroups], top = kLowest;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    float4 sc;
+                    const uint4 raw = lds128(base + kOffScale + ((i & 3) * kGroups + g) * 16);
+                    sc = make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), 0.f);
+                    iv[g] = sc.z;
+                    const f32x2 c = both(sc.x * scale), lv = both(sc.y);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 y = split(fma2(pair(x[16 * g + e], x[16 * g + e + 1]), c, lv));
+                        x[16 * g + e] = y.x;
+                        x[16 * g + e + 1] = y.y;
+                    }
+                }
+                if ((i + 1) * kTok > all_see) {
+#pragma unroll
+                    for (int e = 0; e < kTok; ++e)
+                        if (i * kTok + e >= seen) x[e] = -INFINITY;
+                }
+#pragma unroll
+                for (int e = 0; e < kTok; ++e) top = fmaxf(top, x[e]);
+                if (__any_sync(0xffffffffu, top > M + (kMost - kUp))) {
+                    const float m = fmaxf(M, top), shrink = ex2(M - m);
+                    M = m;
+                    l *= shrink;
+                    if (i > 0) {                      // o is at rest once the last step's product is done
+                        go = __all_sync(0xffffffffu, wait(kPvDone + tile, (i - 1) & 1));
+                        if (!go) break;
+                        fence_after_sync();
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            float o[16];
+                            tmem_ld16(t_o + c, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= shrink;
+                            tmem_st16(t_o + c, o);
+                        }
+                    }
+                }
+                if (i > 0) {                          // the last step's p has been read
+                    go = __all_sync(0xffffffffu, wait(kPvDone + tile, (i - 1) & 1));
+                    if (!go) break;
+                    fence_after_sync();
+                }
+                const f32x2 less = both(kUp - M);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float w[kTok / 4];                // fp16 pairs
+#pragma unroll
+                    for (int g = 2 * half; g < 2 * half + 2; ++g) {
+                        f32x2 sum = both(0.f);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 d = split(add2(pair(x[16 * g + e], x[16 * g + e + 1]), less));
+                            const float a = ex2(d.x), c = ex2(d.y);
+                            sum = add2(sum, pair(a, c));
+                            w[8 * (g & 1) + e / 2] = __uint_as_float(iv[g] < 0.f ? 0u : half2_bits(a, c));
+                        }
+                        l = fmaf(split(sum).x + split(sum).y, fabsf(iv[g]), l);
+                    }
+                    tmem_st16(t_p + 16 * half, w);
+                }
+                fence_before_sync();
+                arrive(bar(kPFull + tile));
+            }
+            if (steps > 0 && go) go = __all_sync(0xffffffffu, wait(kPvDone + tile, (steps - 1) & 1));
+            if (go) {
+                fence_after_sync();
+                const float by = l == 0.f ? 0.f : 1.f / l;
+                const int64_t off = (int64_t)tok * p.o_st + (int64_t)head * p.o_sh;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float o[64];
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) o[e] = 0.f;
+                    if (steps > 0) {
+                        tmem_ld32(t_o + 64 * h, *reinterpret_cast<float (*)[32]>(o));
+                        tmem_ld32(t_o + 64 * h + 32, *reinterpret_cast<float (*)[32]>(o + 32));
+                    }
+                    if (ok) {
+                        // column 8 m + 2 j + e, m = 8 h + 2 w + t, holds d = 64 h + 16 j + 4 w + 2 t + e
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                const float y[4] = {o[16 * w + 2 * j], o[16 * w + 2 * j + 1], o[16 * w + 8 + 2 * j], o[16 * w + 8 + 2 * j + 1]};
+                                const int64_t at = off + 64 * h + 16 * j + 4 * w;
+                                if (!range_in_bounds(at, 4, p.eo, p.status, nullptr)) continue;
+                                __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.o) + at;
+                                const uint2 v = l == 0.f ? make_uint2(0, 0)
+                                                         : make_uint2(pack_bf16x2(y[0] * by, y[1] * by), pack_bf16x2(y[2] * by, y[3] * by));
+                                *reinterpret_cast<uint2 *>(to) = v;
+                            }
+                    }
+                }
+            }
+        }
+    } else if (warp < (2 * kSoft + kLoad) / 32) {
+        // ---------------------------------------------------------------- loading and converting
+        const int t = tid - 2 * kSoft, w = t >> 5;
+        int page[kGroups];                            // of the step to be copied next; -1: nothing to copy
+        auto look = [&](int i) {                      // step i's pages
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const int pos = i * kTok + 16 * g;
+                page[g] = -1;
+                if (pos < end) {
+                    const int64_t at = b * p.table_sb + (pos >> p.shift);
+                    if (in_bounds(at, p.e_table, p.status, nullptr)) page[g] = __ldg(p.table + at);
+                    if (page[g] < 0 || page[g] >= p.num_pages) {
+                        page[g] = -1;
+                        if (t == 0) report(p.status, (int)CGDR_ERR_BOUNDS);
+                    }
+                }
+            }
+        };
+        // scales of group t of a step, from its page on their way to shared memory: k's, v's
+        float2 sc0 = make_float2(0.f, -1.f), sc1 = sc0, sc2 = sc0;
+        auto copy = [&](int i) {                      // step i's bytes; its pages are in `page`
+            float2 sc = make_float2(0.f, -1.f);       // v's below zero: no page
+            if (i < steps) {
+                const uint32_t dst = base + kOffRaw + i % kRawStages * kRaw;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    if (page[g] >= 0) {
+                        const int token = 16 * g + (t >> 3), piece = t & 7;
+                        const int64_t src = ((((int64_t)page[g] * p.Hkv + hk) << p.shift) + ((i * kTok + token) & (p.page - 1))) * D + piece * 16;
+                        const uint32_t to = dst + token * D + (piece ^ raw_swizzle(token)) * 16;
+                        cp_async16(to, p.kc + src, true);
+                        cp_async16(to + kTok * D, p.vc + src, true);
+                        if (t == g) sc = make_float2(__ldg(p.ks + (int64_t)page[g] * p.Hkv + hk), __ldg(p.vs + (int64_t)page[g] * p.Hkv + hk));
+                    }
+                }
+            }
+            cp_async_commit();
+            return sc;
+        };
+        look(0);
+        sc0 = copy(0);
+        look(1);
+        sc1 = copy(1);
+        look(2);
+        bool go = true;
+        for (int i = 0; i < steps; ++i) {             // every warp takes part in every step's barrier, even when a wait gave up
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            named_bar_sync<1, kLoad>();               // everybody's copies of step i, and their reads of step i - 1
+            sc2 = copy(i + 2);
+            look(i + 3);
+            const uint32_t raw = base + kOffRaw + i % kRawStages * kRaw;
+            const int st = i & 1;
+            if (go && i >= 2) go = __all_sync(0xffffffffu, wait(kKFree + st, ((i >> 1) - 1) & 1));
+            if (!go) continue;
+            // (the softmax threads have left step i - 4 behind: the products of step i - 2 are done, which were issued
+            // after they had read s of step i - 3)
+            if (t < kGroups) {
+                // k's scale, and log2 and reciprocal of v's: 0 and -1 where that is (as good as) zero; no page: -inf
+                const bool zero = sc0.y < 0x1p-100f, none = sc0.y < 0.f;
+                sts128(base + kOffScale + ((i & 3) * kGroups + t) * 16, __float_as_uint(sc0.x),
+                       __float_as_uint(none ? -INFINITY : zero ? 0.f : log2f(sc0.y)), __float_as_uint(zero ? -1.f : 1.f / sc0.y), 0);
+            }
+            sc0 = sc1;
+            sc1 = sc2;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {             // 16 bytes of a key: two 16-byte pieces of its fp16 row
+                const int token = 16 * w + 8 * (n >> 1) + (lane & 7), piece = (lane >> 3) + 4 * (n & 1);
+                const uint4 v = lds128(raw + token * D + (piece ^ raw_swizzle(token)) * 16);
+                const uint32_t a[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+                const uint32_t to = base + kOffK + st * kKBytes;
+                sts128(to + sw_off16(kTok, token, 16 * piece), low_pair(a[0]), high_pair(a[0]), low_pair(a[1]), high_pair(a[1]));
+                sts128(to + sw_off16(kTok, token, 16 * piece + 8), low_pair(a[2]), high_pair(a[2]), low_pair(a[3]), high_pair(a[3]));
+            }
+            fence_smem_to_async();
+            arrive(bar(kKFull + st));
+            if (i >= 2) go = __all_sync(0xffffffffu, wait(kVFree + st, ((i >> 1) - 1) & 1));
+            if (!go) continue;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {             // eight tokens at a time
+                const int eight = 2 * w + n, token = 8 * eight + (lane >> 2);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int piece = (lane & 3) + 4 * h;
+                    const uint4 v = lds128(raw + kTok * D + token * D + (piece ^ raw_swizzle(token)) * 16);
+                    const uint32_t a[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {     // four 8 x 8 tiles, of rows 8 m .. 8 m + 7 each
+                        const int m0 = 8 * h + 4 * c, row = 8 * (m0 + (lane >> 3)) + (lane & 7);
+                        stmatrix_t(base + kOffV + st * kVBytes + sw_off16(D, row, 8 * eight), low_pair(a[2 * c]), high_pair(a[2 * c]),
+                                   low_pair(a[2 * c + 1]), high_pair(a[2 * c + 1]));
+                    }
+                }
+            }
+            fence_smem_to_async();
+            arrive(bar(kVFull + st));
+        }
+        cp_async_wait_all();
+    } else if (lane == 0 && steps > 0) {
+        // ---------------------------------------------------------------- the products
+        bool go = wait(kQFull, 0) && wait(kKFull, 0);
+        auto qk = [&](int tile, int i) {
+            gemm16<kTok, D>(tmem + kTmemS + tile * kTok, base + kOffQ + tile * kQBytes, base + kOffK + (i & 1) * kKBytes, false);
+            arrive(bar(kSFull + tile));
+            commit(bar(kSFull + tile));
+        };
+        if (go) {
+            fence_after_sync();
+            for (int tile = 0; tile < tiles; ++tile) qk(tile, 0);
+            commit(bar(kKFree));
+        }
+        for (int i = 0; i < steps && go; ++i) {
+            const bool next = i + 1 < steps;
+            if (next) go = wait(kKFull + ((i + 1) & 1), ((i + 1) >> 1) & 1);
+            for (int tile = 0; tile < tiles && go; ++tile) {
+                if (next) {
+                    go = wait(kSFree + tile, i & 1);
+                    if (!go) break;
+                    fence_after_sync();
+                    qk(tile, i + 1);
+                    if (tile == tiles - 1) commit(bar(kKFree + ((i + 1) & 1)));
+                }
+                go = wait(kPFull + tile, i & 1) && (tile > 0 || wait(kVFull + (i & 1), (i >> 1) & 1));
+                if (!go) break;
+                fence_after_sync();
+                gemm16_ts<D, kTok>(tmem + kTmemO + tile * D, tmem + kTmemP + tile * (kTok / 2), base + kOffV + (i & 1) * kVBytes, i > 0);
+                commit(bar(kPvDone + tile));
+            }
+            if (go) commit(bar(kVFree + (i & 1)));
+        }
+        if (!go) {                                    // what was issued has to end before its memory is given up
+            commit(bar(kDrain));
+            mbar_wait(bar(kDrain), 0, kPolls);
+        }
+    }
+    __syncwarp();
+    fence_before_sync();
+    __syncthreads();
+    if (warp == kThreads / 32 - 1) {
+        fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+}  // namespace
+
+bool attend_prompt_supported(const cgdr_attend_args &a) {
+    const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
+    return a.dtype == CGDR_BF16 && a.D == D && rows > kTile / 2 && (a.o_st | a.o_sh) % 8 == 0 && aligned_to(a.o, 16) && a.Hkv <= 65535;
+}
+
+cgdr_status launch_attend_prompt(const cgdr_attend_args &a, AttendParams &p, cudaStream_t s) {
+    static SmemOnce smem_once;
+    if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_prompt_kernel), kBytes)) return CGDR_ERR_CUDA;
+    const int64_t rows = (int64_t)a.max_q * p.G, pairs = (rows + 2 * kTile - 1) / (2 * kTile);
+    cache_attend_prompt_kernel<<<dim3((unsigned)pairs, a.Hkv, a.B), kThreads, kBytes, s>>>(p);
+    return launched();
+}
+
+}  // namespace cgdr
