@@ -5,8 +5,8 @@
 // walks over the cache 64 tokens at a time.
 //   - Four warps bring in k and v bytes by cp.async, two steps ahead, and turn them into fp16 tiles once for
 //     both row tiles: k as it lies, v transposed on the way by stmatrix (rows d, columns tokens).
-//   - One thread issues the products: s = q k^T into tensor memory, and o += p v with p from tensor memory.
-//     s of the next step is under way while p of this one is formed.
+//   - Four threads issue the products: s = q k^T into tensor memory, and o += p v with p from tensor memory,
+//     for each tile.  s of the next step is under way while p of this one is formed.
 //   - Four warps for each row tile, a thread a row, read s, form p' = 2^(s + log2 vs - M + kUp), and put it
 //     back as fp16.  o stays in tensor memory; it is rescaled when a row's maximum has grown by
 //     more than 2^7, which after the first steps is rare.
@@ -28,7 +28,7 @@ constexpr int kTok = 64;                              // cached tokens of a step
 constexpr int kGroups = kTok / 16;                    // a group of 16 tokens lies in one page
 constexpr int kSoft = 128;                            // softmax threads of a tile
 constexpr int kLoad = 128;                            // loading threads
-constexpr int kThreads = 2 * kSoft + kLoad + 32;      // and the warp that issues the products
+constexpr int kThreads = 2 * kSoft + kLoad + 4 * 32;  // and four warps that issue the products
 constexpr int kRaw = 2 * kTok * D;                    // k and v bytes of a step
 constexpr int kRawStages = 3;
 #ifndef POLLS
@@ -39,9 +39,10 @@ constexpr uint32_t kPolls = POLLS;                    // of a wait, before it gi
 constexpr int kQBytes = kTile * D * 2, kKBytes = kTok * D * 2, kVBytes = D * kTok * 2;
 constexpr int kOffQ = 0, kOffK = 2 * kQBytes, kOffV = kOffK + 2 * kKBytes, kOffRaw = kOffV + 2 * kVBytes;
 constexpr int kOffScale = kOffRaw + kRawStages * kRaw;                // float4 [4][kGroups]: ring of four steps
-constexpr int kOffBar = kOffScale + 4 * kGroups * 16;
+constexpr int kOffRawScale = kOffScale + 4 * kGroups * 16;            // float2 [kRawStages][kGroups]: scales as copied
+constexpr int kOffBar = kOffRawScale + kRawStages * kGroups * 8;
 enum Bar { kQFull, kKFull, kKFree = kKFull + 2, kVFull = kKFree + 2, kVFree = kVFull + 2, kSFull = kVFree + 2, kSFree = kSFull + 2,
-           kPFull = kSFree + 2, kPvDone = kPFull + 2, kDrain = kPvDone + 2, kBars };
+           kPFull = kSFree + 2, kPvDone = kPFull + 2, kDrain = kPvDone + 2, kBars = kDrain + 4 };
 constexpr int kBytes = kOffBar + kBars * 8 + 1024;    // and the room to align to 1024 bytes
 
 constexpr int kTmemO = 0, kTmemS = 2 * D, kTmemP = kTmemS + 2 * kTok, kTmemCols = 512;
@@ -65,10 +66,43 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// 64 consecutive fp32 columns of this thread's TMEM lane (warp-wide), in one instruction.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __noinline__ bool keep_waiting(uint32_t bar, uint32_t parity, volatile int *stop, int *status) {
+    for (uint32_t it = 0; it < kPolls; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*stop) return false;
+    }
+    *stop = 1;
+    report(status, (int)CGDR_ERR_TIMEOUT);
+    return false;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const AttendParams p) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_stop;                   // a wait gave up: everybody leaves
+    __shared__ volatile int s_stop, s_never;          // a wait gave up: everybody leaves; (never set)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int b = blockIdx.z, hk = blockIdx.y, row0 = (int)(gridDim.x - 1 - blockIdx.x) * 2 * kTile;      // the longest rows first
     const Request rq = request(p, b);
@@ -82,16 +116,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
     auto bar = [&](int i) { return base + kOffBar + 8 * i; };
     if (tid == 0) {
         s_stop = 0;
-        mbar_init(bar(kQFull), tiles * kSoft);
-        mbar_init(bar(kDrain), 1);
+        mbar_init(bar(kQFull), tiles * kSoft / 32);
+        s_never = 0;
+        for (int i = 0; i < 4; ++i) mbar_init(bar(kDrain + i), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kKFull + i), kLoad);
-            mbar_init(bar(kVFull + i), kLoad);
-            mbar_init(bar(kKFree + i), 1);
-            mbar_init(bar(kVFree + i), 1);
+            mbar_init(bar(kKFull + i), kLoad / 32);
+            mbar_init(bar(kVFull + i), kLoad / 32);
+            mbar_init(bar(kKFree + i), tiles);
+            mbar_init(bar(kVFree + i), tiles);
             mbar_init(bar(kSFull + i), 2);            // the products, and the thread that issued them (for what it has seen)
-            mbar_init(bar(kSFree + i), kSoft);
-            mbar_init(bar(kPFull + i), kSoft);
+            mbar_init(bar(kSFree + i), kSoft / 32);
+            mbar_init(bar(kPFull + i), kSoft / 32);
             mbar_init(bar(kPvDone + i), 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -102,15 +137,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
     fence_after_sync();
     const uint32_t tmem = s_tmem;
 
-    // false: this wait, or another thread's, gave up
+    // false: this wait, or another thread's, gave up.  The first look is straight-line code: a wait that is
+    // over already costs 50 cycles so, and 190 as a loop.
     auto wait = [&](int which, uint32_t parity) -> bool {
-        for (uint32_t it = 0; it < kPolls; ++it) {
-            if (mbar_try_wait(bar(which), parity)) return true;
-            if (s_stop) return false;
-        }
-        s_stop = 1;
-        report(p.status, (int)CGDR_ERR_TIMEOUT);
-        return false;
+        if (mbar_try_wait(bar(which), parity)) return true;
+        return keep_waiting(bar(which), parity, &s_stop, p.status);
+    };
+    auto done = [&](int which) {                      // a warp's arrival
+        __syncwarp();
+        if (lane == 0) arrive(bar(which));
     };
 
     if (warp < 2 * kSoft / 32) {
@@ -126,33 +161,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
             {
                 // the row in fp16, scaled by a power of two to magnitudes below 2 (4 at the type's end)
                 const int64_t off = (int64_t)tok * p.q_st + (int64_t)head * p.q_sh;
-                uint4 raw[D / 8];
-                float top = 0.f;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    raw[c] = make_uint4(0, 0, 0, 0);
+                auto eight = [&](int c, float (&f)[8]) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
                     if (ok && range_in_bounds(off + 8 * c, 8, p.eq, p.status, nullptr))
-                        raw[c] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off) + c);
-                }
-#pragma unroll
+                        v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off) + c);
+                    Vec<__nv_bfloat16>::unpack(v, f);
+                };
+                float top = 0.f;
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                     float f[8];
-                    Vec<__nv_bfloat16>::unpack(raw[c], f);
+                    eight(c, f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
                 }
                 const int ex = top > 0x1p-100f && top < INFINITY ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
                 const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
                 scale = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale * kLog2e;
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                     float f[8];
-                    Vec<__nv_bfloat16>::unpack(raw[c], f);
+                    eight(c, f);
                     sts128(base + kOffQ + tile * kQBytes + sw_off16(kTile, r, 8 * c), half2_bits(f[0] * down, f[1] * down),
                            half2_bits(f[2] * down, f[3] * down), half2_bits(f[4] * down, f[5] * down), half2_bits(f[6] * down, f[7] * down));
                 }
                 fence_smem_to_async();
-                arrive(bar(kQFull));
+                done(kQFull);
             }
             float M = kLowest, l = 0.f;
             bool go = true;
@@ -163,12 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                 if (!go) break;
                 fence_after_sync();
                 float x[kTok];
-                tmem_ld32(t_s, *reinterpret_cast<float (*)[32]>(x));
-                tmem_ld32(t_s + 32, *reinterpret_cast<float (*)[32]>(x + 32));
+                tmem_ld64(t_s, x);
                 fence_before_sync();
-                arrive(bar(kSFree + tile));
+                done(kSFree + tile);
                 // x <- exponents s + log2 vs; their largest
-                float iv[kGroups], top = kLowest;
+                float iv[kGroups];
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     float4 sc;
@@ -188,8 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                     for (int e = 0; e < kTok; ++e)
                         if (i * kTok + e >= seen) x[e] = -INFINITY;
                 }
+                float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int e = 0; e < kTok; ++e) top = fmaxf(top, x[e]);
+                for (int e = 4; e < kTok; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[e]);
+                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 if (__any_sync(0xffffffffu, top > M + (kMost - kUp))) {
                     const float m = fmaxf(M, top), shrink = ex2(M - m);
                     M = m;
@@ -232,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                     tmem_st16(t_p + 16 * half, w);
                 }
                 fence_before_sync();
-                arrive(bar(kPFull + tile));
+                done(kPFull + tile);
             }
             if (steps > 0 && go) go = __all_sync(0xffffffffu, wait(kPvDone + tile, (steps - 1) & 1));
             if (go) {
@@ -269,136 +304,142 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
     } else if (warp < (2 * kSoft + kLoad) / 32) {
         // ---------------------------------------------------------------- loading and converting
         const int t = tid - 2 * kSoft, w = t >> 5;
-        int page[kGroups];                            // of the step to be copied next; -1: nothing to copy
-        auto look = [&](int i) {                      // step i's pages
+        // Nothing here waits for a load in the step that issues it: page numbers are looked at a step after they
+        // are asked for, and scales come with the copies.
+        int page[kGroups];                            // table entries of the step to be copied next
+        auto look = [&](int i) {
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 const int pos = i * kTok + 16 * g;
+                const int64_t at = b * p.table_sb + (pos >> p.shift);
                 page[g] = -1;
-                if (pos < end) {
-                    const int64_t at = b * p.table_sb + (pos >> p.shift);
-                    if (in_bounds(at, p.e_table, p.status, nullptr)) page[g] = __ldg(p.table + at);
-                    if (page[g] < 0 || page[g] >= p.num_pages) {
-                        page[g] = -1;
-                        if (t == 0) report(p.status, (int)CGDR_ERR_BOUNDS);
-                    }
-                }
+                if (pos < end && in_bounds(at, p.e_table, p.status, nullptr)) page[g] = __ldg(p.table + at);
             }
         };
-        // scales of group t of a step, from its page on their way to shared memory: k's, v's
-        float2 sc0 = make_float2(0.f, -1.f), sc1 = sc0, sc2 = sc0;
-        auto copy = [&](int i) {                      // step i's bytes; its pages are in `page`
-            float2 sc = make_float2(0.f, -1.f);       // v's below zero: no page
+        auto copy = [&](int i) {                      // step i's bytes and scales; its pages are in `page`
             if (i < steps) {
                 const uint32_t dst = base + kOffRaw + i % kRawStages * kRaw;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    if (page[g] >= 0) {
+                    const bool ok = page[g] >= 0 && page[g] < p.num_pages;
+                    if (ok) {
                         const int token = 16 * g + (t >> 3), piece = t & 7;
-                        const int64_t src = ((((int64_t)page[g] * p.Hkv + hk) << p.shift) + ((i * kTok + token) & (p.page - 1))) * D + piece * 16;
+                        const int64_t unit = (int64_t)page[g] * p.Hkv + hk;
+                        const int64_t src = ((unit << p.shift) + ((i * kTok + token) & (p.page - 1))) * D + piece * 16;
                         const uint32_t to = dst + token * D + (piece ^ raw_swizzle(token)) * 16;
                         cp_async16(to, p.kc + src, true);
                         cp_async16(to + kTok * D, p.vc + src, true);
-                        if (t == g) sc = make_float2(__ldg(p.ks + (int64_t)page[g] * p.Hkv + hk), __ldg(p.vs + (int64_t)page[g] * p.Hkv + hk));
+                    }
+                    if (t == g) {                     // k's scale, then v's; below zero: no page
+                        const uint32_t to = base + kOffRawScale + (i % kRawStages * kGroups + g) * 8;
+                        if (ok) {
+                            cp_async4(to, p.ks + (int64_t)page[g] * p.Hkv + hk, true);
+                            cp_async4(to + 4, p.vs + (int64_t)page[g] * p.Hkv + hk, true);
+                        } else {
+                            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(0.f), "f"(-1.f) : "memory");
+                            if (i * kTok + 16 * g < end) report(p.status, (int)CGDR_ERR_BOUNDS);
+                        }
                     }
                 }
             }
             cp_async_commit();
-            return sc;
         };
         look(0);
-        sc0 = copy(0);
+        copy(0);
         look(1);
-        sc1 = copy(1);
+        copy(1);
         look(2);
         bool go = true;
         for (int i = 0; i < steps; ++i) {             // every warp takes part in every step's barrier, even when a wait gave up
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             named_bar_sync<1, kLoad>();               // everybody's copies of step i, and their reads of step i - 1
-            sc2 = copy(i + 2);
+            copy(i + 2);
             look(i + 3);
             const uint32_t raw = base + kOffRaw + i % kRawStages * kRaw;
             const int st = i & 1;
+            uint4 kv4[4];                             // 16 bytes of four keys
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int token = 16 * w + 8 * (n >> 1) + (lane & 7), piece = (lane >> 3) + 4 * (n & 1);
+                kv4[n] = lds128(raw + token * D + (piece ^ raw_swizzle(token)) * 16);
+            }
             if (go && i >= 2) go = __all_sync(0xffffffffu, wait(kKFree + st, ((i >> 1) - 1) & 1));
             if (!go) continue;
             // (the softmax threads have left step i - 4 behind: the products of step i - 2 are done, which were issued
             // after they had read s of step i - 3)
             if (t < kGroups) {
                 // k's scale, and log2 and reciprocal of v's: 0 and -1 where that is (as good as) zero; no page: -inf
-                const bool zero = sc0.y < 0x1p-100f, none = sc0.y < 0.f;
-                sts128(base + kOffScale + ((i & 3) * kGroups + t) * 16, __float_as_uint(sc0.x),
-                       __float_as_uint(none ? -INFINITY : zero ? 0.f : log2f(sc0.y)), __float_as_uint(zero ? -1.f : 1.f / sc0.y), 0);
+                float ks, vs;
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(base + kOffRawScale + (i % kRawStages * kGroups + t) * 8));
+                const bool zero = vs < 0x1p-100f, none = vs < 0.f;
+                sts128(base + kOffScale + ((i & 3) * kGroups + t) * 16, __float_as_uint(ks),
+                       __float_as_uint(none ? -INFINITY : zero ? 0.f : log2f(vs)), __float_as_uint(zero ? -1.f : 1.f / vs), 0);
             }
-            sc0 = sc1;
-            sc1 = sc2;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {             // 16 bytes of a key: two 16-byte pieces of its fp16 row
+            for (int n = 0; n < 4; ++n) {             // two 16-byte pieces of a key's fp16 row each
                 const int token = 16 * w + 8 * (n >> 1) + (lane & 7), piece = (lane >> 3) + 4 * (n & 1);
-                const uint4 v = lds128(raw + token * D + (piece ^ raw_swizzle(token)) * 16);
-                const uint32_t a[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+                const uint32_t a[4] = {kv4[n].x ^ 0x80808080u, kv4[n].y ^ 0x80808080u, kv4[n].z ^ 0x80808080u, kv4[n].w ^ 0x80808080u};
                 const uint32_t to = base + kOffK + st * kKBytes;
                 sts128(to + sw_off16(kTok, token, 16 * piece), low_pair(a[0]), high_pair(a[0]), low_pair(a[1]), high_pair(a[1]));
                 sts128(to + sw_off16(kTok, token, 16 * piece + 8), low_pair(a[2]), high_pair(a[2]), low_pair(a[3]), high_pair(a[3]));
             }
             fence_smem_to_async();
-            arrive(bar(kKFull + st));
+            done(kKFull + st);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {             // and of four values: eight tokens (n / 2) by half of d (n % 2) at a time
+                const int token = 8 * (2 * w + (n >> 1)) + (lane >> 2), piece = (lane & 3) + 4 * (n & 1);
+                kv4[n] = lds128(raw + kTok * D + token * D + (piece ^ raw_swizzle(token)) * 16);
+            }
             if (i >= 2) go = __all_sync(0xffffffffu, wait(kVFree + st, ((i >> 1) - 1) & 1));
             if (!go) continue;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {             // eight tokens at a time
-                const int eight = 2 * w + n, token = 8 * eight + (lane >> 2);
+            for (int n = 0; n < 4; ++n) {
+                const uint32_t a[4] = {kv4[n].x ^ 0x80808080u, kv4[n].y ^ 0x80808080u, kv4[n].z ^ 0x80808080u, kv4[n].w ^ 0x80808080u};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int piece = (lane & 3) + 4 * h;
-                    const uint4 v = lds128(raw + kTok * D + token * D + (piece ^ raw_swizzle(token)) * 16);
-                    const uint32_t a[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {     // four 8 x 8 tiles, of rows 8 m .. 8 m + 7 each
-                        const int m0 = 8 * h + 4 * c, row = 8 * (m0 + (lane >> 3)) + (lane & 7);
-                        stmatrix_t(base + kOffV + st * kVBytes + sw_off16(D, row, 8 * eight), low_pair(a[2 * c]), high_pair(a[2 * c]),
-                                   low_pair(a[2 * c + 1]), high_pair(a[2 * c + 1]));
-                    }
+                for (int c = 0; c < 2; ++c) {         // four 8 x 8 tiles, of rows 8 m .. 8 m + 7 each
+                    const int row = 8 * (8 * (n & 1) + 4 * c + (lane >> 3)) + (lane & 7);
+                    stmatrix_t(base + kOffV + st * kVBytes + sw_off16(D, row, 8 * (2 * w + (n >> 1))), low_pair(a[2 * c]), high_pair(a[2 * c]),
+                               low_pair(a[2 * c + 1]), high_pair(a[2 * c + 1]));
                 }
             }
             fence_smem_to_async();
-            arrive(bar(kVFull + st));
+            done(kVFull + st);
         }
         cp_async_wait_all();
-    } else if (lane == 0 && steps > 0) {
+    } else {
         // ---------------------------------------------------------------- the products
-        bool go = wait(kQFull, 0) && wait(kKFull, 0);
-        auto qk = [&](int tile, int i) {
-            gemm16<kTok, D>(tmem + kTmemS + tile * kTok, base + kOffQ + tile * kQBytes, base + kOffK + (i & 1) * kKBytes, false);
-            arrive(bar(kSFull + tile));
-            commit(bar(kSFull + tile));
-        };
-        if (go) {
-            fence_after_sync();
-            for (int tile = 0; tile < tiles; ++tile) qk(tile, 0);
-            commit(bar(kKFree));
-        }
-        for (int i = 0; i < steps && go; ++i) {
-            const bool next = i + 1 < steps;
-            if (next) go = wait(kKFull + ((i + 1) & 1), ((i + 1) >> 1) & 1);
-            for (int tile = 0; tile < tiles && go; ++tile) {
-                if (next) {
-                    go = wait(kSFree + tile, i & 1);
+        // A warp for each tile's scores and one for each tile's sums: issuing a product takes as long as it runs,
+        // and waits cost hundreds of cycles, so one thread for all four left the tensor core idle two thirds of the time.
+        const int which = warp - (2 * kSoft + kLoad) / 32, tile = which & 1;
+        if (lane == 0 && tile < tiles && steps > 0) {
+            bool go = true;
+            if (which < 2) {
+                go = wait(kQFull, 0);
+                for (int i = 0; i < steps && go; ++i) {
+                    go = wait(kKFull + (i & 1), (i >> 1) & 1);
+                    if (go && i > 0) go = wait(kSFree + tile, (i - 1) & 1);
                     if (!go) break;
                     fence_after_sync();
-                    qk(tile, i + 1);
-                    if (tile == tiles - 1) commit(bar(kKFree + ((i + 1) & 1)));
+                    gemm16<kTok, D>(tmem + kTmemS + tile * kTok, base + kOffQ + tile * kQBytes, base + kOffK + (i & 1) * kKBytes, false);
+                    arrive(bar(kSFull + tile));
+                    commit(bar(kSFull + tile));
+                    commit(bar(kKFree + (i & 1)));
                 }
-                go = wait(kPFull + tile, i & 1) && (tile > 0 || wait(kVFull + (i & 1), (i >> 1) & 1));
-                if (!go) break;
-                fence_after_sync();
-                gemm16_ts<D, kTok>(tmem + kTmemO + tile * D, tmem + kTmemP + tile * (kTok / 2), base + kOffV + (i & 1) * kVBytes, i > 0);
-                commit(bar(kPvDone + tile));
+            } else {
+                for (int i = 0; i < steps && go; ++i) {
+                    go = wait(kVFull + (i & 1), (i >> 1) & 1);
+                    if (go) go = wait(kPFull + tile, i & 1);
+                    if (!go) break;
+                    fence_after_sync();
+                    gemm16_ts<D, kTok>(tmem + kTmemO + tile * D, tmem + kTmemP + tile * (kTok / 2), base + kOffV + (i & 1) * kVBytes, i > 0);
+                    commit(bar(kPvDone + tile));
+                    commit(bar(kVFree + (i & 1)));
+                }
             }
-            if (go) commit(bar(kVFree + (i & 1)));
-        }
-        if (!go) {                                    // what was issued has to end before its memory is given up
-            commit(bar(kDrain));
-            mbar_wait(bar(kDrain), 0, kPolls);
+            if (!go) {                                // what was issued has to end before its memory is given up
+                commit(bar(kDrain + which));
+                keep_waiting(bar(kDrain + which), 0, &s_never, nullptr);
+            }
         }
     }
     __syncwarp();
