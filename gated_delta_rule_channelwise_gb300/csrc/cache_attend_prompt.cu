@@ -38,8 +38,8 @@ constexpr uint32_t kPolls = POLLS;                    // of a wait, before it gi
 
 constexpr int kQBytes = kTile * D * 2, kKBytes = kTok * D * 2, kVBytes = D * kTok * 2;
 constexpr int kOffQ = 0, kOffK = 2 * kQBytes, kOffV = kOffK + 2 * kKBytes, kOffRaw = kOffV + 2 * kVBytes;
-constexpr int kOffScale = kOffRaw + kRawStages * kRaw;                // float4 [4][kGroups]: ring of four steps
-constexpr int kOffRawScale = kOffScale + 4 * kGroups * 16;            // float2 [kRawStages][kGroups]: scales as copied
+constexpr int kOffScale = kOffRaw + kRawStages * kRaw;                // float2 [4][kGroups]: ring of four steps
+constexpr int kOffRawScale = kOffScale + 4 * kGroups * 8;            // float2 [kRawStages][kGroups]: scales as copied
 constexpr int kOffBar = kOffRawScale + kRawStages * kGroups * 8;
 enum Bar { kQFull, kKFull, kKFree = kKFull + 2, kVFull = kKFree + 2, kVFree = kVFull + 2, kSFull = kVFree + 2, kSFree = kSFull + 2,
            kPFull = kSFree + 2, kPvDone = kPFull + 2, kDrain = kPvDone + 2, kBars = kDrain + 4 };
@@ -47,6 +47,11 @@ constexpr int kBytes = kOffBar + kBars * 8 + 1024;    // and the room to align t
 
 constexpr int kTmemO = 0, kTmemS = 2 * D, kTmemP = kTmemS + 2 * kTok, kTmemCols = 512;
 
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -204,11 +209,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                 float iv[kGroups];
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    float4 sc;
-                    const uint4 raw = lds128(base + kOffScale + ((i & 3) * kGroups + g) * 16);
-                    sc = make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z), 0.f);
-                    iv[g] = sc.z;
-                    const f32x2 c = both(sc.x * scale), lv = both(sc.y);
+                    float ks, vs;
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(base + kOffScale + ((i & 3) * kGroups + g) * 8));
+                    // a scale that is (as good as) zero: the values are zero, whatever the bytes; below zero: no page
+                    const bool zero = vs < 0x1p-100f;
+                    iv[g] = zero ? -1.f : rcp(vs);
+                    const f32x2 c = both(ks * scale), lv = both(vs < 0.f ? -INFINITY : zero ? 0.f : lg2(vs));
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         const float2 y = split(fma2(pair(x[16 * g + e], x[16 * g + e + 1]), c, lv));
@@ -306,56 +312,57 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
         const int t = tid - 2 * kSoft, w = t >> 5;
         // Nothing here waits for a load in the step that issues it: page numbers are looked at a step after they
         // are asked for, and scales come with the copies.
-        int page[kGroups];                            // table entries of the step to be copied next
+        int page = -1;                                // lanes 0 .. 3: table entry of that group of the step to be copied next
         auto look = [&](int i) {
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int pos = i * kTok + 16 * g;
-                const int64_t at = b * p.table_sb + (pos >> p.shift);
-                page[g] = -1;
-                if (pos < end && in_bounds(at, p.e_table, p.status, nullptr)) page[g] = __ldg(p.table + at);
-            }
+            const int pos = i * kTok + 16 * lane;
+            const int64_t at = b * p.table_sb + (pos >> p.shift);
+            page = -1;
+            if (lane < kGroups && pos < end && in_bounds(at, p.e_table, p.status, nullptr)) page = __ldg(p.table + at);
         };
-        auto copy = [&](int i) {                      // step i's bytes and scales; its pages are in `page`
+        // this thread's 16 bytes of a group: of token t / 8, piece t % 8 (the swizzle depends on the token modulo 8)
+        const int64_t unit_bytes = (int64_t)D << p.shift, page_bytes = unit_bytes * p.Hkv;
+        const int8_t *kc = p.kc + hk * unit_bytes + t * 16, *vc = p.vc + hk * unit_bytes + t * 16;
+        const uint32_t mine = base + kOffRaw + (t >> 3) * D + ((t & 7) ^ raw_swizzle(t >> 3)) * 16;
+        auto copy = [&](int i, int stage) {           // step i's bytes and scales; its pages are in `page`
             if (i < steps) {
-                const uint32_t dst = base + kOffRaw + i % kRawStages * kRaw;
+                if (page >= p.num_pages) page = -1;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    const bool ok = page[g] >= 0 && page[g] < p.num_pages;
-                    if (ok) {
-                        const int token = 16 * g + (t >> 3), piece = t & 7;
-                        const int64_t unit = (int64_t)page[g] * p.Hkv + hk;
-                        const int64_t src = ((unit << p.shift) + ((i * kTok + token) & (p.page - 1))) * D + piece * 16;
-                        const uint32_t to = dst + token * D + (piece ^ raw_swizzle(token)) * 16;
-                        cp_async16(to, p.kc + src, true);
-                        cp_async16(to + kTok * D, p.vc + src, true);
+                    const int pg = __shfl_sync(0xffffffffu, page, g);
+                    if (pg >= 0) {
+                        const int64_t src = pg * page_bytes + ((i * kTok + 16 * g) & (p.page - 1)) * D;
+                        const uint32_t to = mine + stage * kRaw + 16 * g * D;
+                        cp_async16(to, kc + src, true);
+                        cp_async16(to + kTok * D, vc + src, true);
                     }
-                    if (t == g) {                     // k's scale, then v's; below zero: no page
-                        const uint32_t to = base + kOffRawScale + (i % kRawStages * kGroups + g) * 8;
-                        if (ok) {
-                            cp_async4(to, p.ks + (int64_t)page[g] * p.Hkv + hk, true);
-                            cp_async4(to + 4, p.vs + (int64_t)page[g] * p.Hkv + hk, true);
-                        } else {
-                            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(0.f), "f"(-1.f) : "memory");
-                            if (i * kTok + 16 * g < end) report(p.status, (int)CGDR_ERR_BOUNDS);
-                        }
+                }
+                if (t < kGroups) {                    // k's scale, then v's; below zero: no page
+                    const uint32_t to = base + kOffRawScale + (stage * kGroups + t) * 8;
+                    if (page >= 0) {
+                        cp_async4(to, p.ks + (int64_t)page * p.Hkv + hk, true);
+                        cp_async4(to + 4, p.vs + (int64_t)page * p.Hkv + hk, true);
+                    } else {
+                        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(0.f), "f"(-1.f) : "memory");
+                        if (i * kTok + 16 * t < end) report(p.status, (int)CGDR_ERR_BOUNDS);
                     }
                 }
             }
             cp_async_commit();
         };
+        int stage = 0;                                // of raw bytes: i modulo 3
         look(0);
-        copy(0);
+        copy(0, 0);
         look(1);
-        copy(1);
+        copy(1, 1);
         look(2);
         bool go = true;
         for (int i = 0; i < steps; ++i) {             // every warp takes part in every step's barrier, even when a wait gave up
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             named_bar_sync<1, kLoad>();               // everybody's copies of step i, and their reads of step i - 1
-            copy(i + 2);
+            copy(i + 2, stage == 0 ? 2 : stage - 1);
             look(i + 3);
-            const uint32_t raw = base + kOffRaw + i % kRawStages * kRaw;
+            const uint32_t raw = base + kOffRaw + stage * kRaw, raw_scale = base + kOffRawScale + (stage * kGroups + t) * 8;
+            stage = stage == kRawStages - 1 ? 0 : stage + 1;
             const int st = i & 1;
             uint4 kv4[4];                             // 16 bytes of four keys
 #pragma unroll
@@ -368,12 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
             // (the softmax threads have left step i - 4 behind: the products of step i - 2 are done, which were issued
             // after they had read s of step i - 3)
             if (t < kGroups) {
-                // k's scale, and log2 and reciprocal of v's: 0 and -1 where that is (as good as) zero; no page: -inf
-                float ks, vs;
-                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(base + kOffRawScale + (i % kRawStages * kGroups + t) * 8));
-                const bool zero = vs < 0x1p-100f, none = vs < 0.f;
-                sts128(base + kOffScale + ((i & 3) * kGroups + t) * 16, __float_as_uint(ks),
-                       __float_as_uint(none ? -INFINITY : zero ? 0.f : log2f(vs)), __float_as_uint(zero ? -1.f : 1.f / vs), 0);
+                uint32_t ks, vs;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(ks), "=r"(vs) : "r"(raw_scale));
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(base + kOffScale + ((i & 3) * kGroups + t) * 8), "r"(ks), "r"(vs) : "memory");
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {             // two 16-byte pieces of a key's fp16 row each
