@@ -297,8 +297,8 @@ def validate(A: CgdrArgs, for_prefill: bool) -> int:
     return int(lib().cgdr_validate(ctypes.byref(A), 1 if for_prefill else 0))
 
 
-from .serve import (CachePlan, SIGNATURES, cache_append, cache_attend, cache_attend_workspace_size,  # noqa: E402
-                    cache_plan, conv_decode, conv_prefill, scan_decode, scan_prefill, scan_workspace_size)
+from .serve import (ATTEND_AUTO, ATTEND_ROWS, ATTEND_TILES, CachePlan, SIGNATURES, cache_append,  # noqa: E402
+                    cache_attend, cache_attend_workspace_size, cache_plan, conv_decode, conv_prefill, scan_decode, scan_prefill, scan_workspace_size)
 
 __all__ = ["decode", "prefill", "prefill_noalloc", "prefill_workspace_size", "workspace_status", "validate",
            "status_string", "make_args", "prefill_path_for",

@@ -603,19 +603,23 @@ int tile_of(const cgdr_attend_args &a) {
 int64_t most_of(const cgdr_attend_args &a) {
     return a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page;
 }
+int64_t steps_of(const cgdr_attend_args &a) {         // of a unit at most
+    const int64_t kv = most_of(a);
+    return kv > 0 ? (kv + kBlockStep - 1) / kBlockStep : 1;
+}
 // Blocks of the first kernel: all that fit, but no more than shares of kMinShare steps need.
 template <int D, int NQ, typename T>
 int blocks_of(const cgdr_attend_args &a) {
     const int64_t sms = device_sms() > 0 ? device_sms() : 152;       // sizes workspaces without a device, too
-    const int64_t tiles = ((int64_t)a.max_q * (a.Hq / a.Hkv) + 8 * NQ - 1) / (8 * NQ), kv = most_of(a);
-    const int64_t steps = kv > 0 ? (kv + kBlockStep - 1) / kBlockStep : 1, most = sms * AttendShape<D, NQ, T>::BLOCKS;
-    const int64_t need = ((int64_t)a.B * a.Hkv * tiles * steps + kMinShare - 1) / kMinShare;
+    const int64_t tiles = ((int64_t)a.max_q * (a.Hq / a.Hkv) + 8 * NQ - 1) / (8 * NQ);
+    const int64_t most = sms * AttendShape<D, NQ, T>::BLOCKS;
+    const int64_t need = ((int64_t)a.B * a.Hkv * tiles * steps_of(a) + kMinShare - 1) / kMinShare;
     return (int)(need < most ? need : most);
 }
 template <int D, int NQ, typename T>
 size_t workspace_for(const cgdr_attend_args &a) {
     const int blocks = blocks_of<D, NQ, T>(a);
-    return blocks > 1 ? (size_t)2 * blocks * 8 * NQ * (D + 2) * sizeof(float) : 0;
+    return blocks > 1 && steps_of(a) > 1 ? (size_t)2 * blocks * 8 * NQ * (D + 2) * sizeof(float) : 0;
 }
 
 template <int D, int NQ, typename T>
@@ -626,9 +630,9 @@ cgdr_status launch_attend(const cgdr_attend_args &a, AttendParams &p, float *ws,
     if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_kernel<D, NQ, T>), kBytes)) return CGDR_ERR_CUDA;
     p.blocks = blocks_of<D, NQ, T>(a);
     p.part = ws;
-    p.ml = ws + (size_t)2 * p.blocks * p.tile * D;
+    p.ml = ws != nullptr ? ws + (size_t)2 * p.blocks * p.tile * D : nullptr;
     cache_attend_kernel<D, NQ, T><<<p.blocks, 32 * kWarps, kBytes, s>>>(p);
-    if (p.blocks > 1) {
+    if (p.blocks > 1 && steps_of(a) > 1) {            // units of one step are never in parts
         if (cudaPeekAtLastError() != cudaSuccess) return launched();
         const int64_t all = (int64_t)a.max_q * p.G, tiles = (all + p.tile - 1) / p.tile, rows = all < p.tile ? all : p.tile;
         // begins while the first kernel ends, finds its unit, and waits for that kernel's parts
@@ -668,10 +672,10 @@ cgdr_status launch_of(const cgdr_attend_args &a, AttendParams &p, float *ws, cud
 cgdr_status check(const cgdr_attend_args *a) {
     if (!a) return CGDR_ERR_INVALID_ARG;
     if (a->B < 0 || a->n < 0 || a->Hq <= 0 || a->Hkv <= 0 || a->Hq % a->Hkv != 0 || a->width < 0 || a->num_pages < 0 ||
-        a->max_q < 0 || a->max_kv < 0)
+        a->max_q < 0 || a->max_kv < 0 || a->path < CGDR_ATTEND_AUTO || a->path > CGDR_ATTEND_TILES)
         return CGDR_ERR_INVALID_ARG;
     if (!dtype_ok(a->dtype) || !page_ok(a->page) || (a->D != 32 && a->D != 64 && a->D != 128)) return CGDR_ERR_UNSUPPORTED;
-    if (a->B > 65535 || a->n > kMaxTokens || a->max_kv > kMaxKv) return CGDR_ERR_UNSUPPORTED;
+    if (a->B > 65535 || a->n > kMaxTokens || a->max_kv >= kMaxKv) return CGDR_ERR_UNSUPPORTED;
     if (((int64_t)a->max_q * (a->Hq / a->Hkv) + kRows) * a->Hkv > INT32_MAX) return CGDR_ERR_UNSUPPORTED;
     if (a->B == 0 || a->n == 0 || a->max_q == 0) return CGDR_OK;
     if (!a->q || !a->o || !a->kv_lens || !a->cu) return CGDR_ERR_INVALID_ARG;

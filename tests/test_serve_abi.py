@@ -45,7 +45,8 @@ PLAN = dict(B=2, width=8, page=16, n_tokens=4, F=3, num_pages=99, block_table=P,
             requests=9 * P, positions=10 * P, slots=11 * P, status=0)
 APPEND = dict(n=3, Hkv=2, D=64, page=16, dtype=cg.BF16, num_pages=9, k=P, k_st=128, k_sh=64, v=2 * P, v_st=128, v_sh=64,
               slots=3 * P, k_cache=4 * P, v_cache=5 * P, k_scale=6 * P, v_scale=7 * P, status=0)
-ATTEND = dict(B=2, n=2, Hq=4, Hkv=2, D=64, page=16, width=8, dtype=cg.BF16, num_pages=9, max_q=1, max_kv=100, scale=0.0,
+ATTEND = dict(B=2, n=2, Hq=4, Hkv=2, D=64, page=16, width=8, dtype=cg.BF16, num_pages=9, max_q=1, max_kv=100, path=0,
+              reserved=0, scale=0.0,
               q=P, q_st=256, q_sh=64, o=2 * P, o_st=256, o_sh=64, k_cache=3 * P, v_cache=4 * P, k_scale=5 * P,
               v_scale=6 * P, block_table=7 * P, table_sb=8, kv_lens=8 * P, cu=9 * P, status=0)
 
@@ -83,7 +84,7 @@ INV, UNS, ALN = cg.ERR_INVALID_ARG, cg.ERR_UNSUPPORTED, cg.ERR_ALIGNMENT
     ("append", APPEND, dict(n=-1), INV), ("append", APPEND, dict(Hkv=0), INV), ("append", APPEND, dict(v_scale=0), INV),
     ("append", APPEND, dict(D=96), UNS), ("append", APPEND, dict(page=8), UNS), ("append", APPEND, dict(dtype=9), UNS),
     ("append", APPEND, dict(k=P + 8), ALN), ("append", APPEND, dict(v_sh=60), ALN), ("append", APPEND, dict(k_cache=P + 8), ALN),
-    ("attend", ATTEND, dict(Hq=3), INV), ("attend", ATTEND, dict(max_q=-1), INV), ("attend", ATTEND, dict(q=0), INV),
+    ("attend", ATTEND, dict(Hq=3), INV), ("attend", ATTEND, dict(path=3), INV), ("attend", ATTEND, dict(path=-1), INV), ("attend", ATTEND, dict(max_q=-1), INV), ("attend", ATTEND, dict(q=0), INV),
     ("attend", ATTEND, dict(cu=0), INV), ("attend", ATTEND, dict(block_table=0), INV), ("attend", ATTEND, dict(table_sb=4), INV),
     ("attend", ATTEND, dict(D=256), UNS), ("attend", ATTEND, dict(page=24), UNS), ("attend", ATTEND, dict(max_kv=1 << 30), UNS),
     ("attend", ATTEND, dict(q_st=4), ALN), ("attend", ATTEND, dict(v_cache=P + 4), ALN), ("attend", ATTEND, dict(o_sh=-1), ALN),
@@ -115,6 +116,10 @@ def test_workspace_sizes(lib):
     assert cg.scan_workspace_size(1, 16384, 64, 16) > 0
     assert cg.cache_attend_workspace_size(1, 1, 32, 8, 128, 64, 2048, max_q=1) > 0
     assert cg.cache_attend_workspace_size(64, 64, 32, 8, 128, 64, 2, max_q=1) == 0
+    big = dict(max_q=2000, max_kv=4000)                                       # enough rows: tiles, which need none
+    assert cg.cache_attend_workspace_size(4, 8000, 32, 8, 128, 64, 64, **big) == 0
+    assert cg.cache_attend_workspace_size(4, 8000, 32, 8, 128, 64, 64, path=cg.ATTEND_ROWS, **big) > 0
+    assert cg.cache_attend_workspace_size(4, 8000, 32, 8, 64, 64, 64, path=cg.ATTEND_TILES, **big) > 0    # D = 64: rows
     assert cg.status_string(cg.ERR_CAPACITY).startswith("CGDR_ERR_CAPACITY")
 
 

@@ -371,6 +371,48 @@ def test_attend_several_tokens(dtype, q_lens, kv_lens, Hq, Hkv, D):
         at += ql
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv,page", [
+    ([1], [1], 1, 1, 16), ([70], [70], 1, 1, 64), ([33, 0, 70], [40, 9, 71], 4, 2, 16), ([300], [1000], 2, 1, 128),
+    ([130, 5, 1], [130, 600, 350], 3, 1, 32), ([150, 1], [150, 20], 4, 2, 64), ([200, 3], [50, 0], 2, 2, 16),
+    ([65, 129], [127, 193], 2, 1, 64), ([90], [4097], 8, 1, 16)])
+def test_attend_tiles(q_lens, kv_lens, Hq, Hkv, page):
+    """The tensor-memory kernel: one and two row tiles, ragged ends, pages smaller and larger than a step, blind rows."""
+    case = attend_case(sum(q_lens) + page, q_lens, kv_lens, Hq, Hkv, 128, page, BF)
+    o = check_attend(case, BF, path=cg.ATTEND_TILES)
+    at = 0
+    for ql, kv in zip(q_lens, kv_lens):
+        assert not o[at:at + max(0, ql - kv)].any()
+        at += ql
+    other = cg.cache_attend(*case, max_q=max(q_lens), path=cg.ATTEND_ROWS)
+    close(other, o.cpu(), float(o.float().abs().max()) * 2.0 ** -8, BF)
+
+
+def test_attend_tiles_scales_and_non_finite_values():
+    """Scales of many magnitudes, zeros, pages outside the cache, NaN scales that no row sees, a NaN query row."""
+    case = list(attend_case(40, [140], [333], 2, 1, 128, 16, BF))
+    q, kc, vc, ks, vs, table, kv, cu = case
+    vs *= 10.0 ** torch.linspace(-12, 3, vs.numel(), device=DEV).view_as(vs)
+    vs[3], vs[7] = 0, 0
+    ks[5] = 0
+    first = check_attend(tuple(case), BF, path=cg.ATTEND_TILES)
+    used = set(table[table >= 0].tolist())
+    for p in set(range(kc.shape[0])) - used:
+        ks[p], vs[p] = float("nan"), float("inf")
+    q[7, 1] = float("nan")
+    again = cg.cache_attend(*case, max_q=140, path=cg.ATTEND_TILES)
+    assert torch.isnan(again[7, 1]).all()
+    again[7, 1] = first[7, 1]
+    assert torch.equal(again, first)
+    bad, status = table.clone(), torch.zeros(1, dtype=torch.int32, device=DEV)
+    bad[0, 2], bad[0, 9] = -3, kc.shape[0]
+    o = cg.cache_attend(q, kc, vc, ks, vs, bad, kv, cu, max_q=140, path=cg.ATTEND_TILES, status=status)
+    assert int(status) == cg.ERR_BOUNDS
+    rows = cg.cache_attend(q, kc, vc, ks, vs, bad, kv, cu, max_q=140, path=cg.ATTEND_ROWS)
+    ok = torch.ones_like(o, dtype=torch.bool)
+    ok[7, 1] = False
+    close(o[ok], rows[ok].cpu(), float(rows[ok].float().abs().max()) * 2.0 ** -8, BF)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_attend_long_cache_is_split_and_joined(dtype):
     check_attend(attend_case(5, [1, 1], [6000, 4097], 4, 2, 64, 16, dtype), dtype)
