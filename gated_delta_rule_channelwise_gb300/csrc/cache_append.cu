@@ -52,17 +52,18 @@ __device__ __forceinline__ uint32_t quantised4(const float *f, float by, float i
     return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
-// One run by a warp, or (kBlock) by the block: tokens i .. i + len - 1 into the page of `slot` from its
-// offset on.
+// One run by a warp, or (kBlock) by the block: tokens from i on into the page of `slot` from its offset on, up to the
+// first token that is not on the next slot.  The values that a run of the greatest length would have are
+// asked for before its length is known.
 template <typename T, bool kBlock>
-__device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t slot, int len, int h, int which, float *s_max) {
+__device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t slot, int h, int which, float *s_max) {
     constexpr int V = Vec<T>::n, NT = kBlock ? kAppendThreads : 32, kKeep = 4;
     const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
     const int off = (int)(slot % p.page);
     const int64_t unit = (slot / p.page) * p.Hkv + h;                 // the page's block of this head
     int8_t *dst = p.cache[which] + unit * p.page * p.D;
     const T *x = static_cast<const T *>(p.x[which]);
-    const int per = p.D / V, vecs = len * per;
+    const int per = p.D / V, most = min(p.page - off, p.n - i);       // a page has 128 tokens at most
     auto vec = [&](int e) {
         const int64_t at = (int64_t)(i + e / per) * p.st[which] + h * p.sh[which] + (e % per) * V;
         return range_in_bounds(at, V, p.ex[which], p.status, nullptr) ? __ldg(reinterpret_cast<const uint4 *>(x + at))
@@ -72,7 +73,15 @@ __device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t
 
     uint4 kept[kKeep];
 #pragma unroll
-    for (int k = 0; k < kKeep; ++k) kept[k] = tid + k * NT < vecs ? vec(tid + k * NT) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kKeep; ++k) kept[k] = tid + k * NT < most * per ? vec(tid + k * NT) : make_uint4(0, 0, 0, 0);
+    int len = most;
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {
+        const int t = (tid & 31) + 32 * k;
+        if (t < most && p.slots[i + t] != slot + t) len = t;
+    }
+    len = __reduce_min_sync(0xffffffffu, len);
+    const int vecs = len * per;
     float top = 0.f;
     auto over = [&](const uint4 &r) {
         float f[V];
@@ -81,7 +90,8 @@ __device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t
         for (int j = 0; j < V; ++j) top = max_nan(top, fabsf(f[j]));
     };
 #pragma unroll
-    for (int k = 0; k < kKeep; ++k) over(kept[k]);
+    for (int k = 0; k < kKeep; ++k)
+        if (tid + k * NT < vecs) over(kept[k]);
     for (int e = tid + kKeep * NT; e < vecs; e += NT) over(vec(e));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -136,8 +146,9 @@ template <typename T>
 __global__ void __launch_bounds__(kAppendThreads, 6) cache_append_kernel(const AppendParams p) {
     constexpr int NW = kAppendThreads / 32;
     __shared__ int s_start[kAppendThreads], s_count;
+    __shared__ int64_t s_slot[kAppendThreads];
     __shared__ float s_max[NW];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y, which = blockIdx.z;
+    const int tid = threadIdx.x, warp = tid >> 5, h = blockIdx.y, which = blockIdx.z;
     const int i0 = blockIdx.x * p.window;
     const int64_t slots = (int64_t)p.num_pages * p.page;
     if (tid == 0) s_count = 0;
@@ -148,33 +159,32 @@ __global__ void __launch_bounds__(kAppendThreads, 6) cache_append_kernel(const A
         if (slot >= slots && h == 0 && which == 0 && p.status != nullptr) atomicExch(p.status, (int)CGDR_ERR_BOUNDS);
         // a run begins where a page does, or where the token before is on another slot
         if (slot >= 0 && slot < slots && (slot % p.page == 0 || i == 0 || p.slots[i - 1] != slot - 1))
-            s_start[atomicAdd(&s_count, 1)] = i;      // in any order: runs share nothing
+        {
+            const int at = atomicAdd(&s_count, 1);    // in any order: runs share nothing
+            s_start[at] = i;
+            s_slot[at] = slot;
+        }
     }
     __syncthreads();
     const int runs = s_count;
     const bool alone = runs < NW;                     // the block on one run at a time
     for (int r = alone ? 0 : warp; r < runs; r += alone ? 1 : NW) {
         const int i = s_start[r];
-        const int64_t slot = p.slots[i];
-        const int most = min(p.page - (int)(slot % p.page), p.n - i);
-        int len = most;                               // up to the first token that is not on the next slot
-        for (int t = lane; t < most; t += 32)
-            if (p.slots[i + t] != slot + t) { len = t; break; }
-        len = __reduce_min_sync(0xffffffffu, len);
-        if (alone) append_run<T, true>(p, i, slot, len, h, which, s_max);
-        else append_run<T, false>(p, i, slot, len, h, which, s_max);
+        const int64_t slot = s_slot[r];
+        if (alone) append_run<T, true>(p, i, slot, h, which, s_max);
+        else append_run<T, false>(p, i, slot, h, which, s_max);
     }
 }
 
 // Tokens of a block's window: one where there are few tokens, so that each has a block; up to 64 (a
-// prompt's window then holds a run or two), as long as there are eight blocks to an SM.
+// prompt's window then holds a run or two), as long as there are four blocks to an SM.
 template <typename T>
 cgdr_status launch_append(AppendParams &p, cudaStream_t s) {
     const int sms = device_sms();
     if (sms <= 0) return CGDR_ERR_CUDA;
     const int64_t units = 2 * (int64_t)p.Hkv;
     p.window = kAppendThreads / 32;
-    while (p.window < 64 && p.n * units >= 16 * (int64_t)sms * p.window) p.window *= 2;
+    while (p.window < 64 && p.n * units >= 8 * (int64_t)sms * p.window) p.window *= 2;
     cache_append_kernel<T><<<dim3((p.n + p.window - 1) / p.window, p.Hkv, 2), kAppendThreads, 0, s>>>(p);
     return launched();
 }

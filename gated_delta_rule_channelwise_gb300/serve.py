@@ -15,7 +15,6 @@ allocator; with ``stream`` they are allocated on that stream.
 from __future__ import annotations
 
 import ctypes
-import dataclasses
 import struct
 
 import torch
@@ -287,21 +286,29 @@ def scan_workspace_size(B, T, C, N, G=1, *, n_tokens=None, dtype=torch.bfloat16)
 # --------------------------------------------------------------------------- 8-bit cache
 
 
-@dataclasses.dataclass
 class CachePlan:
-    """What :func:`cache_plan` writes: see there."""
-    slots: torch.Tensor         # [n] int64
-    kv_lens: torch.Tensor       # [B] int32
-    cu_seqlens: torch.Tensor    # [B + 1] int32
-    free_count: torch.Tensor    # [1] int32
-    requests: torch.Tensor      # [n] int32
-    positions: torch.Tensor     # [n] int32
+    """What :func:`cache_plan` writes: see there.  One buffer holds it all; it is cut into tensors when one of
+    them is first asked for, all at once (a view each costs as much as checking a call's arguments)."""
 
-    @classmethod
-    def empty(cls, B, n_tokens, device="cuda"):
-        words = torch.empty(2 * B + 2 + 2 * n_tokens, dtype=torch.int32, device=device)
-        kv, cu, count, req, pos = words.split([B, B + 1, 1, n_tokens, n_tokens])
-        return cls(torch.empty(n_tokens, dtype=torch.int64, device=device), kv, cu, count, req, pos)
+    def __init__(self, B, n_tokens, device="cuda"):
+        self.B, self.n_tokens = B, n_tokens
+        # slots first (int64), then int32 words: kv_lens, cu_seqlens, free_count, requests, positions
+        self._buffer = torch.empty(n_tokens + B + 1 + n_tokens, dtype=torch.int64, device=device)
+        slots = self._buffer.data_ptr()
+        kv = slots + 8 * n_tokens
+        count = kv + 4 * (2 * B + 1)
+        self._addresses = count, kv, kv + 4 * B, count + 4, count + 4 + 4 * n_tokens, slots
+
+    def __getattr__(self, name):
+        parts = {"slots": "[n] int64", "kv_lens": "[B] int32", "cu_seqlens": "[B + 1] int32", "free_count": "[1] int32",
+                 "requests": "[n] int32", "positions": "[n] int32"}
+        if name not in parts:
+            raise AttributeError(name)
+        B, n = self.B, self.n_tokens
+        self.slots = self._buffer[:n]
+        _, self.kv_lens, self.cu_seqlens, self.free_count, self.requests, self.positions = \
+            self._buffer.view(_I32).unsafe_split_with_sizes((2 * n, B, B + 1, 1, n, n))
+        return self.__dict__[name]
 
 
 def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens, page, out=None, *, num_pages=None,
@@ -309,7 +316,8 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
     """Block tables and slots of a step, on the device.  Request b holds ``seq_lens[b]`` cached tokens in
     the first pages of its row of ``block_table [B,width]`` and gets ``new_lens[b]`` more; the pages it
     needs come off the top of the stack ``free_pages[:free_count]``, in request order, and are entered into
-    block_table (in place).  All int32.  Returns a :class:`CachePlan` (``out``, or a new one):
+    block_table (in place).  All int32.  Returns a :class:`CachePlan` (``out``, or a new one; its ``kv_lens`` and
+    ``free_count`` are the next step's ``seq_lens`` and ``free_count``, so steps that reuse buffers take turns with two):
 
     ``cu_seqlens`` prefix sums of new_lens; ``kv_lens = seq_lens + new_lens``; per packed new token its
     ``requests``, ``positions`` (place in the request) and ``slots`` (int64 ``page_number * page + place in
@@ -325,15 +333,9 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
     B, width = block_table.shape
     F = free_pages.numel()
     if out is None:
-        out = CachePlan.empty(B, n_tokens, block_table.device)
-    else:
-        _need_cuda(out.slots, out.kv_lens, out.cu_seqlens, out.free_count, out.requests, out.positions)
-        written = [("kv_lens", B), ("cu_seqlens", B + 1), ("free_count", 1), ("requests", n_tokens), ("positions", n_tokens),
-                   ("slots", n_tokens)]
-        if not all(_fits(getattr(out, name), torch.int64 if name == "slots" else _I32, (size,)) for name, size in written):
-            named = [("out." + name, getattr(out, name), size) for name, size in written]
-            _refuse([(name, t, _I32) for name, t, _ in named[:-1]] + [("out.slots", out.slots, torch.int64)],
-                    [(name, t, (size,)) for name, t, size in named], [(name, t) for name, t, _ in named])
+        out = CachePlan(B, n_tokens, block_table.device)
+    elif out.B != B or out.n_tokens != n_tokens:
+        raise ValueError("out is a plan of %d requests and %d tokens, not of %d and %d" % (out.B, out.n_tokens, B, n_tokens))
     if not (block_table.dtype == _I32 and _fits(seq_lens, _I32, (B,)) and _fits(new_lens, _I32, (B,))
             and _fits(free_pages, _I32, (F,)) and _fits(free_count, _I32, (1,))):
         named = [("seq_lens", seq_lens, B), ("new_lens", new_lens, B), ("free_pages", free_pages, F), ("free_count", free_count, 1)]
@@ -344,9 +346,7 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
         raise ValueError("block_table: innermost dimension must be contiguous")
     block = PLAN.pack(B, width, page, n_tokens, F, 0x7FFFFFFF if num_pages is None else num_pages,
                       block_table.data_ptr(), sb, seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
-                      free_count.data_ptr(), out.free_count.data_ptr(), out.kv_lens.data_ptr(),
-                      out.cu_seqlens.data_ptr(), out.requests.data_ptr(), out.positions.data_ptr(),
-                      out.slots.data_ptr(), _status_word(status))
+                      free_count.data_ptr(), *out._addresses, _status_word(status))
     _check(lib().cgdr_cache_plan(block, _current(block_table.get_device())), "cgdr_cache_plan")
     return out
 
