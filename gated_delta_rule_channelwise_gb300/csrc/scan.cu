@@ -405,10 +405,11 @@ template <> __device__ __forceinline__ float4 four<__nv_bfloat16>(const __nv_bfl
 template <typename T, int N>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanParams p) {
     constexpr int LPC = N / 4;
-    const int64_t unit = (int64_t)blockIdx.x * (kStepThreads / LPC) + threadIdx.x / LPC;
-    const int q = threadIdx.x % LPC;
-    const bool live = unit < (int64_t)p.B * p.C;
-    const int b = live ? (int)(unit / p.C) : 0, c = live ? (int)(unit % p.C) : 0, g = c / p.Cg;
+    const int q = threadIdx.x % LPC, b = blockIdx.y;
+    int c = blockIdx.x * (kStepThreads / LPC) + threadIdx.x / LPC;
+    const bool live = c < p.C;
+    if (!live) c = 0;
+    const int g = p.G == 1 ? 0 : c / p.Cg;
     float *hs = p.state + ((int64_t)b * p.C + c) * N + 4 * q;
     float4 h = *reinterpret_cast<const float4 *>(hs);
     const float4 a = __ldg(reinterpret_cast<const float4 *>(p.A_log + (int64_t)c * N + 4 * q));
@@ -474,8 +475,8 @@ int64_t slots_of(const cgdr_scan_args &a, int chunk) {
 template <typename T, int N>
 cgdr_status launch_scan(const cgdr_scan_args &a, ScanParams &p, cudaStream_t s) {
     if (!a.cu && a.T == 1) {
-        const int64_t units = (int64_t)a.B * a.C, per = kStepThreads / (N / 4);
-        scan_step_kernel<T, N><<<(unsigned)((units + per - 1) / per), kStepThreads, 0, s>>>(p);
+        constexpr int per = kStepThreads / (N / 4);
+        scan_step_kernel<T, N><<<dim3((a.C + per - 1) / per, a.B), kStepThreads, 0, s>>>(p);
         return launched();
     }
     using Sh = ScanShape<N>;
