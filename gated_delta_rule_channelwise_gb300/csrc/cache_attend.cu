@@ -97,7 +97,7 @@ struct AttendShape {                                                  // NQ: til
     static constexpr int RING = kWarps * kStages * STAGE;
     static constexpr int JOIN = kWarps * 8 * NQ * (D + 4) * 4;        // the warps' softmax states, in the ring's place
     static constexpr int BYTES = RING > JOIN ? RING : JOIN;
-    static constexpr int BLOCKS = (D == 128 ? 4 : 6) - NQ - (sizeof(T) == 4 ? 1 : 0); // of an SM, by shared memory and registers
+    static constexpr int BLOCKS = D == 128 ? (NQ == 1 && sizeof(T) == 2 ? 3 : 2) : 6 - NQ - (sizeof(T) == 4 ? 1 : 0); // of an SM, by registers
 };
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {          // an 8 x 8 tile of fp16 over the warp
@@ -479,45 +479,54 @@ __global__ void __launch_bounds__(32 * kWarps, AttendShape<D, NQ, T>::BLOCKS) ca
     extern __shared__ __align__(128) unsigned char smem[];              // copies of 512 bytes: misaligned to a line, each takes two
     __shared__ int64_t s_sum[NT / 32], s_at;
     __shared__ int s_b;
-    const Share share = share_of<NT>(p, s_sum);
-    int64_t left = share.size, at = share.size * blockIdx.x;          // steps to do, from this one of all on
-    if (left > share.total - at) left = share.total - at;
-    // the request of the first step, and the step in it: by prefix sums over groups of NT requests
-    if (threadIdx.x == 0) s_b = p.B;
-    for (int b0 = 0; left > 0 && b0 < p.B; b0 += NT) {
-        int64_t mine = 0;
-        if (b0 + threadIdx.x < p.B) {
-            const Request r = request(p, b0 + threadIdx.x);
-            mine = (int64_t)r.units * r.steps;
-        }
-        int64_t upto = mine;
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += x;
-        }
-        __syncthreads();
-        if (lane == 31) s_sum[warp] = upto;
-        __syncthreads();
-        int64_t group = 0;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) {
-            if (w < warp) upto += s_sum[w];
-            group += s_sum[w];
-        }
-        if (at < group) {
-            if (at < upto && at >= upto - mine) {
-                s_b = b0 + threadIdx.x;
-                s_at = at - (upto - mine);
+    int b;
+    int64_t left, at;                                 // steps to do, from this one of request b on
+    if (p.whole) {
+        b = blockIdx.y;
+        const Request r = request(p, b);
+        at = (int64_t)blockIdx.x * r.steps;
+        left = (int)blockIdx.x < r.units ? r.steps : 0;
+    } else {
+        const Share share = share_of<NT>(p, s_sum);
+        at = share.size * blockIdx.x;
+        left = min(share.size, share.total - at);
+        // the request of the first step, and the step in it: by prefix sums over groups of NT requests
+        if (threadIdx.x == 0) s_b = p.B;
+        for (int b0 = 0; left > 0 && b0 < p.B; b0 += NT) {
+            int64_t mine = 0;
+            if (b0 + threadIdx.x < p.B) {
+                const Request r = request(p, b0 + threadIdx.x);
+                mine = (int64_t)r.units * r.steps;
             }
-            break;
+            int64_t upto = mine;
+            const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += x;
+            }
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = upto;
+            __syncthreads();
+            int64_t group = 0;
+#pragma unroll
+            for (int w = 0; w < NT / 32; ++w) {
+                if (w < warp) upto += s_sum[w];
+                group += s_sum[w];
+            }
+            if (at < group) {
+                if (at < upto && at >= upto - mine) {
+                    s_b = b0 + threadIdx.x;
+                    s_at = at - (upto - mine);
+                }
+                break;
+            }
+            at -= group;
         }
-        at -= group;
+        __syncthreads();
+        b = s_b;
+        at = b < p.B ? s_at : 0;
     }
-    __syncthreads();
-    int b = s_b;
-    at = b < p.B ? s_at : 0;
     for (; b < p.B && left > 0; ++b) {
         const Request r = request(p, b);
         const int64_t all = (int64_t)r.units * r.steps;
@@ -531,7 +540,7 @@ __global__ void __launch_bounds__(32 * kWarps, AttendShape<D, NQ, T>::BLOCKS) ca
         at = at > all ? at - all : 0;
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < p.B; i += NT)
             if (cut(p, i)) report(p.status, (int)CGDR_ERR_CAPACITY);
 }
@@ -607,19 +616,43 @@ int64_t steps_of(const cgdr_attend_args &a) {         // of a unit at most
     const int64_t kv = most_of(a);
     return kv > 0 ? (kv + kBlockStep - 1) / kBlockStep : 1;
 }
-// Blocks of the first kernel: all that fit, but no more than shares of kMinShare steps need.
+// Blocks of the first kernel that an SM array holds at a time.
+template <int D, int NQ, typename T>
+int64_t resident() {
+    return (int64_t)(device_sms() > 0 ? device_sms() : 152) * AttendShape<D, NQ, T>::BLOCKS;  // sizes workspaces without a device, too
+}
+template <int NQ>
+int64_t tiles_of(const cgdr_attend_args &a) { return ((int64_t)a.max_q * (a.Hq / a.Hkv) + 8 * NQ - 1) / (8 * NQ); }
+// Whether every unit goes to a block of its own, which needs no schedule, no workspace and no second kernel,
+// but leaves the SMs to the longest unit where units are few or long.  With u = units / resident blocks, the
+// limit is 8 steps of 128 tokens where u is small and 40 from u = 1 on.  Measured (bf16, D 128, whole / shared;
+// lengths spread from 100 to the stated one; units of one token and four heads unless said):
+//   u 0.14: 1024 tokens 9.9 / 11.5 us, 2048 16.8 / 12.6       u 0.6 (8 tokens): 4096 45 / 58, 8192 83 / 75
+//   u 1.1:  1024 21 / 32, 4096 59 / 67, 8192 110 / 105        u 2.2: 4096 106 / 116, 8192 207 / 193
+// Tiles of 16 rows have no limit from u = 1.5 on: a block that takes several of their units one after the other
+// waits for instructions a third of its time (fp32, u 1.7: 8192 tokens 174 / 276; bf16, D 64, u 3.4: 204 / 274).
+// Requests of unequal tokens launch blocks that find no unit; beyond a few for each that does, the shares win.
+constexpr int kWholeSteps = 8, kWholeMore = 32, kWholeEmpty = 4;
+template <int D, int NQ, typename T>
+bool whole(const cgdr_attend_args &a) {
+    const int64_t at_once = resident<D, NQ, T>(), grid = a.B * tiles_of<NQ>(a) * a.Hkv;
+    const int64_t rows = ((int64_t)a.n * (a.Hq / a.Hkv) + 8 * NQ - 1) / (8 * NQ) * a.Hkv;      // units of full tiles
+    const int64_t units = grid < rows + (int64_t)a.B * a.Hkv ? grid : rows + (int64_t)a.B * a.Hkv;
+    if (grid > kWholeEmpty * (units > at_once ? units : at_once)) return false;
+    if (NQ == 2 && 2 * units >= 3 * at_once) return true;
+    return steps_of(a) <= kWholeSteps + kWholeMore * (units < at_once ? units : at_once) / at_once;
+}
+// Blocks of the first kernel where they share: all that fit, but no more than shares of kMinShare steps need.
 template <int D, int NQ, typename T>
 int blocks_of(const cgdr_attend_args &a) {
-    const int64_t sms = device_sms() > 0 ? device_sms() : 152;       // sizes workspaces without a device, too
-    const int64_t tiles = ((int64_t)a.max_q * (a.Hq / a.Hkv) + 8 * NQ - 1) / (8 * NQ);
-    const int64_t most = sms * AttendShape<D, NQ, T>::BLOCKS;
-    const int64_t need = ((int64_t)a.B * a.Hkv * tiles * steps_of(a) + kMinShare - 1) / kMinShare;
+    const int64_t most = resident<D, NQ, T>();
+    const int64_t need = ((int64_t)a.B * a.Hkv * tiles_of<NQ>(a) * steps_of(a) + kMinShare - 1) / kMinShare;
     return (int)(need < most ? need : most);
 }
 template <int D, int NQ, typename T>
 size_t workspace_for(const cgdr_attend_args &a) {
     const int blocks = blocks_of<D, NQ, T>(a);
-    return blocks > 1 && steps_of(a) > 1 ? (size_t)2 * blocks * 8 * NQ * (D + 2) * sizeof(float) : 0;
+    return blocks > 1 && !whole<D, NQ, T>(a) ? (size_t)2 * blocks * 8 * NQ * (D + 2) * sizeof(float) : 0;
 }
 
 template <int D, int NQ, typename T>
@@ -628,13 +661,19 @@ cgdr_status launch_attend(const cgdr_attend_args &a, AttendParams &p, float *ws,
     static SmemOnce smem_once;
     constexpr int kBytes = Sh::BYTES + (kInfos + 1) * (int)sizeof(PageInfo);
     if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_kernel<D, NQ, T>), kBytes)) return CGDR_ERR_CUDA;
+    const int64_t tiles = tiles_of<NQ>(a);
+    if (whole<D, NQ, T>(a)) {
+        p.whole = 1;
+        cache_attend_kernel<D, NQ, T><<<dim3((unsigned)(tiles * a.Hkv), a.B), 32 * kWarps, kBytes, s>>>(p);
+        return launched();
+    }
     p.blocks = blocks_of<D, NQ, T>(a);
     p.part = ws;
     p.ml = ws != nullptr ? ws + (size_t)2 * p.blocks * p.tile * D : nullptr;
     cache_attend_kernel<D, NQ, T><<<p.blocks, 32 * kWarps, kBytes, s>>>(p);
-    if (p.blocks > 1 && steps_of(a) > 1) {            // units of one step are never in parts
+    if (p.blocks > 1) {
         if (cudaPeekAtLastError() != cudaSuccess) return launched();
-        const int64_t all = (int64_t)a.max_q * p.G, tiles = (all + p.tile - 1) / p.tile, rows = all < p.tile ? all : p.tile;
+        const int64_t rows = tiles > 1 ? p.tile : (int64_t)a.max_q * p.G;
         // begins while the first kernel ends, finds its unit, and waits for that kernel's parts
         cudaLaunchConfig_t c{};
         c.gridDim = dim3((unsigned)(tiles * a.Hkv), (unsigned)((rows + kJoinRows - 1) / kJoinRows), a.B);

@@ -21,7 +21,7 @@ struct AttendParams {
     int64_t table_sb;
     const int32_t *kv_lens, *cu;
     float *ml, *part;                                 // parts: [2 grid][kRows][2] maximum and denominator, [2 grid][kRows][D]
-    int blocks;                                       // of the first kernel
+    int blocks, whole;                                // of the first kernel; nonzero: a block a unit, nothing split
     int *status;
 };
 

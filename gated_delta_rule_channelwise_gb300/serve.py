@@ -19,7 +19,7 @@ import struct
 
 import torch
 
-from . import BF16, F32, _check, _need_cuda, lib
+from . import BF16, F32, CgdrError, _need_cuda, lib
 
 _F32, _I32 = torch.float32, torch.int32
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -110,20 +110,11 @@ def _fits(t, dtype, shape):
     return t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous())
 
 
-def _code(t, name):
-    try:
-        return _CODES[t.dtype]
-    except KeyError:
-        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype)) from None
-
-
 def _address(t):
     return 0 if t is None else t.data_ptr()
 
 
 def _status_word(status):
-    if status is None:
-        return 0
     if status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda:
         raise TypeError("status must be an int32 CUDA tensor")
     return status.data_ptr()
@@ -135,15 +126,15 @@ def _rows(t, name, step):
     st = t.stride()
     if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError("%s: innermost dimension must be contiguous" % name)
-    return t.data_ptr(), st[0], st[0] if step else st[1]
+    return (t.data_ptr(), st[0], st[0]) if step else (t.data_ptr(), st[0], st[1])
 
 
-def _grouped(t, name, step):
+def _grouped(t, name, step, shape):
     """The same for [B, T, G, N], or [B, G, N] and packed [n, G, N], whose groups have to be dense."""
-    st, shape = t.stride(), t.shape
+    st = t.stride()
     if (st[-1] != 1 and shape[-1] > 1) or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError("%s: the last two dimensions must be contiguous" % name)
-    return t.data_ptr(), st[0], st[0] if step else st[1]
+    return (t.data_ptr(), st[0], st[0]) if step else (t.data_ptr(), st[0], st[1])
 
 
 def _heads(t, name):
@@ -169,7 +160,9 @@ def _sequences(x, state, cu):
 
 def _conv(x, weight, state, o, bias, silu, B, T, cu, status):
     """x is [B, T, C], or [B, C] / packed [n, C] (T is 1 / 0)."""
-    _need_cuda(x, weight, state, o, bias, cu)
+    if not (x.is_cuda and weight.is_cuda and state.is_cuda and (bias is None or bias.is_cuda) and (cu is None or cu.is_cuda)
+            and (o is None or o.is_cuda)):
+        _need_cuda(x, weight, state, o, bias, cu)
     if o is None:
         o = torch.empty_like(x)
     dtype, shape = x.dtype, x.shape
@@ -179,10 +172,12 @@ def _conv(x, weight, state, o, bias, silu, B, T, cu, status):
         _refuse([("weight", weight, _F32), ("bias", bias, _F32), ("state", state, dtype), ("o", o, dtype)],
                 [("o", o, shape), ("weight", weight, (C, W)), ("bias", bias, (C,)), ("state", state, (B, W - 1, C))],
                 [("weight", weight), ("bias", bias), ("state", state)])
-    block = CONV.pack(B, T, C, W, _code(x, "x"), 1 if silu else 0, 0 if cu is None else shape[0], 0, *_rows(x, "x", step),
+    block = CONV.pack(B, T, C, W, _CODES.get(dtype, -1), 1 if silu else 0, 0 if cu is None else shape[0], 0, *_rows(x, "x", step),
                       *_rows(o, "o", step), weight.data_ptr(), _address(bias), state.data_ptr(), _address(cu),
-                      _status_word(status))
-    _check(lib().cgdr_conv(block, _current(x.get_device())), "cgdr_conv")
+                      0 if status is None else _status_word(status))
+    st = lib().cgdr_conv(block, _current(x.get_device()))
+    if st:
+        raise CgdrError(st, "cgdr_conv")
     return o
 
 
@@ -214,7 +209,11 @@ def conv_decode(x, weight, state, o=None, *, bias=None, silu=True, status=None, 
 
 def _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, B, T, cu, workspace, status):
     """x is [B, T, C], or [B, C] / packed [n, C] (T is 1 / 0)."""
-    _need_cuda(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, cu, workspace)
+    if not (x.is_cuda and dt.is_cuda and A_log.is_cuda and Bm.is_cuda and Cm.is_cuda and state.is_cuda
+            and (o is None or o.is_cuda) and (D is None or D.is_cuda) and (z is None or z.is_cuda)
+            and (dt_bias is None or dt_bias.is_cuda) and (cu is None or cu.is_cuda)
+            and (workspace is None or workspace.is_cuda)):
+        _need_cuda(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, cu, workspace)
     if o is None:
         o = torch.empty_like(x)
     dtype, shape = x.dtype, x.shape
@@ -229,15 +228,17 @@ def _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, B, T, cu, wor
                 [("dt", dt, shape), ("z", z, shape), ("o", o, shape), ("Bm", Bm, grouped), ("Cm", Cm, grouped),
                  ("A_log", A_log, (C, N)), ("state", state, (B, C, N)), ("D", D, (C,)), ("dt_bias", dt_bias, (C,))],
                 [("A_log", A_log), ("state", state), ("D", D), ("dt_bias", dt_bias)])
-    block = SCAN.pack(B, T, C, N, G, _code(x, "x"), _code(o, "o"), 1 if softplus else 0, 0 if cu is None else shape[0], 0,
+    block = SCAN.pack(B, T, C, N, G, _CODES.get(dtype, -1), _CODES.get(o.dtype, -1), 1 if softplus else 0, 0 if cu is None else shape[0], 0,
                       *_rows(x, "x", step), *_rows(dt, "dt", step), *(_rows(z, "z", step) if z is not None else _NONE),
-                      *_grouped(Bm, "Bm", step), *_grouped(Cm, "Cm", step), *_rows(o, "o", step), A_log.data_ptr(),
-                      _address(D), _address(dt_bias), state.data_ptr(), _address(cu), _status_word(status))
+                      *_grouped(Bm, "Bm", step, grouped), *_grouped(Cm, "Cm", step, grouped), *_rows(o, "o", step), A_log.data_ptr(),
+                      _address(D), _address(dt_bias), state.data_ptr(), _address(cu), 0 if status is None else _status_word(status))
     L = lib()
     need = 0 if T == 1 else L.cgdr_scan_workspace_size(block)
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _check(L.cgdr_scan(block, workspace.data_ptr() if need else None, need, _current(x.get_device())), "cgdr_scan")
+    st = L.cgdr_scan(block, workspace.data_ptr() if need else None, need, _current(x.get_device()))
+    if st:
+        raise CgdrError(st, "cgdr_scan")
     return o
 
 
@@ -329,7 +330,8 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
     if stream is not None:
         return _on(stream, cache_plan, block_table, seq_lens, new_lens, free_pages, free_count, n_tokens, page, out,
                    num_pages=num_pages, status=status)
-    _need_cuda(block_table, seq_lens, new_lens, free_pages, free_count)
+    if not (block_table.is_cuda and seq_lens.is_cuda and new_lens.is_cuda and free_pages.is_cuda and free_count.is_cuda):
+        _need_cuda(block_table, seq_lens, new_lens, free_pages, free_count)
     B, width = block_table.shape
     F = free_pages.numel()
     if out is None:
@@ -346,14 +348,17 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
         raise ValueError("block_table: innermost dimension must be contiguous")
     block = PLAN.pack(B, width, page, n_tokens, F, 0x7FFFFFFF if num_pages is None else num_pages,
                       block_table.data_ptr(), sb, seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
-                      free_count.data_ptr(), *out._addresses, _status_word(status))
-    _check(lib().cgdr_cache_plan(block, _current(block_table.get_device())), "cgdr_cache_plan")
+                      free_count.data_ptr(), *out._addresses, 0 if status is None else _status_word(status))
+    st = lib().cgdr_cache_plan(block, _current(block_table.get_device()))
+    if st:
+        raise CgdrError(st, "cgdr_cache_plan")
     return out
 
 
 def _check_cache(k_cache, v_cache, k_scale, v_scale):
     """(pages, Hkv, page, D) of a cache: int8 [pages, Hkv, page, D] with fp32 scales [pages, Hkv]."""
-    _need_cuda(k_cache, v_cache, k_scale, v_scale)
+    if not (k_cache.is_cuda and v_cache.is_cuda and k_scale.is_cuda and v_scale.is_cuda):
+        _need_cuda(k_cache, v_cache, k_scale, v_scale)
     shape = k_cache.shape
     if len(shape) != 4:
         raise ValueError("k_cache must be [pages, Hkv, page, D]")
@@ -376,16 +381,19 @@ def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, status=None
     if stream is not None:
         return _on(stream, cache_append, k, v, slots, k_cache, v_cache, k_scale, v_scale, status=status)
     pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
-    _need_cuda(k, v, slots)
+    if not (k.is_cuda and v.is_cuda and slots.is_cuda):
+        _need_cuda(k, v, slots)
     n = k.shape[0]
     shape = (n, Hkv, D)
     if not (k.shape == shape and v.shape == shape and v.dtype == k.dtype and _fits(slots, torch.int64, (n,))):
         _refuse([("v", v, k.dtype), ("slots", slots, torch.int64)], [("k", k, shape), ("v", v, shape), ("slots", slots, (n,))],
                 [("slots", slots)])
-    block = APPEND.pack(n, Hkv, D, page, _code(k, "k"), pages, *_heads(k, "k"), *_heads(v, "v"), slots.data_ptr(),
+    block = APPEND.pack(n, Hkv, D, page, _CODES.get(k.dtype, -1), pages, *_heads(k, "k"), *_heads(v, "v"), slots.data_ptr(),
                         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                        _status_word(status))
-    _check(lib().cgdr_cache_append(block, _current(k.get_device())), "cgdr_cache_append")
+                        0 if status is None else _status_word(status))
+    st = lib().cgdr_cache_append(block, _current(k.get_device()))
+    if st:
+        raise CgdrError(st, "cgdr_cache_append")
 
 
 def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o=None, *, max_q, max_kv=None,
@@ -408,7 +416,9 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
     if o is None:
         o = torch.empty_like(q)
-    _need_cuda(q, o, block_table, kv_lens, cu_seqlens, workspace)
+    if not (q.is_cuda and o.is_cuda and block_table.is_cuda and kv_lens.is_cuda and cu_seqlens.is_cuda
+            and (workspace is None or workspace.is_cuda)):
+        _need_cuda(q, o, block_table, kv_lens, cu_seqlens, workspace)
     n, Hq, Dq = q.shape
     if Dq != D:
         raise ValueError("q has head dimension %d, the cache %d" % (Dq, D))
@@ -422,16 +432,17 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     sb, sw = block_table.stride()
     if sw != 1 and width > 1:
         raise ValueError("block_table: innermost dimension must be contiguous")
-    block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _code(q, "q"), pages, max_q, width * page if max_kv is None else max_kv,
+    block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _CODES.get(q.dtype, -1), pages, max_q, width * page if max_kv is None else max_kv,
                         path, 0, 0.0 if scale is None else scale, *_heads(q, "q"), *_heads(o, "o"), k_cache.data_ptr(),
                         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), sb,
-                        kv_lens.data_ptr(), cu_seqlens.data_ptr(), _status_word(status))
+                        kv_lens.data_ptr(), cu_seqlens.data_ptr(), 0 if status is None else _status_word(status))
     L = lib()
     need = L.cgdr_cache_attend_workspace_size(block)
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(L.cgdr_cache_attend(block, workspace.data_ptr() if need else None, need, _current(q.get_device())),
-           "cgdr_cache_attend")
+    st = L.cgdr_cache_attend(block, workspace.data_ptr() if need else None, need, _current(q.get_device()))
+    if st:
+        raise CgdrError(st, "cgdr_cache_attend")
     return o
 
 
