@@ -170,29 +170,36 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
     const bool live = cg0 + ch < p.Cg;                                // Cg is a multiple of 8: all four channels or none
     const int c = live ? c0 + ch : c0;
 
-    float A[4][4];
-    f32x2 h[4][2] = {};
+    // in pairs of channels: d and d x come from shared memory as pairs, and a pair of y needs no sum across
+    f32x2 A[2][4], h[2][4] = {};
+    auto load_four = [&](const float *src, f32x2 (&to)[2][4]) {       // [channel][state] rows of N
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p.A_log + (int64_t)(c + i) * N + 4 * q));
-        A[i][0] = -kLog2e * expf(a.x); A[i][1] = -kLog2e * expf(a.y);
-        A[i][2] = -kLog2e * expf(a.z); A[i][3] = -kLog2e * expf(a.w);
-    }
-    // h <- exp(A d) h + in, for the four states of channel i
-    auto step = [&](int i, float d, f32x2 in0, f32x2 in1) {
-        h[i][0] = fma2(pair(ex2(d * A[i][0]), ex2(d * A[i][1])), h[i][0], in0);
-        h[i][1] = fma2(pair(ex2(d * A[i][2]), ex2(d * A[i][3])), h[i][1], in1);
-    };
-    auto load_h = [&](const float *src) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(src + i * N);
-            h[i][0] = v.x; h[i][1] = v.y;
+        for (int j = 0; j < 2; ++j) {
+            const float4 lo = *reinterpret_cast<const float4 *>(src + 2 * j * N), hi = *reinterpret_cast<const float4 *>(src + (2 * j + 1) * N);
+            to[j][0] = pair(lo.x, hi.x); to[j][1] = pair(lo.y, hi.y); to[j][2] = pair(lo.z, hi.z); to[j][3] = pair(lo.w, hi.w);
         }
     };
+    auto load_h = [&](const float *src) { load_four(src, h); };
     auto store_h = [&](float *dst) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<ulonglong2 *>(dst + i * N) = make_ulonglong2(h[i][0], h[i][1]);
+        for (int j = 0; j < 2; ++j) {
+            const float2 f[4] = {split(h[j][0]), split(h[j][1]), split(h[j][2]), split(h[j][3])};
+            *reinterpret_cast<float4 *>(dst + 2 * j * N) = make_float4(f[0].x, f[1].x, f[2].x, f[3].x);
+            *reinterpret_cast<float4 *>(dst + (2 * j + 1) * N) = make_float4(f[0].y, f[1].y, f[2].y, f[3].y);
+        }
+    };
+    load_four(p.A_log + (int64_t)c * N + 4 * q, A);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float2 a = split(A[j][n]);
+            A[j][n] = pair(-kLog2e * expf(a.x), -kLog2e * expf(a.y));
+        }
+    // h <- exp(A d) h + in, for state n of channels 2 j, 2 j + 1
+    auto step = [&](int j, int n, f32x2 d, f32x2 in) {
+        const float2 e = split(mul2(d, A[j][n]));
+        h[j][n] = fma2(pair(ex2(e.x), ex2(e.y)), h[j][n], in);
     };
     float *hs = p.state + ((int64_t)pc.b * p.C + c) * N + 4 * q;
     auto end_of = [&](int k) { return p.ends + ((int64_t)(pc.slot + k) * p.C + c) * N + 4 * q; };
@@ -206,12 +213,13 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
         load_h(end_of(0));
 #pragma unroll 4
         for (int k = 1; k < pc.k; ++k) {
-            const float4 d = *reinterpret_cast<const float4 *>(p.sums + (int64_t)(pc.slot + k) * p.C + c);
-            const float ds[4] = {d.x, d.y, d.z, d.w};
+            const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(p.sums + (int64_t)(pc.slot + k) * p.C + c);
+            f32x2 e[2][4];
+            load_four(end_of(k), e);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(end_of(k) + i * N);
-                step(i, ds[i], e.x, e.y);
+            for (int n = 0; n < 4; ++n) {
+                step(0, n, d.x, e[0][n]);
+                step(1, n, d.y, e[1][n]);
             }
         }
     }
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
         }
     };
     load(pc.len);
-    float total[4] = {0.f, 0.f, 0.f, 0.f};
+    f32x2 total[2] = {};
     for (int left = pc.len; left > 0; left -= TT) {
         const Eight<T> px = rx, pz = rz;              // what the tile's outputs need again
         if (stages) {
@@ -307,28 +315,30 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
         // multiply-add a token: unrolled, they run ahead of it
 #pragma unroll 4
         for (int t = 0; t < TT; ++t) {
-            const float4 dd = *reinterpret_cast<const float4 *>(&sm.d[t][ch]), uu = *reinterpret_cast<const float4 *>(&sm.u[t][ch]);
-            const float4 b = *reinterpret_cast<const float4 *>(&sm.b[t][4 * q]);
-            const float d[4] = {dd.x, dd.y, dd.z, dd.w}, u[4] = {uu.x, uu.y, uu.z, uu.w};
+            const ulonglong2 dd = *reinterpret_cast<const ulonglong2 *>(&sm.d[t][ch]), uu = *reinterpret_cast<const ulonglong2 *>(&sm.u[t][ch]);
+            const float4 bb = *reinterpret_cast<const float4 *>(&sm.b[t][4 * q]);
+            const f32x2 d[2] = {dd.x, dd.y}, u[2] = {uu.x, uu.y}, b[4] = {both(bb.x), both(bb.y), both(bb.z), both(bb.w)};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) step(i, d[i], pair(u[i] * b.x, u[i] * b.y), pair(u[i] * b.z, u[i] * b.w));
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) step(j, n, d[j], mul2(u[j], b[n]));
             if (kEnds) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) total[i] += d[i];
+                total[0] = add2(total[0], d[0]);
+                total[1] = add2(total[1], d[1]);
             } else {
-                const ulonglong2 cc = *reinterpret_cast<const ulonglong2 *>(&sm.c[kEnds ? 0 : t][4 * q]);
-                float y[4];
+                const float4 cc = *reinterpret_cast<const float4 *>(&sm.c[kEnds ? 0 : t][4 * q]);
+                f32x2 y2[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 s = split(fma2(cc.y, h[i][1], mul2(cc.x, h[i][0])));
-                    y[i] = s.x + s.y;
-                }
+                for (int j = 0; j < 2; ++j)
+                    y2[j] = fma2(both(cc.w), h[j][3], fma2(both(cc.z), h[j][2], fma2(both(cc.y), h[j][1], mul2(both(cc.x), h[j][0]))));
                 // down to four lanes that hold parts of the same y: lanes give away half of their
                 // channels, then half of what is left, then add whole values
                 float *part = &sm.y[kEnds ? 0 : t][q & 3][ch];
                 if (LPC == 4) {
-                    *reinterpret_cast<float4 *>(part) = make_float4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<ulonglong2 *>(part) = make_ulonglong2(y2[0], y2[1]);
                 } else {
+                    const float2 y01 = split(y2[0]), y23 = split(y2[1]);
+                    const float y[4] = {y01.x, y01.y, y23.x, y23.y};
                     const bool hi4 = q & 4;
                     float r0 = hi4 ? y[2] : y[0], r1 = hi4 ? y[3] : y[1];
                     r0 += __shfl_xor_sync(0xffffffffu, hi4 ? y[0] : y[2], 4);
@@ -386,7 +396,7 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
     if (kEnds) {
         store_h(end_of(pc.k));
         if (q == 0)
-            *reinterpret_cast<float4 *>(p.sums + (int64_t)(pc.slot + pc.k) * p.C + c) = make_float4(total[0], total[1], total[2], total[3]);
+            *reinterpret_cast<ulonglong2 *>(p.sums + (int64_t)(pc.slot + pc.k) * p.C + c) = make_ulonglong2(total[0], total[1]);
     } else if (pc.k == pc.chunks - 1) {
         store_h(hs);
     }

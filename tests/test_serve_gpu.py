@@ -419,6 +419,19 @@ def test_attend_long_cache_is_split_and_joined(dtype):
     check_attend(attend_case(6, [3, 2], [2500, 700], 2, 1, 128, 128, dtype), dtype, scale=0.3)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 2, 128, 64), (16, 1, 64, 16), (6, 3, 32, 128), (16, 2, 128, 16)])
+def test_attend_units_of_unequal_lengths_share_the_blocks(dtype, Hq, Hkv, D, page):
+    q_lens, kv_lens = [1, 2, 0, 5, 1, 1], [1100, 0, 40, 1537, 130, 1025]
+    check_attend(attend_case(17, q_lens, kv_lens, Hq, Hkv, D, page, dtype), dtype)
+
+
+def test_attend_one_prompt_among_many_single_tokens():
+    q_lens = [1] * 20 + [600] + [0, 1] * 10
+    kv_lens = [(37 * i) % 300 for i in range(20)] + [700] + [5, 129] * 10
+    check_attend(attend_case(18, q_lens, kv_lens, 8, 2, 64, 32, F32), F32)
+
+
 def test_attend_empty_cache_gives_zeros():
     case = attend_case(1, [1, 2], [0, 0], 2, 1, 64, 16, BF)
     assert not check_attend(case, BF).any()
