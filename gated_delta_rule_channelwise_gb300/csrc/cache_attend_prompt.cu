@@ -31,10 +31,7 @@ constexpr int kLoad = 128;                            // loading threads
 constexpr int kThreads = 2 * kSoft + kLoad + 4 * 32;  // and four warps that issue the products
 constexpr int kRaw = 2 * kTok * D;                    // k and v bytes of a step
 constexpr int kRawStages = 3;
-#ifndef POLLS
-#define POLLS (1u << 18)
-#endif
-constexpr uint32_t kPolls = POLLS;                    // of a wait, before it gives up
+constexpr uint32_t kPolls = 1u << 18;                 // of a wait, before it gives up
 
 constexpr int kQBytes = kTile * D * 2, kKBytes = kTok * D * 2, kVBytes = D * kTok * 2;
 constexpr int kOffQ = 0, kOffK = 2 * kQBytes, kOffV = kOffK + 2 * kKBytes, kOffRaw = kOffV + 2 * kVBytes;
@@ -459,17 +456,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
 }  // namespace
 
 // Where this kernel covers the call and is expected to need less time than the other one, from what both
-// measured: a step of 64 cached tokens takes a block 1.0 us (0.8 us with one row tile), and the other
-// kernel takes 16 rows past 15,200 cached tokens in a microsecond.  With few blocks and a long cache that
-// one wins, as it splits the cache.
+// measured (us): here a round of resident blocks takes 1.08 for a step of 64 cached tokens, 0.86 with one
+// row tile, and 9 to begin and end; there 16 rows pass 27,000 cached tokens in one, and 8.  Few rows or few heads
+// leave SMs idle here, while that kernel splits the cache.  8 heads, groups of 4; there / here:
+//   1 request of 128 tokens: 2048 cached 28 / 46, 8192 91 / 142; of 512: 88 / 47 and 310 / 142
+//   8 requests of 16 tokens: 2048 cached 28 / 36, 8192 93 / 122; of 32: 54 / 36 and 179 / 113
 bool attend_prompt_supported(const cgdr_attend_args &a) {
     const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv), pairs = (rows + 2 * kTile - 1) / (2 * kTile);
     if (a.path == CGDR_ATTEND_ROWS || a.dtype != CGDR_BF16 || a.D != D || pairs > 65535 || !aligned_to(a.o, 16) || (a.o_st | a.o_sh) % 8 != 0)
         return false;
     if (a.path == CGDR_ATTEND_TILES) return true;
     const int64_t sms = device_sms() > 0 ? device_sms() : 152, blocks = pairs * a.Hkv * a.B, kv = a.max_kv;
-    const double here = (double)((blocks + sms - 1) / sms) * (double)kv / kTok * (rows > kTile ? 1.0 : 0.8);
-    const double other = (double)a.B * a.Hkv * (double)((rows + 15) / 16) * (double)kv / 15200.0;
+    const double here = 9.0 + (double)((blocks + sms - 1) / sms) * (double)kv / kTok * (rows > kTile ? 1.08 : 0.86);
+    const double other = 8.0 + (double)a.B * a.Hkv * (double)((rows + 15) / 16) * (double)kv / 27000.0;
     return rows > 32 && here < other;
 }
 
