@@ -35,37 +35,43 @@ __device__ __forceinline__ int quantised(float x, float scale) {
 // Four values as bytes of round(x / by), |x / by| <= 127.  Adding 1.5 2^23 rounds the product with the
 // reciprocal to the nearest integer, ties to even, in the low bits; product and quotient are rounded
 // from values 127 2^-23 apart at most, so where the product is 1e-4 off a tie the quotient rounds the same.
-__device__ __forceinline__ uint32_t quantised4(const float *f, float by, float inverse, bool sure) {
+__device__ __forceinline__ uint32_t quantised4(f32x2 x, f32x2 y, float by, f32x2 inverse, bool sure) {
     constexpr float kMagic = 12582912.f;
-    uint32_t b[4];
-    bool exact = !sure;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const float t = f[c] * inverse, r = t + kMagic;
-        exact |= fabsf(fabsf(t - (r - kMagic)) - 0.5f) < 1e-4f;
-        b[c] = __float_as_uint(r);
-    }
-    if (exact) {
+    const f32x2 tx = mul2(x, inverse), ty = mul2(y, inverse), rx = add2(tx, both(kMagic)), ry = add2(ty, both(kMagic));
+    const float2 bx = split(rx), ry2 = split(ry);
+    const float2 ex = split(fma2(add2(rx, both(-kMagic)), both(-1.f), tx)), ey = split(fma2(add2(ry, both(-kMagic)), both(-1.f), ty));
+    uint32_t b[4] = {__float_as_uint(bx.x), __float_as_uint(bx.y), __float_as_uint(ry2.x), __float_as_uint(ry2.y)};
+    const float off = fmaxf(fmaxf(fabsf(ex.x), fabsf(ex.y)), fmaxf(fabsf(ey.x), fabsf(ey.y)));
+    if (!sure || off > 0.5f - 1e-4f) {
+        const float2 fx = split(x), fy = split(y);
+        const float f[4] = {fx.x, fx.y, fy.x, fy.y};
 #pragma unroll
         for (int c = 0; c < 4; ++c) b[c] = (uint32_t)quantised(f[c], by);
     }
     return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
+// The largest magnitude as bits, which order as integers do, a NaN above all: two bf16 to a word, or one fp32.
+template <typename T> __device__ __forceinline__ uint32_t larger(uint32_t top, uint32_t w);
+template <> __device__ __forceinline__ uint32_t larger<float>(uint32_t top, uint32_t w) { return max(top, w & 0x7FFFFFFFu); }
+template <> __device__ __forceinline__ uint32_t larger<__nv_bfloat16>(uint32_t top, uint32_t w) { return __vmaxu2(top, w & 0x7FFF7FFFu); }
+
 // One run by a warp, or (kBlock) by the block: tokens from i on into the page of `slot` from its offset on, up to the
 // first token that is not on the next slot.  The values that a run of the greatest length would have are
 // asked for before its length is known.
 template <typename T, bool kBlock>
-__device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t slot, int h, int which, float *s_max) {
+__device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t slot, int h, int which, uint32_t *s_max) {
     constexpr int V = Vec<T>::n, NT = kBlock ? kAppendThreads : 32, kKeep = 4;
     const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
     const int off = (int)(slot % p.page);
     const int64_t unit = (slot / p.page) * p.Hkv + h;                 // the page's block of this head
     int8_t *dst = p.cache[which] + unit * p.page * p.D;
     const T *x = static_cast<const T *>(p.x[which]);
-    const int per = p.D / V, most = min(p.page - off, p.n - i);       // a page has 128 tokens at most
+    const int per = p.D / V, shift = 31 - __clz(per);                 // vectors of a token: a power of two
+    const int most = min(p.page - off, p.n - i);                      // a page has 128 tokens at most
+    const int64_t head = h * p.sh[which];
     auto vec = [&](int e) {
-        const int64_t at = (int64_t)(i + e / per) * p.st[which] + h * p.sh[which] + (e % per) * V;
+        const int64_t at = (int64_t)(i + (e >> shift)) * p.st[which] + head + (e & (per - 1)) * V;
         return range_in_bounds(at, V, p.ex[which], p.status, nullptr) ? __ldg(reinterpret_cast<const uint4 *>(x + at))
                                                                       : make_uint4(0, 0, 0, 0);
     };
@@ -82,26 +88,21 @@ __device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t
     }
     len = __reduce_min_sync(0xffffffffu, len);
     const int vecs = len * per;
-    float top = 0.f;
-    auto over = [&](const uint4 &r) {
-        float f[V];
-        Vec<T>::unpack(r, f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) top = max_nan(top, fabsf(f[j]));
-    };
+    uint32_t top = 0;
+    auto over = [&](const uint4 &r) { top = larger<T>(larger<T>(larger<T>(larger<T>(top, r.x), r.y), r.z), r.w); };
 #pragma unroll
     for (int k = 0; k < kKeep; ++k)
         if (tid + k * NT < vecs) over(kept[k]);
     for (int e = tid + kKeep * NT; e < vecs; e += NT) over(vec(e));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (V == 8) top = max(top << 16, top & 0xFFFF0000u);
+    top = __reduce_max_sync(0xffffffffu, top);
     if (kBlock) {
         if ((tid & 31) == 0) s_max[tid >> 5] = top;
         __syncthreads();                              // also: every thread has read the scale that is replaced
 #pragma unroll
-        for (int w = 0; w < kAppendThreads / 32; ++w) top = max_nan(top, s_max[w]);
+        for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, s_max[w]);
     }
-    const float grown = max_nan(had, top * (1.f / 127.f));
+    const float grown = max_nan(had, __uint_as_float(top) * (1.f / 127.f));
     const float by = grown > 0.f ? grown : 1.f;       // nothing but zeros: any divisor gives them
     const float inverse = __frcp_rn(by);
     const bool sure = grown > 0x1p-100f && grown < INFINITY;          // and not a NaN: 1 / by is as exact as numbers get
@@ -130,7 +131,8 @@ __device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t
         Vec<T>::unpack(r, f);
         uint32_t w[V / 4];
 #pragma unroll
-        for (int j = 0; j < V / 4; ++j) w[j] = quantised4(f + 4 * j, by, inverse, sure);
+        for (int j = 0; j < V / 4; ++j)
+            w[j] = quantised4(pair(f[4 * j], f[4 * j + 1]), pair(f[4 * j + 2], f[4 * j + 3]), by, both(inverse), sure);
         uint32_t *to = reinterpret_cast<uint32_t *>(dst + (int64_t)off * p.D + e * V);
         if (V == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[V / 4 - 1]);
         else *to = w[0];
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) cache_append_kernel(const A
     constexpr int NW = kAppendThreads / 32;
     __shared__ int s_start[kAppendThreads], s_count;
     __shared__ int64_t s_slot[kAppendThreads];
-    __shared__ float s_max[NW];
+    __shared__ uint32_t s_max[NW];
     const int tid = threadIdx.x, warp = tid >> 5, h = blockIdx.y, which = blockIdx.z;
     const int i0 = blockIdx.x * p.window;
     const int64_t slots = (int64_t)p.num_pages * p.page;
