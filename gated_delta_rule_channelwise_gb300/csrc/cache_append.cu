@@ -1,12 +1,15 @@
 // Quantising append to the 8-bit cache (cgdr_cache_append).
 //
-// Bound by memory for prompts (k and v read once, a byte an element written) and by the launch for
-// single tokens.  The unit of work is a run: consecutive packed tokens on consecutive slots of one
+// Single tokens are bound by the launch (64 tokens of 8 heads of 128: 3.0 us), prompts by the chain that every
+// run goes through, once: slots, values, their largest magnitude, bytes.  2 x 128 values of 8 heads of 4,000
+// tokens, 24.6 MB, take 10.0 us; their bytes alone are 3.7 us, the 28 instructions that a value took once were 14.
+// The unit of work is a run: consecutive packed tokens on consecutive slots of one
 // page, for one head, of k or of v.  Whoever has a run has its page's scale, so nothing is exchanged
 // between blocks.  A block finds the runs that begin in its window of tokens: few of them (a prompt)
 // it works on one after the other with all its threads, many (single tokens) a warp each.  The
-// largest magnitude has to be known before the first byte: a thread keeps the first four vectors that it
-// reads (eight cost more in resident blocks than they save) and reads the rest again, from L1 or L2.
+// largest magnitude has to be known before the first byte: a thread keeps the first two vectors that it
+// reads and reads the rest again, from L1 or L2 (one / four / eight kept: 5 / 9 / 7 % slower; 256 threads are as fast
+// on pages of 64 and take 2.8 times as long on pages of 16).
 // The quotient is only formed where its rounding is in doubt: x (1 / scale) is within 3e-5 of it.
 #include "serve.cuh"
 
@@ -61,7 +64,7 @@ template <> __device__ __forceinline__ uint32_t larger<__nv_bfloat16>(uint32_t t
 // asked for before its length is known.
 template <typename T, bool kBlock>
 __device__ __forceinline__ void append_run(const AppendParams &p, int i, int64_t slot, int h, int which, uint32_t *s_max) {
-    constexpr int V = Vec<T>::n, NT = kBlock ? kAppendThreads : 32, kKeep = 4;
+    constexpr int V = Vec<T>::n, NT = kBlock ? kAppendThreads : 32, kKeep = 2;
     const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
     const int off = (int)(slot % p.page);
     const int64_t unit = (slot / p.page) * p.Hkv + h;                 // the page's block of this head
@@ -178,8 +181,9 @@ __global__ void __launch_bounds__(kAppendThreads, 6) cache_append_kernel(const A
     }
 }
 
-// Tokens of a block's window: one where there are few tokens, so that each has a block; up to 64 (a
-// prompt's window then holds a run or two), as long as there are four blocks to an SM.
+// Tokens of a block's window: four where there are few tokens, a warp for each; up to 64 (a prompt's window then
+// holds a run or two), as long as there are four blocks to an SM.  Up to 32 instead: the same on pages of 64, two
+// thirds more time on pages of 16.
 template <typename T>
 cgdr_status launch_append(AppendParams &p, cudaStream_t s) {
     const int sms = device_sms();

@@ -20,7 +20,7 @@ struct AttendParams {
     const int32_t *table;
     int64_t table_sb;
     const int32_t *kv_lens, *cu;
-    float *ml, *part;                                 // parts: [2 grid][kRows][2] maximum and denominator, [2 grid][kRows][D]
+    float *ml, *part;                                 // parts: [2 grid][tile][2] maximum and denominator, [2 grid][tile][D]
     int blocks, whole;                                // of the first kernel; nonzero: a block a unit, nothing split
     int *status;
 };

@@ -1,6 +1,7 @@
 // Block tables and slots from request lengths (cgdr_cache_plan).
 //
-// A few kilobytes of integers: the launch itself is the time.  So there is one launch and no wait
+// A few kilobytes of integers: the launch itself is the time (250 requests of a token: 4.0 us; 33 prompts of
+// 66,000 tokens: 6.0 us).  So there is one launch and no wait
 // between blocks: every block forms the two prefix sums over the requests (new tokens, pages taken)
 // again in shared memory, finds the same verdict on capacity, and then fills its share of the
 // tokens and of the new table entries, finding each one's request by bisection.  What one block

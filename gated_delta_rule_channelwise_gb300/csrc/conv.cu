@@ -1,7 +1,9 @@
 // Short causal convolution (cgdr_conv): y[t] = act(bias + sum_j w[j] u[t - (W-1) + j]) per channel,
 // u = the W-1 state rows followed by the sequence.
 //
-// Bound by memory: each x is read once and each y written once, 2 W + 4 operations per element.
+// Bound by memory: each x is read once and each y written once, 2 W + 4 operations per element.  4,001 tokens
+// of 8,192 bf16 channels in five sequences, W = 4, silu: 131.7 MB in 25.8 us, 5.1 TB/s, 76 % of a plain copy's; the
+// sigmoid's two special-function instructions a value are 7 us beside it.  Single tokens of 64 x 12,288 channels: 3.9 us.
 // A thread owns four channels and walks along the tokens with the last W-1 rows in
 // registers, so a row is loaded once per tile of tokens (plus W-1 rows where a tile begins).
 // Tiles cut the packed token axis without regard to the sequences, which keeps ragged batches

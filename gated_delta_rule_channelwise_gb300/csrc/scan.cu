@@ -1,22 +1,26 @@
 // Selective state space scan (cgdr_scan): per channel c and state n
 //     h[n] = exp(A[c, n] d) h[n] + d x B[n],   y = sum_n C[n] h[n],   A = -exp(A_log).
 //
-// A thread holds four states of one channel in registers, N/4 neighbouring lanes one channel, a
-// block 16 channels.  The tokens come in tiles of 32: their rows are loaded into registers one tile
-// ahead, turned into the fp32 values that the recurrence reads (d and d x once per channel, not once
-// per state) and put into shared memory.
+// A thread holds four states of four neighbouring channels in registers, N/4 neighbouring lanes the
+// channels' N states, a block 1024/N channels (16 for N = 128).  The tokens come in tiles of 8 (16): their
+// rows are loaded into registers one tile ahead, turned into the fp32 values that the recurrence reads (d and d x
+// once per channel, not once per state) and put into shared memory.  Arithmetic is in packed pairs of channels.
 //
 // The work is N exponentials and 4 N multiply-adds a token and channel, against 8 bytes: the scan is
-// bound by instruction issue and the exponential unit, and, with few channels, by the length of the
-// recurrence.  Then a sequence is cut into chunks.  The state that leaves a chunk is
+// bound by instruction issue and the exponential unit (32 a clock of an SM), and, with few channels, by the length
+// of the recurrence.  Then a sequence is cut into chunks.  The state that leaves a chunk is
 // exp(A sum d) h_in + e, with e the chunk's own end state from zero, so one launch forms (sum d, e) of
 // every chunk but the last, and a second runs all chunks, each joining its h_in from the pairs
 // before it.  That does the exponentials twice, so chunks are as long as the SM count allows.
+//
+// Measured: one sequence of 4,000 tokens, 4,096 bf16 channels, N = 16, gated: 132 us for 262 M exponentials done
+// twice, which are 57 us of their unit; the schedulers issue in 58 % of the cycles with the 12 warps that
+// 160 registers a thread leave an SM.  16,412 tokens of 1,000 fp32 channels: 200 us.  A step of 64 x 4,096 channels:
+// 8.1 us for 35.9 MB.
 #include "serve.cuh"
 
 namespace cgdr {
 namespace {
-
 
 struct ScanParams {
     int B, T, C, Cg, G, n, chunk, softplus, o_f32;

@@ -9,7 +9,10 @@
  * the prefill workspace word) and skips the access; a skipped copy into shared memory is
  * zero-filled or its barrier phase is completed without data, so no wait is left hanging.
  * Accesses through TMA tensor maps are bounds-checked by the hardware already (rows past the
- * tensor read as zeros).  It exports everything cgdr.h declares, plus the call below, and has
+ * tensor read as zeros).  In the kernels of cgdr_serve.h the checked accesses are the rows of tokens,
+ * the outputs and the block table; a page number, slot or length out of range is refused in every
+ * build, and the address of a state, cache page, scale or weight follows from one that has passed.
+ * It exports everything cgdr.h and cgdr_serve.h declare, plus the call below, and has
  * no counterpart in the method's description: it is a tool for checking this library.
  */
 #ifndef CGDR_DEBUG_H_
