@@ -546,10 +546,6 @@ __global__ void __launch_bounds__(32 * kWarps, AttendShape<D, NQ, T>::BLOCKS) ca
             if (cut(p, i)) report(p.status, (int)CGDR_ERR_CAPACITY);
 }
 
-// Waits for the first kernel, whose end this one overlaps.  Every thread does before it returns, so that
-// what follows in the stream finds both kernels done.
-__device__ __forceinline__ void joined() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Joins the parts of a unit: four rows to a block, four groups of threads that take every fourth part.
 constexpr int kJoinRows = 4, kJoinGroups = 4;
 template <int D, typename T>
@@ -738,7 +734,8 @@ extern "C" {
 
 size_t cgdr_cache_attend_workspace_size(const cgdr_attend_args *a) {
     using namespace cgdr;
-    return check(a) != CGDR_OK || a->B == 0 || a->n == 0 || a->max_q == 0 || attend_prompt_supported(*a) ? 0 : workspace_of(*a);
+    if (check(a) != CGDR_OK || a->B == 0 || a->n == 0 || a->max_q == 0) return 0;
+    return attend_prompt_supported(*a) ? attend_prompt_workspace(*a) : workspace_of(*a);
 }
 
 cgdr_status cgdr_cache_attend(const cgdr_attend_args *a, void *ws, size_t ws_bytes, void *stream) {
@@ -746,7 +743,7 @@ cgdr_status cgdr_cache_attend(const cgdr_attend_args *a, void *ws, size_t ws_byt
     const cgdr_status st = check(a);
     if (st != CGDR_OK || a->B == 0 || a->n == 0 || a->max_q == 0) return st;
     const bool prompt = attend_prompt_supported(*a);
-    const size_t need = prompt ? 0 : workspace_of(*a);
+    const size_t need = prompt ? attend_prompt_workspace(*a) : workspace_of(*a);
     if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned_to(ws, 16))) return CGDR_ERR_WORKSPACE;
     AttendParams p{};
     p.B = a->B; p.n = a->n; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = a->Hq / a->Hkv; p.page = a->page; p.shift = __builtin_ctz(a->page); p.width = a->width;
@@ -759,7 +756,7 @@ cgdr_status cgdr_cache_attend(const cgdr_attend_args *a, void *ws, size_t ws_byt
     p.table = a->block_table; p.table_sb = a->table_sb; p.e_table = (a->B - 1) * a->table_sb + a->width;
     p.kv_lens = a->kv_lens; p.cu = a->cu; p.status = a->status;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return prompt ? launch_attend_prompt(*a, p, s) : launch_of(*a, p, static_cast<float *>(ws), s);
+    return prompt ? launch_attend_prompt(*a, p, static_cast<float *>(ws), s) : launch_of(*a, p, static_cast<float *>(ws), s);
 }
 
 }  // extern "C"

@@ -22,6 +22,7 @@ struct AttendParams {
     const int32_t *kv_lens, *cu;
     float *ml, *part;                                 // parts: [2 grid][tile][2] maximum and denominator, [2 grid][tile][D]
     int blocks, whole;                                // of the first kernel; nonzero: a block a unit, nothing split
+    int splits, height;                               // parts of the cache, and rows of a part (cache_attend_prompt.cu)
     int *status;
 };
 
@@ -78,8 +79,13 @@ __device__ __forceinline__ void put_row(const AttendParams &p, int tok, int head
         if (in_bounds(off + e, p.eo, p.status, nullptr)) static_cast<T *>(p.o)[off + e] = Cvt<T>::from_f(sum == 0.f ? 0.f : o[e] * by);
 }
 
-// Whether the tensor-core kernel takes the call, and the call.
+// A second kernel that starts early waits here for the first.  Every thread does before it returns, so that
+// what follows in the stream finds both kernels done.
+__device__ __forceinline__ void joined() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Whether the tensor-core kernel takes the call, its workspace, and the call.
 bool attend_prompt_supported(const cgdr_attend_args &a);
-cgdr_status launch_attend_prompt(const cgdr_attend_args &a, AttendParams &p, cudaStream_t s);
+size_t attend_prompt_workspace(const cgdr_attend_args &a);
+cgdr_status launch_attend_prompt(const cgdr_attend_args &a, AttendParams &p, float *ws, cudaStream_t s);
 
 }  // namespace cgdr

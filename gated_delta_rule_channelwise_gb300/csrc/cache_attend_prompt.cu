@@ -110,13 +110,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
     __shared__ volatile int s_stop, s_never;          // a wait gave up: everybody leaves; (never set)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // the last rows, which see the most, first: what runs at the end is short
-    const int b = blockIdx.y, hk = blockIdx.x, row0 = (int)(gridDim.z - 1 - blockIdx.z) * 2 * kTile;
+    const int b = blockIdx.y, hk = blockIdx.x, part = blockIdx.z % p.splits, pairs = gridDim.z / p.splits,
+              pair_at = pairs - 1 - blockIdx.z / p.splits, row0 = pair_at * 2 * kTile;
     const Request rq = request(p, b);
     const int rows = rq.q_len * p.G, kv = rq.kv, behind = rq.behind;
+    if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0 && cut(p, b)) report(p.status, (int)CGDR_ERR_CAPACITY);
     if (row0 >= rows) return;
     const int tiles = rows - row0 > kTile ? 2 : 1, last_row = min(row0 + 2 * kTile, rows) - 1;
     const int end = min(kv, behind + last_row / p.G + 1);             // what the last row sees
-    const int steps = end > 0 ? (end + kTok - 1) / kTok : 0;
+    const int all_steps = end > 0 ? (end + kTok - 1) / kTok : 0, share = (all_steps + p.splits - 1) / p.splits;
+    const int steps = max(min(all_steps - part * share, share), 0), from = part * share * kTok;  // the part's, and its first position
 
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     auto bar = [&](int i) { return base + kOffBar + 8 * i; };
@@ -161,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
             const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
             const int tok = rq.first + row / p.G, head = hk * p.G + row % p.G;
             const bool ok = row < rows;
-            const int seen = ok ? min(behind + row / p.G + 1, kv) : 0;
-            const int all_see = row0 + (tile + 1) * kTile <= rows ? min(kv, behind + (row0 + tile * kTile) / p.G + 1) : 0;
+            const int seen = (ok ? min(behind + row / p.G + 1, kv) : 0) - from;
+            const int all_see = (row0 + (tile + 1) * kTile <= rows ? min(kv, behind + (row0 + tile * kTile) / p.G + 1) : 0) - from;
             float scale;
             {
                 // the row in fp16, scaled by a power of two to magnitudes below 2 (4 at the type's end)
@@ -281,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                 fence_after_sync();
                 const float by = l == 0.f ? 0.f : 1.f / l;
                 const int64_t off = (int64_t)tok * p.o_st + (int64_t)head * p.o_sh;
+                const int64_t slot = (((int64_t)(b * p.Hkv + hk) * pairs + pair_at) * p.splits + part) * p.height + tile * kTile + r;
+                if (p.splits > 1 && ok) *reinterpret_cast<float2 *>(p.ml + 2 * slot) = make_float2(M, l);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float o[64];
@@ -297,6 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
 #pragma unroll
                             for (int w = 0; w < 4; ++w) {
                                 const float y[4] = {o[16 * w + 2 * j], o[16 * w + 2 * j + 1], o[16 * w + 8 + 2 * j], o[16 * w + 8 + 2 * j + 1]};
+                                if (p.splits > 1) {
+                                    *reinterpret_cast<float4 *>(p.part + slot * D + 64 * h + 16 * j + 4 * w) = make_float4(y[0], y[1], y[2], y[3]);
+                                    continue;
+                                }
                                 const int64_t at = off + 64 * h + 16 * j + 4 * w;
                                 if (!range_in_bounds(at, 4, p.eo, p.status, nullptr)) continue;
                                 __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.o) + at;
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
         // are asked for, and scales come with the copies.
         int page = -1;                                // lanes 0 .. 3: table entry of that group of the step to be copied next
         auto look = [&](int i) {
-            const int pos = i * kTok + 16 * lane;
+            const int pos = from + i * kTok + 16 * lane;
             const int64_t at = b * p.table_sb + (pos >> p.shift);
             page = -1;
             if (lane < kGroups && pos < end && in_bounds(at, p.e_table, p.status, nullptr)) page = __ldg(p.table + at);
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                 for (int g = 0; g < kGroups; ++g) {
                     const int pg = __shfl_sync(0xffffffffu, page, g);
                     if (pg >= 0) {
-                        const int64_t src = pg * page_bytes + ((i * kTok + 16 * g) & (p.page - 1)) * D;
+                        const int64_t src = pg * page_bytes + ((from + i * kTok + 16 * g) & (p.page - 1)) * D;
                         const uint32_t to = mine + stage * kRaw + 16 * g * D;
                         cp_async16(to, kc + src, true);
                         cp_async16(to + kTok * D, vc + src, true);
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                         cp_async4(to + 4, p.vs + (int64_t)page * p.Hkv + hk, true);
                     } else {
                         asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(0.f), "f"(-1.f) : "memory");
-                        if (i * kTok + 16 * t < end) report(p.status, (int)CGDR_ERR_BOUNDS);
+                        if (from + i * kTok + 16 * t < end) report(p.status, (int)CGDR_ERR_BOUNDS);
                     }
                 }
             }
@@ -456,30 +465,96 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
     }
 }
 
+// Joins the parts of a row: a warp a row, four values a lane.
+constexpr int kJoinRows = 8;
+__global__ void __launch_bounds__(32 * kJoinRows) cache_join_prompt_kernel(const AttendParams p) {
+    const int per = p.height / kJoinRows, hk = blockIdx.x / per, r = blockIdx.x % per * kJoinRows + (threadIdx.x >> 5), d = 4 * (threadIdx.x & 31);
+    const int row = blockIdx.z * 2 * kTile + r;
+    const Request rq = request(p, blockIdx.y);
+    joined();
+    if (row >= rq.q_len * p.G) return;
+    const int64_t slot = ((int64_t)(blockIdx.y * p.Hkv + hk) * gridDim.z + blockIdx.z) * p.splits * p.height + r;
+    float m = kLowest, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < p.splits; ++i) {
+        const float2 ml = *reinterpret_cast<const float2 *>(p.ml + 2 * (slot + (int64_t)i * p.height));
+        const float4 x = *reinterpret_cast<const float4 *>(p.part + (slot + (int64_t)i * p.height) * D + d);
+        const float top = fmaxf(m, ml.x), keep = ex2(m - top), add = ex2(ml.x - top);
+        sum = fmaf(add, ml.y, sum * keep);
+        o[0] = fmaf(add, x.x, o[0] * keep); o[1] = fmaf(add, x.y, o[1] * keep);
+        o[2] = fmaf(add, x.z, o[2] * keep); o[3] = fmaf(add, x.w, o[3] * keep);
+        m = top;
+    }
+    put_row<__nv_bfloat16>(p, rq.first + row / p.G, hk * p.G + row % p.G, d, o, sum);
+}
+
+struct Plan {
+    int64_t pairs, blocks;
+    int height, splits;                               // rows of a block, parts of the cache
+    double us;
+};
+// The parts that a row pair's cache is cut into: as many as pay, in rounds of one block to an SM.  Measured (us): a round
+// takes 1.02 for a step of 64 cached tokens and 13 to begin and end, 0.88 and 7 with one row tile; a second kernel, which
+// joins the parts, adds 3, and they pass at 8 TB/s, mostly through L2.  512 tokens of 8 heads, groups of 4, over 8192
+// cached tokens: 85 in two parts, 142 in one; 128 tokens: 35 in eight, 142 in one.
+Plan plan_of(const cgdr_attend_args &a) {
+    const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv), sms = device_sms() > 0 ? device_sms() : 152;
+    const int64_t kv = a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page, steps = (kv + kTok - 1) / kTok;
+    Plan best{(rows + 2 * kTile - 1) / (2 * kTile), 0, rows > kTile ? 2 * kTile : kTile, 1, 0.0};
+    best.blocks = best.pairs * a.Hkv * a.B;
+    for (int n = 1; n <= 32 && (n == 1 || 4 * n <= steps); ++n) {
+        if (n > 1 && best.blocks * n > 2 * sms) break;
+        const double rounds = (double)((best.blocks * n + sms - 1) / sms), step = best.height > kTile ? 1.02 : 0.88, ends = best.height > kTile ? 13.0 : 7.0;
+        const double join = n > 1 ? 3.0 + (double)best.blocks * n * best.height * (D + 2) * 8.0 / 8e6 : 0.0;
+        const double us = rounds * (ends + (double)((steps + n - 1) / n) * step) + join;
+        if (n == 1 || us < best.us) { best.splits = n; best.us = us; }
+    }
+    return best;
+}
+
 }  // namespace
 
-// Where this kernel covers the call and is expected to need less time than the other one, from what both
-// measured (us): here a round of resident blocks takes 1.08 for a step of 64 cached tokens, 0.86 with one
-// row tile, and 9 to begin and end; there 16 rows pass 27,000 cached tokens in one, and 8.  Few rows or few heads
-// leave SMs idle here, while that kernel splits the cache.  8 heads, groups of 4; there / here:
-//   1 request of 128 tokens: 2048 cached 28 / 46, 8192 91 / 142; of 512: 88 / 47 and 310 / 142
-//   8 requests of 16 tokens: 2048 cached 28 / 36, 8192 93 / 122; of 32: 54 / 36 and 179 / 113
+// Where this kernel covers the call and is expected to need less time than the other one, which was measured to take
+// 16 rows past 27,000 cached tokens in a microsecond, and 8 more.  8 heads, groups of 4; there / here:
+//   1 request of 32 tokens:  512 cached 9.7 / 15.8, 2048 16.1 / 16.1, 8192 33 / 22
+//   1 request of 128 tokens: 512 cached 12 / 22, 2048 28 / 23, 8192 91 / 35
+//   8 requests of 16 tokens: 512 cached 12 / 14, 2048 28 / 25, 8192 93 / 68
 bool attend_prompt_supported(const cgdr_attend_args &a) {
     const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv), pairs = (rows + 2 * kTile - 1) / (2 * kTile);
     if (a.path == CGDR_ATTEND_ROWS || a.dtype != CGDR_BF16 || a.D != D || pairs > 65535 || !aligned_to(a.o, 16) || (a.o_st | a.o_sh) % 8 != 0)
         return false;
     if (a.path == CGDR_ATTEND_TILES) return true;
-    const int64_t sms = device_sms() > 0 ? device_sms() : 152, blocks = pairs * a.Hkv * a.B, kv = a.max_kv;
-    const double here = 9.0 + (double)((blocks + sms - 1) / sms) * (double)kv / kTok * (rows > kTile ? 1.08 : 0.86);
-    const double other = 8.0 + (double)a.B * a.Hkv * (double)((rows + 15) / 16) * (double)kv / 27000.0;
-    return rows > 32 && here < other;
+    const double other = 8.0 + (double)a.B * a.Hkv * (double)((rows + 15) / 16) * (double)a.max_kv / 27000.0;
+    return rows > 32 && plan_of(a).us < other;
 }
 
-cgdr_status launch_attend_prompt(const cgdr_attend_args &a, AttendParams &p, cudaStream_t s) {
+size_t attend_prompt_workspace(const cgdr_attend_args &a) {
+    const Plan plan = plan_of(a);
+    return plan.splits > 1 ? (size_t)plan.blocks * plan.splits * plan.height * (D + 2) * sizeof(float) : 0;
+}
+
+cgdr_status launch_attend_prompt(const cgdr_attend_args &a, AttendParams &p, float *ws, cudaStream_t s) {
     static SmemOnce smem_once;
     if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_prompt_kernel), kBytes)) return CGDR_ERR_CUDA;
-    const int64_t rows = (int64_t)a.max_q * p.G, pairs = (rows + 2 * kTile - 1) / (2 * kTile);
-    cache_attend_prompt_kernel<<<dim3(a.Hkv, a.B, (unsigned)pairs), kThreads, kBytes, s>>>(p);
+    const Plan plan = plan_of(a);
+    p.splits = plan.splits;
+    p.height = plan.height;
+    p.part = ws;
+    p.ml = ws != nullptr ? ws + (size_t)plan.blocks * plan.splits * plan.height * D : nullptr;
+    cache_attend_prompt_kernel<<<dim3(a.Hkv, a.B, (unsigned)(plan.pairs * plan.splits)), kThreads, kBytes, s>>>(p);
+    if (plan.splits > 1) {
+        if (cudaPeekAtLastError() != cudaSuccess) return launched();
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3((unsigned)(a.Hkv * (plan.height / kJoinRows)), a.B, (unsigned)plan.pairs);
+        c.blockDim = dim3(32 * kJoinRows);
+        c.stream = s;
+        cudaLaunchAttribute early{};
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        c.attrs = &early;
+        c.numAttrs = 1;
+        if (cudaLaunchKernelEx(&c, cache_join_prompt_kernel, p) != cudaSuccess) return launched();
+    }
     return launched();
 }
 

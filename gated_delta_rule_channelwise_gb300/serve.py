@@ -287,13 +287,16 @@ def scan_workspace_size(B, T, C, N, G=1, *, n_tokens=None, dtype=torch.bfloat16)
 # --------------------------------------------------------------------------- 8-bit cache
 
 
+_PLAN_PARTS = frozenset(("slots", "kv_lens", "cu_seqlens", "free_count", "requests", "positions"))
+
+
 class CachePlan:
     """What :func:`cache_plan` writes: see there.  One buffer holds it all; it is cut into tensors when one of
     them is first asked for, all at once (a view each costs as much as checking a call's arguments)."""
 
     def __init__(self, B, n_tokens, device="cuda"):
         self.B, self.n_tokens = B, n_tokens
-        # slots first (int64), then int32 words: kv_lens, cu_seqlens, free_count, requests, positions
+        # slots [n] int64 first, then int32: kv_lens [B], cu_seqlens [B + 1], free_count [1], requests [n], positions [n]
         self._buffer = torch.empty(n_tokens + B + 1 + n_tokens, dtype=torch.int64, device=device)
         slots = self._buffer.data_ptr()
         kv = slots + 8 * n_tokens
@@ -301,15 +304,13 @@ class CachePlan:
         self._addresses = count, kv, kv + 4 * B, count + 4, count + 4 + 4 * n_tokens, slots
 
     def __getattr__(self, name):
-        parts = {"slots": "[n] int64", "kv_lens": "[B] int32", "cu_seqlens": "[B + 1] int32", "free_count": "[1] int32",
-                 "requests": "[n] int32", "positions": "[n] int32"}
-        if name not in parts:
+        if name not in _PLAN_PARTS:
             raise AttributeError(name)
-        B, n = self.B, self.n_tokens
-        self.slots = self._buffer[:n]
-        _, self.kv_lens, self.cu_seqlens, self.free_count, self.requests, self.positions = \
+        B, n, parts = self.B, self.n_tokens, self.__dict__
+        slots, parts["kv_lens"], parts["cu_seqlens"], parts["free_count"], parts["requests"], parts["positions"] = \
             self._buffer.view(_I32).unsafe_split_with_sizes((2 * n, B, B + 1, 1, n, n))
-        return self.__dict__[name]
+        parts["slots"] = slots.view(torch.int64)
+        return parts[name]
 
 
 def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens, page, out=None, *, num_pages=None,

@@ -119,11 +119,10 @@ def test_workspace_sizes(lib):
     big = dict(max_q=2000, max_kv=4000)                                       # enough rows: tiles, which need none
     assert cg.cache_attend_workspace_size(4, 8000, 32, 8, 128, 64, 64, **big) == 0
     assert cg.cache_attend_workspace_size(4, 8000, 32, 8, 128, 64, 64, path=cg.ATTEND_ROWS, **big) == 0   # a block a unit
-    few = dict(max_q=40, max_kv=100000)                                       # few units of many steps: shared
-    assert cg.cache_attend_workspace_size(1, 40, 32, 8, 128, 64, 1600, path=cg.ATTEND_TILES, **few) == 0
+    few = dict(max_q=40, max_kv=100000)                                       # few units of many steps: the cache is split
+    assert cg.cache_attend_workspace_size(1, 40, 32, 8, 128, 64, 1600, path=cg.ATTEND_TILES, **few) > 0
     assert cg.cache_attend_workspace_size(1, 40, 32, 8, 128, 64, 1600, path=cg.ATTEND_ROWS, **few) > 0
-    assert cg.cache_attend_workspace_size(1, 40, 32, 8, 64, 64, 1600, path=cg.ATTEND_TILES, **few) > 0    # D = 64: rows
-    assert cg.status_string(cg.ERR_CAPACITY).startswith("CGDR_ERR_CAPACITY")
+    assert cg.cache_attend_workspace_size(1, 40, 32, 8, 128, 64, 3, path=cg.ATTEND_TILES, **few) == 0
 
 
 def test_python_checks_types_and_shapes():

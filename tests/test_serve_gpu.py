@@ -387,6 +387,22 @@ def test_attend_tiles(q_lens, kv_lens, Hq, Hkv, page):
     close(other, o.cpu(), float(o.float().abs().max()) * 2.0 ** -8, BF)
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv,page", [
+    ([70], [3001], 4, 1, 64), ([9, 0, 33], [1500, 700, 2049], 16, 2, 16), ([129, 2], [600, 4000], 2, 2, 128)])
+def test_attend_tiles_over_a_cache_in_parts(q_lens, kv_lens, Hq, Hkv, page):
+    sizes = (len(q_lens), sum(q_lens), Hq, Hkv, 128, page, -(-max(kv_lens) // page) + 1)
+    assert cg.cache_attend_workspace_size(*sizes, max_q=max(q_lens), max_kv=max(kv_lens), path=cg.ATTEND_TILES) > 0
+    check_attend(attend_case(sum(q_lens) + page, q_lens, kv_lens, Hq, Hkv, 128, page, BF), BF, path=cg.ATTEND_TILES)
+
+
+def test_attend_tiles_reports_what_it_cuts_off():
+    q, kc, vc, ks, vs, table, kv, cu = attend_case(13, [1, 40], [100, 200], 2, 1, 128, 16, BF)
+    for kw in (dict(max_q=40, max_kv=150), dict(max_q=39, max_kv=200)):
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        cg.cache_attend(q, kc, vc, ks, vs, table, kv, cu, path=cg.ATTEND_TILES, status=status, **kw)
+        assert int(status) == cg.ERR_CAPACITY
+
+
 def test_attend_tiles_scales_and_non_finite_values():
     """Scales of many magnitudes, zeros, pages outside the cache, NaN scales that no row sees, a NaN query row."""
     case = list(attend_case(40, [140], [333], 2, 1, 128, 16, BF))
