@@ -73,7 +73,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = lib + ".tmp.%d" % os.getpid()
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
+    # One CUDA runtime in the process: with a static copy of its own beside the one that torch has loaded, a call
+    # that allocates its output takes 2.3 us more of the host's time (single-token convolution 12.1 -> 9.8 us).
+    lib64 = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "lib64")
+    cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath", "-Xlinker", lib64, "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
