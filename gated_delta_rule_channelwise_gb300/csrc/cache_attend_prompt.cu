@@ -170,27 +170,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
             {
                 // the row in fp16, scaled by a power of two to magnitudes below 2 (4 at the type's end)
                 const int64_t off = (int64_t)tok * p.q_st + (int64_t)head * p.q_sh;
-                auto eight = [&](int c, float (&f)[8]) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
+                uint4 raw[D / 8];                     // all of it at once: the row costs one latency
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    raw[c] = make_uint4(0, 0, 0, 0);
                     if (ok && range_in_bounds(off + 8 * c, 8, p.eq, p.status, nullptr))
-                        v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off) + c);
-                    Vec<__nv_bfloat16>::unpack(v, f);
-                };
+                        raw[c] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off) + c);
+                }
                 float top = 0.f;
-#pragma unroll 4
+#pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
                     float f[8];
-                    eight(c, f);
+                    Vec<__nv_bfloat16>::unpack(raw[c], f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
                 }
                 const int ex = top > 0x1p-100f && top < INFINITY ? min((int)(__float_as_uint(top) >> 23) - 127, 126) : 0;
                 const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
                 scale = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale * kLog2e;
-#pragma unroll 4
+#pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
                     float f[8];
-                    eight(c, f);
+                    Vec<__nv_bfloat16>::unpack(raw[c], f);
                     sts128(base + kOffQ + tile * kQBytes + sw_off16(kTile, r, 8 * c), half2_bits(f[0] * down, f[1] * down),
                            half2_bits(f[2] * down, f[3] * down), half2_bits(f[4] * down, f[5] * down), half2_bits(f[6] * down, f[7] * down));
                 }
@@ -300,18 +301,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                const float y[4] = {o[16 * w + 2 * j], o[16 * w + 2 * j + 1], o[16 * w + 8 + 2 * j], o[16 * w + 8 + 2 * j + 1]};
+                            for (int w = 0; w < 4; w += 2) {
+                                float y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] = o[16 * (w + e / 4) + 8 * (e / 2 % 2) + 2 * j + e % 2];
                                 if (p.splits > 1) {
-                                    *reinterpret_cast<float4 *>(p.part + slot * D + 64 * h + 16 * j + 4 * w) = make_float4(y[0], y[1], y[2], y[3]);
+                                    float4 *to = reinterpret_cast<float4 *>(p.part + slot * D + 64 * h + 16 * j + 4 * w);
+                                    to[0] = make_float4(y[0], y[1], y[2], y[3]);
+                                    to[1] = make_float4(y[4], y[5], y[6], y[7]);
                                     continue;
                                 }
                                 const int64_t at = off + 64 * h + 16 * j + 4 * w;
-                                if (!range_in_bounds(at, 4, p.eo, p.status, nullptr)) continue;
-                                __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.o) + at;
-                                const uint2 v = l == 0.f ? make_uint2(0, 0)
-                                                         : make_uint2(pack_bf16x2(y[0] * by, y[1] * by), pack_bf16x2(y[2] * by, y[3] * by));
-                                *reinterpret_cast<uint2 *>(to) = v;
+                                if (!range_in_bounds(at, 8, p.eo, p.status, nullptr)) continue;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : y[e] * by;
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at) = Vec<__nv_bfloat16>::pack(y);
                             }
                     }
                 }
