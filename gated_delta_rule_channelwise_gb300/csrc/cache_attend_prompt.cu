@@ -14,9 +14,11 @@
 // shares the conversions.  A step of 64 tokens by 256 rows is 16,384 exponentials (512 cycles of that unit),
 // about 900 issue cycles of the four schedulers for softmax and conversions, and products of 768 cycles (q k^T, 64
 // columns wide, is bound by reading q and k from shared memory: 384 cycles a tile, not 256) and 512.  It takes
-// 2,000: the products of a step wait for its softmax, and the other tile's fill only a part of that.
-// Three prompts of 500 to 2011 tokens over up to 4,000 cached ones, 32 heads on 8: 171 GFLOP in 225 us,
-// 760 TFLOP/s, 39 % of what a large bf16 matrix product reaches; the rows kernel took 1,020 us there.
+// 1,980.  With the softmax cut down to a load and a store and no loader work it is 1,600 still: most of it is the
+// products and the hand-overs between the warps, and two threads a row instead of one, with half of the softmax
+// each, gained nothing (153 us against 139 for 8 x 128 tokens over 8,192).
+// Three prompts of 500 to 2011 tokens over up to 4,000 cached ones, 32 heads on 8: 171 GFLOP in 209 us,
+// 816 TFLOP/s, 42 % of what a large bf16 matrix product reaches; the rows kernel took 1,020 us there.
 #include "cache_attend.cuh"
 #include "tc05.cuh"
 
@@ -498,9 +500,9 @@ struct Plan {
     double us;
 };
 // The parts that a row pair's cache is cut into: as many as pay, in rounds of one block to an SM.  Measured (us): a round
-// takes 1.02 for a step of 64 cached tokens and 13 to begin and end, 0.88 and 7 with one row tile; a second kernel, which
-// joins the parts, adds 3, and they pass at 8 TB/s, mostly through L2.  512 tokens of 8 heads, groups of 4, over 8192
-// cached tokens: 85 in two parts, 142 in one; 128 tokens: 35 in eight, 142 in one.
+// takes 1.02 for a step of 64 cached tokens and 10 to begin and end, 0.88 and 6 with one row tile; a second kernel, which
+// joins the parts, adds 3 and 0.2 a part, and they pass at 8 TB/s, mostly through L2.  512 tokens of 8 heads, groups of 4, over 8192
+// cached tokens: 83 in two parts, 140 in one; 128 tokens: 33 in eight, 140 in one.
 Plan plan_of(const cgdr_attend_args &a) {
     const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv), sms = device_sms() > 0 ? device_sms() : 152;
     const int64_t kv = a.max_kv < (int64_t)a.width * a.page ? a.max_kv : (int64_t)a.width * a.page, steps = (kv + kTok - 1) / kTok;
@@ -508,8 +510,8 @@ Plan plan_of(const cgdr_attend_args &a) {
     best.blocks = best.pairs * a.Hkv * a.B;
     for (int n = 1; n <= 32 && (n == 1 || 4 * n <= steps); ++n) {
         if (n > 1 && best.blocks * n > 2 * sms) break;
-        const double rounds = (double)((best.blocks * n + sms - 1) / sms), step = best.height > kTile ? 1.02 : 0.88, ends = best.height > kTile ? 13.0 : 7.0;
-        const double join = n > 1 ? 3.0 + (double)best.blocks * n * best.height * (D + 2) * 8.0 / 8e6 : 0.0;
+        const double rounds = (double)((best.blocks * n + sms - 1) / sms), step = best.height > kTile ? 1.02 : 0.88, ends = best.height > kTile ? 10.0 : 6.0;
+        const double join = n > 1 ? 3.0 + 0.2 * n + (double)best.blocks * n * best.height * (D + 2) * 8.0 / 8e6 : 0.0;
         const double us = rounds * (ends + (double)((steps + n - 1) / n) * step) + join;
         if (n == 1 || us < best.us) { best.splits = n; best.us = us; }
     }
@@ -519,16 +521,16 @@ Plan plan_of(const cgdr_attend_args &a) {
 }  // namespace
 
 // Where this kernel covers the call and is expected to need less time than the other one, which was measured to take
-// 16 rows past 27,000 cached tokens in a microsecond, and 8 more.  8 heads, groups of 4; there / here:
-//   1 request of 32 tokens:  512 cached 9.7 / 15.8, 2048 16.1 / 16.1, 8192 33 / 22
-//   1 request of 128 tokens: 512 cached 12 / 22, 2048 28 / 23, 8192 91 / 35
-//   8 requests of 16 tokens: 512 cached 12 / 14, 2048 28 / 25, 8192 93 / 68
+// 16 rows past 24,000 cached tokens in a microsecond, and 10 more.  8 heads, groups of 4; there / here:
+//   1 request of 32 tokens:  512 cached 9.7 / 13.1, 2048 16 / 15, 8192 33 / 21
+//   1 request of 128 tokens: 512 cached 12 / 19, 2048 28 / 21, 8192 91 / 33
+//   8 requests of 16 tokens: 512 cached 12 / 13, 2048 28 / 24, 8192 93 / 67
 bool attend_prompt_supported(const cgdr_attend_args &a) {
     const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv), pairs = (rows + 2 * kTile - 1) / (2 * kTile);
     if (a.path == CGDR_ATTEND_ROWS || a.dtype != CGDR_BF16 || a.D != D || pairs > 65535 || !aligned_to(a.o, 16) || (a.o_st | a.o_sh) % 8 != 0)
         return false;
     if (a.path == CGDR_ATTEND_TILES) return true;
-    const double other = 8.0 + (double)a.B * a.Hkv * (double)((rows + 15) / 16) * (double)a.max_kv / 27000.0;
+    const double other = 10.0 + (double)a.B * a.Hkv * (double)((rows + 15) / 16) * (double)a.max_kv / 24000.0;
     return rows > 32 && plan_of(a).us < other;
 }
 
