@@ -485,7 +485,9 @@ __global__ void __launch_bounds__(32 * kWarps, AttendShape<D, NQ, T>::BLOCKS) ca
     if (p.whole) {
         b = blockIdx.y;
         const Request r = request(p, b);
-        at = (int64_t)blockIdx.x * r.steps;
+        // the last rows, which see the most, first: what runs at the end is short (fp32, up to 400 tokens of four
+        // requests over 2000 cached: 159 -> 151 us)
+        at = (int64_t)(r.units - 1 - (int)blockIdx.x) * r.steps;
         left = (int)blockIdx.x < r.units ? r.steps : 0;
     } else {
         const Share share = share_of<NT>(p, s_sum);
