@@ -23,6 +23,8 @@ struct AttendParams {
     float *ml, *part;                                 // parts: [2 grid][tile][2] maximum and denominator, [2 grid][tile][D]
     int blocks, whole;                                // of the first kernel; nonzero: a block a unit, nothing split
     int splits, height;                               // parts of the cache, and rows of a part (cache_attend_prompt.cu)
+    uint32_t polls;                                   // of a wait there
+    int inject;                                       // test hook: its first wait of every block is on a barrier that nothing completes
     int *status;
 };
 

@@ -36,7 +36,7 @@ constexpr int kLoad = 128;                            // loading threads
 constexpr int kThreads = 2 * kSoft + kLoad + 4 * 32;  // and four warps that issue the products
 constexpr int kRaw = 2 * kTok * D;                    // k and v bytes of a step
 constexpr int kRawStages = 3;
-constexpr uint32_t kPolls = 1u << 18;                 // of a wait, before it gives up
+constexpr uint32_t kPolls = 1u << 18;                 // of a wait, before it gives up (args.wait_polls, 0)
 
 constexpr int kQBytes = kTile * D * 2, kKBytes = kTok * D * 2, kVBytes = D * kTok * 2;
 constexpr int kOffQ = 0, kOffK = 2 * kQBytes, kOffV = kOffK + 2 * kKBytes, kOffRaw = kOffV + 2 * kVBytes;
@@ -44,7 +44,7 @@ constexpr int kOffScale = kOffRaw + kRawStages * kRaw;                // float2 
 constexpr int kOffRawScale = kOffScale + 4 * kGroups * 8;            // float2 [kRawStages][kGroups]: scales as copied
 constexpr int kOffBar = kOffRawScale + kRawStages * kGroups * 8;
 enum Bar { kQFull, kKFull, kKFree = kKFull + 2, kVFull = kKFree + 2, kVFree = kVFull + 2, kSFull = kVFree + 2, kSFree = kSFull + 2,
-           kPFull = kSFree + 2, kPvDone = kPFull + 2, kDrain = kPvDone + 2, kBars = kDrain + 4 };
+           kPFull = kSFree + 2, kPvDone = kPFull + 2, kDrain = kPvDone + 2, kNever = kDrain + 4, kBars };
 constexpr int kBytes = kOffBar + kBars * 8 + 1024;    // and the room to align to 1024 bytes
 
 constexpr int kTmemO = 0, kTmemS = 2 * D, kTmemP = kTmemS + 2 * kTok, kTmemCols = 512;
@@ -96,8 +96,8 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
     for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __noinline__ bool keep_waiting(uint32_t bar, uint32_t parity, volatile int *stop, int *status) {
-    for (uint32_t it = 0; it < kPolls; ++it) {
+__device__ __noinline__ bool keep_waiting(uint32_t bar, uint32_t parity, volatile int *stop, int *status, uint32_t polls) {
+    for (uint32_t it = 0; it < polls; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*stop) return false;
     }
@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
         mbar_init(bar(kQFull), tiles * kSoft / 32);
         s_never = 0;
         for (int i = 0; i < 4; ++i) mbar_init(bar(kDrain + i), 1);
+        mbar_init(bar(kNever), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kKFull + i), kLoad / 32);
             mbar_init(bar(kVFull + i), kLoad / 32);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
     // over already costs 50 cycles so, and 190 as a loop.
     auto wait = [&](int which, uint32_t parity) -> bool {
         if (mbar_try_wait(bar(which), parity)) return true;
-        return keep_waiting(bar(which), parity, &s_stop, p.status);
+        return keep_waiting(bar(which), parity, &s_stop, p.status, p.polls);
     };
     auto done = [&](int which) {                      // a warp's arrival
         __syncwarp();
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
             const uint32_t t_s = tmem + lanes + kTmemS + tile * kTok, t_p = tmem + lanes + kTmemP + tile * (kTok / 2),
                            t_o = tmem + lanes + kTmemO + tile * D;
             for (int i = 0; i < steps && go; ++i) {
-                go = __all_sync(0xffffffffu, wait(kSFull + tile, i & 1));
+                go = __all_sync(0xffffffffu, p.inject ? wait(kNever, 0) : wait(kSFull + tile, i & 1));
                 if (!go) break;
                 fence_after_sync();
                 float x[kTok];
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
             }
             if (!go) {                                // what was issued has to end before its memory is given up
                 commit(bar(kDrain + which));
-                keep_waiting(bar(kDrain + which), 0, &s_never, nullptr);
+                keep_waiting(bar(kDrain + which), 0, &s_never, nullptr, kPolls);
             }
         }
     }
@@ -543,6 +544,8 @@ cgdr_status launch_attend_prompt(const cgdr_attend_args &a, AttendParams &p, flo
     static SmemOnce smem_once;
     if (!smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_attend_prompt_kernel), kBytes)) return CGDR_ERR_CUDA;
     const Plan plan = plan_of(a);
+    p.polls = a.wait_polls > 0 ? (uint32_t)a.wait_polls : a.wait_polls < 0 ? (uint32_t)(-(int64_t)a.wait_polls) : kPolls;
+    p.inject = a.wait_polls < 0;
     p.splits = plan.splits;
     p.height = plan.height;
     p.part = ws;

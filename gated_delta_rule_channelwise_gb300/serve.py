@@ -69,7 +69,7 @@ PLAN = Block(*_i("B width page n_tokens F num_pages"), *_p("block_table"), ("tab
              *_p("seq_lens new_lens free_pages free_count free_count_out kv_lens cu requests positions slots status"))
 APPEND = Block(*_i("n Hkv D page dtype num_pages"), *_strided("k", "st", "sh"), *_strided("v", "st", "sh"),
                *_p("slots k_cache v_cache k_scale v_scale status"))
-ATTEND = Block(*_i("B n Hq Hkv D page width dtype num_pages max_q max_kv path reserved"), ("scale", "f"), *_strided("q", "st", "sh"),
+ATTEND = Block(*_i("B n Hq Hkv D page width dtype num_pages max_q max_kv path wait_polls"), ("scale", "f"), *_strided("q", "st", "sh"),
                *_strided("o", "st", "sh"), *_p("k_cache v_cache k_scale v_scale block_table"), ("table_sb", "q"),
                *_p("kv_lens cu status"))
 
@@ -287,6 +287,7 @@ def scan_workspace_size(B, T, C, N, G=1, *, n_tokens=None, dtype=torch.bfloat16)
 # --------------------------------------------------------------------------- 8-bit cache
 
 
+_MAX_KV = (1 << 30) - 1                               # cached tokens of a request at most
 _PLAN_PARTS = frozenset(("slots", "kv_lens", "cu_seqlens", "free_count", "requests", "positions"))
 
 
@@ -398,7 +399,7 @@ def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, status=None
 
 
 def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o=None, *, max_q, max_kv=None,
-                 scale=None, path=ATTEND_AUTO, workspace=None, status=None, stream=None):
+                 scale=None, path=ATTEND_AUTO, workspace=None, status=None, wait_polls=0, stream=None):
     """Attention of the newest tokens over the cache (layout as in :func:`cache_append`).  ``q [n,Hq,D]`` (fp32 or
     bf16) packs the query tokens of all requests, ``cu_seqlens [B+1]`` says whose they are; they are the last of
     the ``kv_lens[b]`` cached tokens, each sees the tokens up to itself, and a row that sees nothing is zero.
@@ -409,11 +410,12 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     the table holds); what exceeds them is cut off and reported in ``status`` (``ERR_CAPACITY``), and pages
     outside the cache are left out (``ERR_BOUNDS``).  Rows of q past ``cu_seqlens[B]`` are not computed.  Returns
     o ``[n,Hq,D]``, like q.  ``path`` forces one of the two kernels for this call (``ATTEND_ROWS``,
-    ``ATTEND_TILES``; the latter covers bf16 with D = 128).  ``workspace``: a buffer of :func:`cache_attend_workspace_size` bytes or more keeps
-    the call free of allocations."""
+    ``ATTEND_TILES``; the latter covers bf16 with D = 128).  ``workspace``: a buffer of
+    :func:`cache_attend_workspace_size` bytes (for dense q and o) or more keeps the call free of allocations.
+    ``wait_polls``: polls of a bounded device wait (0: the default; ``ERR_TIMEOUT`` in ``status`` when one gives up)."""
     if stream is not None:
         return _on(stream, cache_attend, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o,
-                   max_q=max_q, max_kv=max_kv, scale=scale, path=path, workspace=workspace, status=status)
+                   max_q=max_q, max_kv=max_kv, scale=scale, path=path, workspace=workspace, status=status, wait_polls=wait_polls)
     pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
     if o is None:
         o = torch.empty_like(q)
@@ -433,8 +435,8 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     sb, sw = block_table.stride()
     if sw != 1 and width > 1:
         raise ValueError("block_table: innermost dimension must be contiguous")
-    block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _CODES.get(q.dtype, -1), pages, max_q, width * page if max_kv is None else max_kv,
-                        path, 0, 0.0 if scale is None else scale, *_heads(q, "q"), *_heads(o, "o"), k_cache.data_ptr(),
+    block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _CODES.get(q.dtype, -1), pages, max_q,
+                        min(width * page, _MAX_KV) if max_kv is None else max_kv, path, wait_polls, 0.0 if scale is None else scale, *_heads(q, "q"), *_heads(o, "o"), k_cache.data_ptr(),
                         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), sb,
                         kv_lens.data_ptr(), cu_seqlens.data_ptr(), 0 if status is None else _status_word(status))
     L = lib()
@@ -451,8 +453,8 @@ def cache_attend_workspace_size(B, n, Hq, Hkv, D, page, width, *, max_q, max_kv=
                                 path=ATTEND_AUTO) -> int:
     """Bytes of workspace of a :func:`cache_attend` of these sizes."""
     fake = 1 << 20                                    # checked for alignment, never read
-    block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _CODES[dtype], 1, max_q, width * page if max_kv is None else max_kv,
-                        path, 0, 0.0, fake, Hq * D, D, fake, Hq * D, D, fake, fake, fake, fake, fake, width, fake, fake, 0)
+    block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _CODES[dtype], 1, max_q,
+                        min(width * page, _MAX_KV) if max_kv is None else max_kv, path, 0, 0.0, fake, Hq * D, D, fake, Hq * D, D, fake, fake, fake, fake, fake, width, fake, fake, 0)
     return lib().cgdr_cache_attend_workspace_size(block)
 
 

@@ -159,14 +159,16 @@ cgdr_status cgdr_cache_append(const cgdr_append_args *args, void *stream);
  * the host (they size the launch): what exceeds them, or the table's width * page, is cut off and
  * reported as CGDR_ERR_CAPACITY.  Table entries past a request's pages are not read; a page
  * outside [0, num_pages) is left out of the sums and reported as CGDR_ERR_BOUNDS.
- * For few rows key-value positions are split over CTAs; `workspace` (16-byte aligned) holds the parts.
+ * Where rows are few, key-value positions are split over CTAs; `workspace` (16-byte aligned) holds the parts.
+ * A wait that gives up reports CGDR_ERR_TIMEOUT in *status; the rows of its CTA are then undefined.
  * bf16: products of fp16 operands (int8 values are exact in fp16, queries are scaled by a power of
  * two per row first).  fp32: both queries and probabilities in two fp16 parts.
  */
 typedef enum cgdr_attend_path {
     CGDR_ATTEND_AUTO = 0,           /* per call: whichever of the two needs less time by what they measured */
-    CGDR_ATTEND_ROWS = 1,           /* row tiles of 8 or 16, the cache split evenly over all SMs */
-    CGDR_ATTEND_TILES = 2           /* tensor memory, row tiles of 128 (bf16, D = 128; elsewhere ROWS) */
+    CGDR_ATTEND_ROWS = 1,           /* row tiles of 8 or 16; a CTA a tile, or the cache split evenly over all SMs */
+    CGDR_ATTEND_TILES = 2           /* tensor memory, row tiles of 128, the cache in parts where they are few (bf16,
+                                       D = 128, o in 16-byte rows; elsewhere ROWS) */
 } cgdr_attend_path;
 
 typedef struct cgdr_attend_args {
@@ -175,7 +177,8 @@ typedef struct cgdr_attend_args {
     int32_t num_pages;
     int32_t max_q, max_kv;
     int32_t path;                   /* cgdr_attend_path of this call */
-    int32_t reserved;
+    int32_t wait_polls;             /* polls before a device wait of TILES gives up; 0: 2^18; below 0 (tests): -wait_polls,
+                                       and the first wait of every CTA is for something that never comes */
     float scale;                    /* <= 0 selects 1/sqrt(D) */
     const void *q;  int64_t q_st, q_sh;     /* [n,Hq,D] */
     void *o;        int64_t o_st, o_sh;

@@ -46,7 +46,7 @@ PLAN = dict(B=2, width=8, page=16, n_tokens=4, F=3, num_pages=99, block_table=P,
 APPEND = dict(n=3, Hkv=2, D=64, page=16, dtype=cg.BF16, num_pages=9, k=P, k_st=128, k_sh=64, v=2 * P, v_st=128, v_sh=64,
               slots=3 * P, k_cache=4 * P, v_cache=5 * P, k_scale=6 * P, v_scale=7 * P, status=0)
 ATTEND = dict(B=2, n=2, Hq=4, Hkv=2, D=64, page=16, width=8, dtype=cg.BF16, num_pages=9, max_q=1, max_kv=100, path=0,
-              reserved=0, scale=0.0,
+              wait_polls=0, scale=0.0,
               q=P, q_st=256, q_sh=64, o=2 * P, o_st=256, o_sh=64, k_cache=3 * P, v_cache=4 * P, k_scale=5 * P,
               v_scale=6 * P, block_table=7 * P, table_sb=8, kv_lens=8 * P, cu=9 * P, status=0)
 

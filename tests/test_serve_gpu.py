@@ -395,6 +395,17 @@ def test_attend_tiles_over_a_cache_in_parts(q_lens, kv_lens, Hq, Hkv, page):
     check_attend(attend_case(sum(q_lens) + page, q_lens, kv_lens, Hq, Hkv, 128, page, BF), BF, path=cg.ATTEND_TILES)
 
 
+def test_attend_tiles_a_wait_that_gives_up():
+    """The test hook: every block's first wait runs out, the status says so, and the next call is as if nothing had been."""
+    case = attend_case(7, [150, 20], [700, 300], 4, 2, 128, 64, BF)
+    q, kc, vc, ks, vs, table, kv, cu = case
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cg.cache_attend(q, kc, vc, ks, vs, table, kv, cu, max_q=150, max_kv=700, path=cg.ATTEND_TILES, status=status, wait_polls=-4)
+    torch.cuda.synchronize()
+    assert int(status) == cg.ERR_TIMEOUT
+    check_attend(case, BF, path=cg.ATTEND_TILES)
+
+
 def test_attend_tiles_reports_what_it_cuts_off():
     q, kc, vc, ks, vs, table, kv, cu = attend_case(13, [1, 40], [100, 200], 2, 1, 128, 16, BF)
     for kw in (dict(max_q=40, max_kv=150), dict(max_q=39, max_kv=200)):
