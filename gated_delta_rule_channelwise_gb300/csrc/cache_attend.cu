@@ -603,7 +603,8 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) cache_join_ke
     put_row<T>(p, rq.first + row / p.G, unit % p.Hkv * p.G + row % p.G, d, v, sum);
 }
 
-// Rows of a tile: eight where that holds all of a request's.
+// Rows of a tile: eight where that holds all of a request's (64 requests of one token and four heads: 102 us, 150 in
+// tiles of 16).
 int tile_of(const cgdr_attend_args &a) {
     const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hkv);
     return rows <= 8 ? 8 : 16;

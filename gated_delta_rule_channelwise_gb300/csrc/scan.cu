@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
     }
 }
 
-// One token a sequence: a thread reads, updates and writes four states.  Bound by the state's bytes.
+// One token a sequence: a thread reads, updates and writes four states.  Bound by the state's bytes: 64 x 4,096 channels
+// take 8.1 us, and 17.4 in the kernel above, which stages tiles of tokens.
 constexpr int kStepThreads = 128;
 template <typename T> __device__ __forceinline__ float4 four(const T *p);
 template <> __device__ __forceinline__ float4 four<float>(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
@@ -458,16 +459,17 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanParam
     }
 }
 
-// Tokens of a chunk.  One pass keeps every warp busy for the whole sequence, two passes with chunks cost
-// 1.7 times the instructions; so a sequence stays whole where the channels and sequences give at least
-// six warps to an SM, and otherwise the chunks are as many as make that twelve, which is what fits at
-// once (sixteen and twenty-four measured 10 and 3 % slower at 4000 tokens of 4096 channels).
+// Tokens of a chunk.  Two passes cost 1.7 times the instructions of one, but fill the SMs.  Measured on sequences of
+// 1,000 tokens of 4,096 channels (0.84 warps to an SM each), whole / in chunks: two 136 / 70 us, four 142 / 152, six 188 / 213,
+// eight 195 / 313.  So sequences of one length stay whole from three warps to an SM on; packed ones, whose lengths
+// are not known here, from six (five of 1 to 1,000 tokens: 104 us in chunks, 150 whole).  The chunks are as many as
+// make twelve warps, which is what fits at once (ten and sixteen: 14 and 13 % slower at one of 4,000 tokens).
 int chunk_of(const cgdr_scan_args &a) {
     const int64_t sms = device_sms() > 0 ? device_sms() : 152;       // sizes workspaces without a device, too
     const int64_t warps = ((int64_t)a.C * a.N + 511) / 512;          // 16 states to a thread
     const int64_t n = a.cu ? a.n_tokens : (int64_t)a.B * a.T, longest = a.cu ? a.n_tokens : a.T;
     int64_t chunk = longest;
-    if (warps * a.B < 6 * sms || a.cu) {
+    if (warps * a.B < 3 * sms || a.cu) {
         chunk = n * warps / (12 * sms);
         // packed lengths are not known here: sequences up to twice the mean stay whole if there are enough
         if (warps * a.B >= 6 * sms && chunk < 2 * (n / a.B)) chunk = 2 * (n / a.B);

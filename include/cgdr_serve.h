@@ -67,7 +67,7 @@ cgdr_status cgdr_conv(const cgdr_conv_args *args, void *stream);
  * these.  `workspace` (16-byte aligned) holds them; cgdr_scan_workspace_size may be 0.
  */
 typedef struct cgdr_scan_args {
-    int32_t B, T, C, N, G;          /* N in {16, 32, 64, 128}; C/G a multiple of 8 */
+    int32_t B, T, C, N, G;          /* N in {16, 32, 64, 128}; C/G a multiple of 8; B <= 32768 */
     int32_t dtype;                  /* cgdr_dtype of x, dt, z, B, C */
     int32_t o_dtype;                /* cgdr_dtype of o */
     int32_t softplus;
