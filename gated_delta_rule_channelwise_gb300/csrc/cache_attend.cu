@@ -20,7 +20,8 @@
 //
 // The scales stay out of the products: k's multiplies the score; v's becomes part of the exponent,
 // p' = 2^(s + log2 vs - M), with its own running maximum M of s + log2 vs, so that p' lies in (0, 1]
-// whatever the scales are and fits fp16; the denominator adds p' / vs.  M follows the maximum loosely:
+// whatever the scales are and fits fp16; the denominator adds p' / vs (of pages of zeros, which have
+// no logarithm, see kZero).  M follows the maximum loosely:
 // it is only looked for, over the lanes, when some score passes it by more than 2^7, which after the
 // first step is rare, and a vote otherwise.  p' is carried times 2^8: it stays below 2^15 even so,
 // and keeps fp16's relative accuracy down to 2^-22 of the largest (2^-33 of it is where it ends).
@@ -87,8 +88,8 @@ constexpr int kMaxKv = 1 << 30;                       // positions stay well ins
 struct PageInfo {
     int page;                                         // -1: outside the cache
     float k;                                          // k's scale
-    float lv, iv;                                     // log2 and reciprocal of v's scale; 0 and -1 where that is (as good
-                                                      // as) zero, and so are the values
+    float lv, iv;                                     // log2 and reciprocal of v's scale; kZeroLog and kZeroInverse where
+                                                      // that is (as good as) zero, and so are the values
 };
 
 template <int D, int NQ, typename T>
@@ -204,10 +205,10 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
         for (int r = 0; r < kOf; ++r) {
             const int i = tid + r * 32 * kWarps;
             if (i <= last) {
-                const bool zero = vs[r] < 0x1p-100f;  // not so for a NaN, which then spreads as it has to
+                const bool zero = vs[r] < kZero;      // not so for a NaN, which then spreads as it has to
                 info[i].k = ks[r];
-                info[i].lv = zero ? 0.f : log2f(vs[r]);
-                info[i].iv = zero ? -1.f : 1.f / vs[r];
+                info[i].lv = zero ? kZeroLog : log2f(vs[r]);
+                info[i].iv = zero ? kZeroInverse : 1.f / vs[r];
             }
         }
         __syncthreads();

@@ -58,6 +58,10 @@ __device__ __forceinline__ void report(int *status, int code) {
 
 constexpr float kUp = 8.f, kMost = 15.f;              // p' is carried times 2^kUp and stays below 2^kMost
 constexpr float kLowest = -3e38f;                     // below every score: M before there is one
+// Of a page whose v scale is below kZero the values are as good as zero, and p' only serves the denominator.  It is
+// carried as if the scale were 2^kZeroLog: at 2^0 such a page would hold M up by -log2 vs over the others of its row and
+// leave their p' no bits of fp16.  Not lower, so that 2^30 tokens of p' / 2^kZeroLog stay below 2^126.
+constexpr float kZero = 0x1p-100f, kZeroLog = -80.f, kZeroInverse = -0x1p80f;     // below 0: p' is left out of p v
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);

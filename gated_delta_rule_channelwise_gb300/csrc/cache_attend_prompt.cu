@@ -220,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                     float ks, vs;
                     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(base + kOffScale + ((i & 3) * kGroups + g) * 8));
                     // a scale that is (as good as) zero: the values are zero, whatever the bytes; below zero: no page
-                    const bool zero = vs < 0x1p-100f;
-                    iv[g] = zero ? -1.f : rcp(vs);
-                    const f32x2 c = both(ks * scale), lv = both(vs < 0.f ? -INFINITY : zero ? 0.f : lg2(vs));
+                    const bool zero = vs < kZero;
+                    iv[g] = zero ? kZeroInverse : rcp(vs);
+                    const f32x2 c = both(ks * scale), lv = both(vs < 0.f ? -INFINITY : zero ? kZeroLog : lg2(vs));
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         const float2 y = split(fma2(pair(x[16 * g + e], x[16 * g + e + 1]), c, lv));

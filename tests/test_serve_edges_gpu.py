@@ -1,0 +1,44 @@
+"""GPU tests of the serving operators at the edges of their inputs, against the plain 64-bit forms.
+
+Tolerances are those of test_serve_gpu.py.
+"""
+import pytest
+import torch
+
+import gated_delta_rule_channelwise_gb300 as cg
+from test_serve_gpu import BF, F32, attend_case, check_attend
+
+pytestmark = pytest.mark.gpu
+
+KERNELS = [(F32, 128, cg.ATTEND_ROWS), (F32, 64, cg.ATTEND_ROWS), (BF, 128, cg.ATTEND_ROWS), (BF, 32, cg.ATTEND_ROWS),
+           (BF, 128, cg.ATTEND_TILES)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gated_delta_rule_channelwise_gb300 import build
+    build.build()
+    cg.lib()
+
+
+# ------------------------------------------------------------------------------------ attention
+
+
+@pytest.mark.parametrize("dtype,D,path", KERNELS)
+@pytest.mark.parametrize("size", [1.0, 1e-4, 1e-6, 1e-8, 1e-20])
+def test_attend_pages_of_zeros_beside_small_values(dtype, D, path, size):
+    """Attention is linear in v: a third of the pages hold zeros, the others values of any size."""
+    kv_lens = [200, 333, 64]
+    case = attend_case(50, [1, 40, 3], kv_lens, 4, 2, D, 16, dtype)
+    vs, table = case[4], case[5]
+    vs *= size
+    for b, kv in enumerate(kv_lens):
+        vs[table[b, :-(-kv // 16):3].long()] = 0
+    check_attend(case, dtype, path=path)
+
+
+@pytest.mark.parametrize("dtype,D,path", KERNELS)
+def test_attend_nothing_but_zeros(dtype, D, path):
+    case = attend_case(52, [1, 40], [5000, 333], 4, 2, D, 16, dtype)
+    case[4].zero_()
+    assert not check_attend(case, dtype, path=path).any()
