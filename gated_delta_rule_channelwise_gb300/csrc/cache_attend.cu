@@ -205,10 +205,12 @@ __device__ __forceinline__ void attend_unit(const AttendParams &p, const Request
         for (int r = 0; r < kOf; ++r) {
             const int i = tid + r * 32 * kWarps;
             if (i <= last) {
-                const bool zero = vs[r] < kZero;      // not so for a NaN, which then spreads as it has to
+                // A NaN is not below kZero: by lv it reaches every row that sees the page.  iv leaves it out (fmaxf does),
+                // as 0 times that would reach the denominators of the rows that do not.
+                const bool zero = vs[r] < kZero;
                 info[i].k = ks[r];
                 info[i].lv = zero ? kZeroLog : log2f(vs[r]);
-                info[i].iv = zero ? kZeroInverse : 1.f / vs[r];
+                info[i].iv = zero ? kZeroInverse : fmaxf(1.f / vs[r], 0.f);
             }
         }
         __syncthreads();

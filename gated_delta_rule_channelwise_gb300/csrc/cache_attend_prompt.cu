@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(base + kOffScale + ((i & 3) * kGroups + g) * 8));
                     // a scale that is (as good as) zero: the values are zero, whatever the bytes; below zero: no page
                     const bool zero = vs < kZero;
-                    iv[g] = zero ? kZeroInverse : rcp(vs);
+                    // of a NaN 0, which leaves the rows that do not see it as they are: lv takes it to the others
+                    iv[g] = zero ? kZeroInverse : fmaxf(rcp(vs), 0.f);
                     const f32x2 c = both(ks * scale), lv = both(vs < 0.f ? -INFINITY : zero ? kZeroLog : lg2(vs));
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {

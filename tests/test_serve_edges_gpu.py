@@ -42,3 +42,15 @@ def test_attend_nothing_but_zeros(dtype, D, path):
     case = attend_case(52, [1, 40], [5000, 333], 4, 2, D, 16, dtype)
     case[4].zero_()
     assert not check_attend(case, dtype, path=path).any()
+
+
+@pytest.mark.parametrize("dtype,D,path", KERNELS)
+@pytest.mark.parametrize("which", [3, 4])                                # k's scale, v's
+def test_attend_nan_scale_reaches_only_the_rows_that_see_its_page(dtype, D, path, which):
+    """Prompts over six and ten pages, a later one with a NaN scale: rows before it are as if it were not there."""
+    case = attend_case(51, [90, 7], [90, 150], 4, 2, D, 16, dtype)
+    table = case[5]
+    case[which][table[0, 5]] = float("nan")
+    case[which][table[1, 9], 1] = float("nan")                           # of one head, seen by the last six rows
+    o = check_attend(case, dtype, path=path)                             # NaN exactly where the formula has it
+    assert torch.isfinite(o[:80]).all() and torch.isnan(o[80:90]).all()
