@@ -105,6 +105,13 @@ __device__ __forceinline__ f32x2 softplus_pair(f32x2 v) {
     return fma2(add2(s, s), r, pair(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 
+// -exp(A_log) / log 2, finite: where the exponential overflows, an infinity times a step of zero (a tile's padding, or a
+// softplus that underflows) would be a NaN, and exp(A 0) is 1.  A NaN compares false and stays.
+__device__ __forceinline__ float rate(float A_log) {
+    const float r = -kLog2e * expf(A_log);
+    return r < -3e38f ? -3e38f : r;
+}
+
 // Eight consecutive elements as stored, and as fp32.
 template <typename T> struct Eight;
 template <> struct Eight<__nv_bfloat16> {
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float2 a = split(A[j][n]);
-            A[j][n] = pair(-kLog2e * expf(a.x), -kLog2e * expf(a.y));
+            A[j][n] = pair(rate(a.x), rate(a.y));
         }
     // h <- exp(A d) h + in, for state n of channels 2 j, 2 j + 1
     auto step = [&](int j, int n, f32x2 d, f32x2 in) {
@@ -439,11 +446,11 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanParam
     float d = one(p.dt, b * p.dt_sb + c, p.edt) + (p.dt_bias != nullptr ? __ldg(p.dt_bias + c) : 0.f);
     const float4 bb = quad(p.Bm, b * p.B_sb + g * N + 4 * q, p.eB), cc = quad(p.Cm, b * p.C_sb + g * N + 4 * q, p.eC);
     if (p.softplus) d = split(softplus_pair(both(d))).x;
-    const float u = d * x, s = -kLog2e * d;
-    h.x = fmaf(ex2(s * expf(a.x)), h.x, u * bb.x);
-    h.y = fmaf(ex2(s * expf(a.y)), h.y, u * bb.y);
-    h.z = fmaf(ex2(s * expf(a.z)), h.z, u * bb.z);
-    h.w = fmaf(ex2(s * expf(a.w)), h.w, u * bb.w);
+    const float u = d * x;
+    h.x = fmaf(ex2(d * rate(a.x)), h.x, u * bb.x);
+    h.y = fmaf(ex2(d * rate(a.y)), h.y, u * bb.y);
+    h.z = fmaf(ex2(d * rate(a.z)), h.z, u * bb.z);
+    h.w = fmaf(ex2(d * rate(a.w)), h.w, u * bb.w);
     if (live) *reinterpret_cast<float4 *>(hs) = h;
     float y = fmaf(cc.x, h.x, fmaf(cc.y, h.y, fmaf(cc.z, h.z, cc.w * h.w)));
 #pragma unroll

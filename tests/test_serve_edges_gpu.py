@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import gated_delta_rule_channelwise_gb300 as cg
-from test_serve_gpu import BF, F32, attend_case, check_attend
+import serve_ref as ref
+from test_serve_gpu import BF, F32, attend_case, check_attend, close, gen, offsets, rms, scan_inputs, scan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +55,24 @@ def test_attend_nan_scale_reaches_only_the_rows_that_see_its_page(dtype, D, path
     case[which][table[1, 9], 1] = float("nan")                           # of one head, seen by the last six rows
     o = check_attend(case, dtype, path=path)                             # NaN exactly where the formula has it
     assert torch.isfinite(o[:80]).all() and torch.isnan(o[80:90]).all()
+
+
+# ------------------------------------------------------------------------------------ scan
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [16, 128])
+@pytest.mark.parametrize("lens", [[1], [3, 9], [200]])                   # a step, ragged tiles, a prompt in chunks
+def test_scan_rates_beyond_fp32(dtype, N, lens):
+    """A third of the states decay by exp(100) a unit of time, a channel takes steps that round to zero."""
+    g = gen(11)
+    n, B, cu = sum(lens), len(lens), offsets(lens)
+    s = scan_inputs(g, n, B, 24, N, 1, dtype, True)
+    s["A_log"][:, ::3] = 100.0
+    s["dt"][:, 5] = -200.0
+    want, new = scan_ref(s, ref.spans_of(0, 0, cu))
+    args = [s[k] for k in ("x", "dt", "A_log", "Bm", "Cm", "state")]
+    kw = dict(D=s["D"], z=s["z"], dt_bias=s["dt_bias"])
+    o = cg.scan_decode(*args, **kw) if n == 1 else cg.scan_prefill(*args, cu_seqlens=cu, **kw)
+    close(o, want, 1e-4 * rms(want), dtype)
+    close(s["state"], new, 1e-4 * rms(new))
