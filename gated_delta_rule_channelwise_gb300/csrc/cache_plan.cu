@@ -16,6 +16,7 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanTokens = 1024;                     // tokens of a block
 constexpr int kMaxRequests = 8192;
+constexpr int kStaticBytes = 1024;                    // of shared memory at most, beside the sums
 
 struct PlanParams {
     cgdr_plan_args a;
@@ -40,6 +41,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
     extern __shared__ int s_first[];                  // new tokens before request b, [B + 1]
     int *s_taken = s_first + p.B + 1;                 // pages taken before request b, [B + 1]
     __shared__ int64_t s_warp[2][kPlanThreads / 32];
+    static_assert(sizeof(s_warp) <= kStaticBytes, "shared memory beside the sums");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = kPlanThreads / 32;
     const int count = *p.free_count;
@@ -154,7 +156,7 @@ extern "C" cgdr_status cgdr_cache_plan(const cgdr_plan_args *a, void *stream) {
     if (st != CGDR_OK) return st;
     static SmemOnce smem_once;
     const int bytes = 2 * (a->B + 1) * (int)sizeof(int);
-    if (bytes > 48 * 1024 &&
+    if (bytes + kStaticBytes > 48 * 1024 &&           // the limit without it covers both kinds
         !smem_limit_once(smem_once, reinterpret_cast<const void *>(cache_plan_kernel), 2 * (kMaxRequests + 1) * (int)sizeof(int)))
         return CGDR_ERR_CUDA;
     const int work = a->n_tokens > a->B ? a->n_tokens : a->B;

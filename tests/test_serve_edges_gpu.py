@@ -2,6 +2,10 @@
 
 Tolerances are those of test_serve_gpu.py.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -11,6 +15,7 @@ from test_serve_gpu import BF, F32, attend_case, check_attend, close, gen, offse
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 KERNELS = [(F32, 128, cg.ATTEND_ROWS), (F32, 64, cg.ATTEND_ROWS), (BF, 128, cg.ATTEND_ROWS), (BF, 32, cg.ATTEND_ROWS),
            (BF, 128, cg.ATTEND_TILES)]
 
@@ -76,3 +81,26 @@ def test_scan_rates_beyond_fp32(dtype, N, lens):
     o = cg.scan_decode(*args, **kw) if n == 1 else cg.scan_prefill(*args, cu_seqlens=cu, **kw)
     close(o, want, 1e-4 * rms(want), dtype)
     close(s["state"], new, 1e-4 * rms(new))
+
+
+# ------------------------------------------------------------------------------------ cache plan
+
+
+FRESH_PLAN = """
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+import gated_delta_rule_channelwise_gb300 as cg
+B = int(sys.argv[2])
+ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+p = cg.cache_plan(torch.zeros(B, 1, dtype=torch.int32, device="cuda"), ints([0] * B), ints([1] * B), ints(list(range(B))),
+                  ints([B]), B, 16)
+assert p.slots.tolist() == [16 * (B - 1 - b) for b in range(B)] and p.free_count.tolist() == [0]
+"""
+
+
+@pytest.mark.parametrize("B", [6127, 6128, 6143, 6144])                  # around 48 KB of shared memory
+def test_plan_of_any_size_in_a_fresh_process(B):
+    """Whether a launch is accepted does not depend on the calls before it."""
+    r = subprocess.run([sys.executable, "-c", FRESH_PLAN, ROOT, str(B)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
