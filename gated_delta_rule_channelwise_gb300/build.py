@@ -2,7 +2,7 @@
 
 Every translation unit is compiled by nvcc in parallel, then linked into one
 shared library next to this file.  No CMake; a rebuild happens only when a
-source or header is newer than the library.
+source, a header or this file is newer than the library.
 """
 from __future__ import annotations
 
@@ -40,7 +40,7 @@ def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    return files
+    return files + [os.path.abspath(__file__)]        # the flags
 
 
 def is_stale(lib: str = LIB) -> bool:
@@ -73,10 +73,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = lib + ".tmp.%d" % os.getpid()
-    # One CUDA runtime in the process: with a static copy of its own beside the one that torch has loaded, a call
-    # that allocates its output takes 2.3 us more of the host's time (single-token convolution 12.1 -> 9.8 us).
-    lib64 = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "lib64")
-    cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath", "-Xlinker", lib64, "-o", tmp, *objs]
+    # With a CUDA runtime of its own inside (nvcc's default): a C caller needs no other library, and an error that
+    # another user of a shared runtime has left behind is not taken for one of a launch here.
+    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
