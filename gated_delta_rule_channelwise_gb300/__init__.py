@@ -25,6 +25,8 @@ block, so concurrent calls never affect each other.
 from __future__ import annotations
 
 import ctypes
+import importlib
+import importlib.util
 import os
 import threading
 
@@ -36,6 +38,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_CUDA, ER
 F32, BF16 = 0, 1
 GATE_CHANNEL, GATE_GDN = 0, 1
 PREFILL_AUTO, PREFILL_PER_HEAD, PREFILL_CLUSTER, PREFILL_SIMT, PREFILL_RECURRENT, PREFILL_COOP = range(6)
+ATTEND_AUTO, ATTEND_ROWS, ATTEND_TILES = range(3)
 
 
 class CgdrArgs(ctypes.Structure):
@@ -76,6 +79,17 @@ _SIGNATURES = [
     ("cgdr_workspace_status", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     ("cgdr_prefill_noalloc", ctypes.c_int, [ctypes.POINTER(CgdrArgs), ctypes.c_void_p]),
     ("cgdr_prefill_path_for", ctypes.c_int, [ctypes.POINTER(CgdrArgs)]),
+]
+
+#: The same for include/cgdr_serve.h, whose argument blocks are packed bytes (serve.py).
+SIGNATURES = [
+    ("cgdr_conv", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_scan_workspace_size", ctypes.c_size_t, [ctypes.c_char_p]),
+    ("cgdr_scan", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    ("cgdr_cache_plan", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_cache_append", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_cache_attend_workspace_size", ctypes.c_size_t, [ctypes.c_char_p]),
+    ("cgdr_cache_attend", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
 ]
 
 
@@ -297,11 +311,26 @@ def validate(A: CgdrArgs, for_prefill: bool) -> int:
     return int(lib().cgdr_validate(ctypes.byref(A), 1 if for_prefill else 0))
 
 
-from .serve import (ATTEND_AUTO, ATTEND_ROWS, ATTEND_TILES, CachePlan, SIGNATURES, cache_append,  # noqa: E402
-                    cache_attend, cache_attend_workspace_size, cache_plan, conv_decode, conv_prefill, scan_decode, scan_prefill, scan_workspace_size)
+# The operators around the delta rule: serve.py needs torch, which importing the package does not, so it is imported with
+# the first of them that is asked for.
+_SERVE = ("conv_prefill", "conv_decode", "scan_prefill", "scan_decode", "scan_workspace_size", "CachePlan", "cache_plan",
+          "cache_append", "cache_attend", "cache_attend_workspace_size")
+
+
+def __getattr__(name):
+    if name != "serve" and name not in _SERVE:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    module = importlib.import_module(__name__ + ".serve")
+    value = module if name == "serve" else getattr(module, name)
+    globals()[name] = value
+    return value
+
+
+def __dir__():
+    return sorted({*globals(), *_SERVE, "serve"})
+
 
 __all__ = ["decode", "prefill", "prefill_noalloc", "prefill_workspace_size", "workspace_status", "validate",
            "status_string", "make_args", "prefill_path_for",
-           "conv_prefill", "conv_decode", "scan_prefill", "scan_decode", "scan_workspace_size", "CachePlan",
-           "cache_plan", "cache_append", "cache_attend", "cache_attend_workspace_size",
+           *(_SERVE if importlib.util.find_spec("torch") else ()),
            "CgdrArgs", "CgdrError", "lib", "LIB_PATH"]

@@ -14,17 +14,15 @@ allocator; with ``stream`` they are allocated on that stream.
 """
 from __future__ import annotations
 
-import ctypes
 import struct
 
 import torch
 
-from . import BF16, F32, CgdrError, _need_cuda, lib
+from . import ATTEND_AUTO, ATTEND_ROWS, ATTEND_TILES, BF16, F32, SIGNATURES, CgdrError, _need_cuda, lib  # noqa: F401
 
 _F32, _I32 = torch.float32, torch.int32
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
 _NONE = (0, 0, 0)
-ATTEND_AUTO, ATTEND_ROWS, ATTEND_TILES = range(3)
 
 
 class Block:
@@ -456,15 +454,3 @@ def cache_attend_workspace_size(B, n, Hq, Hkv, D, page, width, *, max_q, max_kv=
     block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _CODES[dtype], 1, max_q,
                         min(width * page, _MAX_KV) if max_kv is None else max_kv, path, 0, 0.0, fake, Hq * D, D, fake, Hq * D, D, fake, fake, fake, fake, fake, width, fake, fake, 0)
     return lib().cgdr_cache_attend_workspace_size(block)
-
-
-#: (name, restype, argtypes) of every symbol include/cgdr_serve.h declares.
-SIGNATURES = [
-    ("cgdr_conv", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
-    ("cgdr_scan_workspace_size", ctypes.c_size_t, [ctypes.c_char_p]),
-    ("cgdr_scan", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
-    ("cgdr_cache_plan", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
-    ("cgdr_cache_append", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
-    ("cgdr_cache_attend_workspace_size", ctypes.c_size_t, [ctypes.c_char_p]),
-    ("cgdr_cache_attend", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
-]
