@@ -151,10 +151,21 @@ def _check_status(status):
         raise TypeError("status must be an int32 CUDA tensor")
 
 
+def _device_now():
+    import torch
+    return torch.cuda.current_device()
+
+
 def _need_cuda(*ts):
-    for t in ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError("every tensor must live on a CUDA device (the library has no CPU path)")
+    """All on one CUDA device, the calling thread's current one: that is where the library launches."""
+    devices = {t.get_device() for t in ts if t is not None}
+    if min(devices, default=0) < 0:
+        raise ValueError("every tensor must live on a CUDA device (the library has no CPU path)")
+    if len(devices) > 1:
+        raise ValueError("the tensors of a call must share one device, got %s" % sorted(devices))
+    if devices and devices != {_device_now()}:
+        raise ValueError("the tensors are on CUDA device %d, the current device is %d (torch.cuda.device makes theirs current)"
+                         % (*devices, _device_now()))
 
 
 def _ptr_strides(t, name):
@@ -207,9 +218,9 @@ def make_args(q, k, v, state, o, *, T, g=None, beta=None, a=None, b=None, A_log=
                     status.data_ptr() if status is not None else None)
 
 
-def _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias):
+def _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias, *others):
     import torch
-    _need_cuda(q, k, v, state, o, g, beta, a, b, A_log, dt_bias)
+    _need_cuda(q, k, v, state, o, g, beta, a, b, A_log, dt_bias, *others)
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k and v must share one dtype")
     if o.dtype not in (torch.float32, torch.bfloat16):
@@ -234,8 +245,8 @@ def decode(q, k, v, state, o=None, *, g=None, beta=None, a=None, b=None, A_log=N
     import torch
     if o is None:
         o = torch.empty(v.shape, dtype=torch.float32, device=v.device)
-    _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias)
     _check_status(status)
+    _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias, status)
     u = lambda t: None if t is None else t.unsqueeze(1)
     A = make_args(u(q), u(k), u(v), state, u(o), T=1, g=u(g), beta=u(beta), a=u(a), b=u(b),
                   A_log=A_log, dt_bias=dt_bias, l2norm=l2norm, q_scale=q_scale, eps=eps,
@@ -264,8 +275,8 @@ def prefill(q, k, v, state, o=None, *, g=None, beta=None, a=None, b=None, A_log=
     import torch
     if o is None:
         o = torch.empty(v.shape, dtype=torch.float32, device=v.device)
-    _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias)
     _check_status(status)
+    _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias, status, workspace)
     A = make_args(q, k, v, state, o, T=q.shape[1], g=g, beta=beta, a=a, b=b, A_log=A_log, dt_bias=dt_bias,
                   l2norm=l2norm, q_scale=q_scale, eps=eps, chunk=chunk, path=path, wait_polls=wait_polls,
                   status=status)
@@ -287,8 +298,8 @@ def prefill_noalloc(q, k, v, state, o=None, *, g=None, beta=None, a=None, b=None
     import torch
     if o is None:
         o = torch.empty(v.shape, dtype=torch.float32, device=v.device)
-    _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias)
     _check_status(status)
+    _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias, status)
     A = make_args(q, k, v, state, o, T=q.shape[1], g=g, beta=beta, a=a, b=b, A_log=A_log, dt_bias=dt_bias,
                   l2norm=l2norm, q_scale=q_scale, eps=eps, chunk=chunk, path=path, status=status)
     _check(lib().cgdr_prefill_noalloc(ctypes.byref(A), _stream_handle(stream)), "cgdr_prefill_noalloc")

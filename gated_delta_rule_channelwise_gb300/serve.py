@@ -3,8 +3,9 @@
 Python side of ``include/cgdr_serve.h``: each call checks types and shapes, packs the argument
 block of its C entry point and runs it on the current CUDA stream (or ``stream``).  As for
 :func:`~gated_delta_rule_channelwise_gb300.decode`, every step runs in the library's kernels and
-there is no CPU fallback.  Outputs that are not given, and workspaces, come from torch's caching
-allocator; with ``stream`` they are allocated on that stream.
+there is no CPU fallback.  The tensors of a call share one device, the current one.  Outputs that
+are not given, and workspaces, come from torch's caching allocator; with ``stream`` they are
+allocated on that stream.
 
 * :func:`conv_prefill`, :func:`conv_decode` -- short causal convolution with its state.
 * :func:`scan_prefill`, :func:`scan_decode` -- selective state space scan.
@@ -85,6 +86,9 @@ def _on(stream, fn, *args, **kw):
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
+# The current device, without the initialisation check of torch.cuda.current_device: only asked beside a CUDA tensor.
+_here = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _refuse(dtypes, shapes, dense):
     """Raises for what is wrong: (name, tensor, dtype), (name, tensor, shape) and (name, tensor) triples.
@@ -112,10 +116,16 @@ def _address(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _status_word(status):
+def _status_word(status, device):
     if status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda:
         raise TypeError("status must be an int32 CUDA tensor")
+    if status.get_device() != device:
+        raise ValueError("status is on CUDA device %d, the other tensors on %d" % (status.get_device(), device))
     return status.data_ptr()
+
+
+def _on_device(t, device):
+    return t is None or t.get_device() == device
 
 
 def _rows(t, name, step):
@@ -158,8 +168,9 @@ def _sequences(x, state, cu):
 
 def _conv(x, weight, state, o, bias, silu, B, T, cu, status):
     """x is [B, T, C], or [B, C] / packed [n, C] (T is 1 / 0)."""
-    if not (x.is_cuda and weight.is_cuda and state.is_cuda and (bias is None or bias.is_cuda) and (cu is None or cu.is_cuda)
-            and (o is None or o.is_cuda)):
+    device = x.get_device()
+    if not (device >= 0 and device == weight.get_device() == state.get_device() == _here() and _on_device(bias, device)
+            and _on_device(cu, device) and _on_device(o, device)):
         _need_cuda(x, weight, state, o, bias, cu)
     if o is None:
         o = torch.empty_like(x)
@@ -172,8 +183,8 @@ def _conv(x, weight, state, o, bias, silu, B, T, cu, status):
                 [("weight", weight), ("bias", bias), ("state", state)])
     block = CONV.pack(B, T, C, W, _CODES.get(dtype, -1), 1 if silu else 0, 0 if cu is None else shape[0], 0, *_rows(x, "x", step),
                       *_rows(o, "o", step), weight.data_ptr(), _address(bias), state.data_ptr(), _address(cu),
-                      0 if status is None else _status_word(status))
-    st = lib().cgdr_conv(block, _current(x.get_device()))
+                      0 if status is None else _status_word(status, device))
+    st = lib().cgdr_conv(block, _current(device))
     if st:
         raise CgdrError(st, "cgdr_conv")
     return o
@@ -207,10 +218,10 @@ def conv_decode(x, weight, state, o=None, *, bias=None, silu=True, status=None, 
 
 def _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, B, T, cu, workspace, status):
     """x is [B, T, C], or [B, C] / packed [n, C] (T is 1 / 0)."""
-    if not (x.is_cuda and dt.is_cuda and A_log.is_cuda and Bm.is_cuda and Cm.is_cuda and state.is_cuda
-            and (o is None or o.is_cuda) and (D is None or D.is_cuda) and (z is None or z.is_cuda)
-            and (dt_bias is None or dt_bias.is_cuda) and (cu is None or cu.is_cuda)
-            and (workspace is None or workspace.is_cuda)):
+    device = x.get_device()
+    if not (device >= 0 and device == dt.get_device() == A_log.get_device() == Bm.get_device() == Cm.get_device()
+            == state.get_device() == _here() and _on_device(o, device) and _on_device(D, device) and _on_device(z, device)
+            and _on_device(dt_bias, device) and _on_device(cu, device) and _on_device(workspace, device)):
         _need_cuda(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, cu, workspace)
     if o is None:
         o = torch.empty_like(x)
@@ -229,12 +240,12 @@ def _scan(x, dt, A_log, Bm, Cm, state, o, D, z, dt_bias, softplus, B, T, cu, wor
     block = SCAN.pack(B, T, C, N, G, _CODES.get(dtype, -1), _CODES.get(o.dtype, -1), 1 if softplus else 0, 0 if cu is None else shape[0], 0,
                       *_rows(x, "x", step), *_rows(dt, "dt", step), *(_rows(z, "z", step) if z is not None else _NONE),
                       *_grouped(Bm, "Bm", step, grouped), *_grouped(Cm, "Cm", step, grouped), *_rows(o, "o", step), A_log.data_ptr(),
-                      _address(D), _address(dt_bias), state.data_ptr(), _address(cu), 0 if status is None else _status_word(status))
+                      _address(D), _address(dt_bias), state.data_ptr(), _address(cu), 0 if status is None else _status_word(status, device))
     L = lib()
     need = 0 if T == 1 else L.cgdr_scan_workspace_size(block)
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    st = L.cgdr_scan(block, workspace.data_ptr() if need else None, need, _current(x.get_device()))
+    st = L.cgdr_scan(block, workspace.data_ptr() if need else None, need, _current(device))
     if st:
         raise CgdrError(st, "cgdr_scan")
     return o
@@ -330,8 +341,10 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
     if stream is not None:
         return _on(stream, cache_plan, block_table, seq_lens, new_lens, free_pages, free_count, n_tokens, page, out,
                    num_pages=num_pages, status=status)
-    if not (block_table.is_cuda and seq_lens.is_cuda and new_lens.is_cuda and free_pages.is_cuda and free_count.is_cuda):
-        _need_cuda(block_table, seq_lens, new_lens, free_pages, free_count)
+    device = block_table.get_device()
+    if not (device >= 0 and device == seq_lens.get_device() == new_lens.get_device() == free_pages.get_device()
+            == free_count.get_device() == _here() and (out is None or out._buffer.get_device() == device)):
+        _need_cuda(block_table, seq_lens, new_lens, free_pages, free_count, None if out is None else out._buffer)
     B, width = block_table.shape
     F = free_pages.numel()
     if out is None:
@@ -348,8 +361,8 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
         raise ValueError("block_table: innermost dimension must be contiguous")
     block = PLAN.pack(B, width, page, n_tokens, F, 0x7FFFFFFF if num_pages is None else num_pages,
                       block_table.data_ptr(), sb, seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
-                      free_count.data_ptr(), *out._addresses, 0 if status is None else _status_word(status))
-    st = lib().cgdr_cache_plan(block, _current(block_table.get_device()))
+                      free_count.data_ptr(), *out._addresses, 0 if status is None else _status_word(status, device))
+    st = lib().cgdr_cache_plan(block, _current(device))
     if st:
         raise CgdrError(st, "cgdr_cache_plan")
     return out
@@ -357,7 +370,8 @@ def cache_plan(block_table, seq_lens, new_lens, free_pages, free_count, n_tokens
 
 def _check_cache(k_cache, v_cache, k_scale, v_scale):
     """(pages, Hkv, page, D) of a cache: int8 [pages, Hkv, page, D] with fp32 scales [pages, Hkv]."""
-    if not (k_cache.is_cuda and v_cache.is_cuda and k_scale.is_cuda and v_scale.is_cuda):
+    device = k_cache.get_device()
+    if not (device >= 0 and device == v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == _here()):
         _need_cuda(k_cache, v_cache, k_scale, v_scale)
     shape = k_cache.shape
     if len(shape) != 4:
@@ -381,8 +395,9 @@ def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, status=None
     if stream is not None:
         return _on(stream, cache_append, k, v, slots, k_cache, v_cache, k_scale, v_scale, status=status)
     pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
-    if not (k.is_cuda and v.is_cuda and slots.is_cuda):
-        _need_cuda(k, v, slots)
+    device = k.get_device()
+    if not (device == v.get_device() == slots.get_device() == k_cache.get_device()):
+        _need_cuda(k, v, slots, k_cache)
     n = k.shape[0]
     shape = (n, Hkv, D)
     if not (k.shape == shape and v.shape == shape and v.dtype == k.dtype and _fits(slots, torch.int64, (n,))):
@@ -390,8 +405,8 @@ def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, status=None
                 [("slots", slots)])
     block = APPEND.pack(n, Hkv, D, page, _CODES.get(k.dtype, -1), pages, *_heads(k, "k"), *_heads(v, "v"), slots.data_ptr(),
                         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                        0 if status is None else _status_word(status))
-    st = lib().cgdr_cache_append(block, _current(k.get_device()))
+                        0 if status is None else _status_word(status, device))
+    st = lib().cgdr_cache_append(block, _current(device))
     if st:
         raise CgdrError(st, "cgdr_cache_append")
 
@@ -415,11 +430,12 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
         return _on(stream, cache_attend, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o,
                    max_q=max_q, max_kv=max_kv, scale=scale, path=path, workspace=workspace, status=status, wait_polls=wait_polls)
     pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    device = q.get_device()
+    if not (device == block_table.get_device() == kv_lens.get_device() == cu_seqlens.get_device() == k_cache.get_device()
+            and _on_device(o, device) and _on_device(workspace, device)):
+        _need_cuda(q, o, block_table, kv_lens, cu_seqlens, workspace, k_cache)
     if o is None:
         o = torch.empty_like(q)
-    if not (q.is_cuda and o.is_cuda and block_table.is_cuda and kv_lens.is_cuda and cu_seqlens.is_cuda
-            and (workspace is None or workspace.is_cuda)):
-        _need_cuda(q, o, block_table, kv_lens, cu_seqlens, workspace)
     n, Hq, Dq = q.shape
     if Dq != D:
         raise ValueError("q has head dimension %d, the cache %d" % (Dq, D))
@@ -436,12 +452,12 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     block = ATTEND.pack(B, n, Hq, Hkv, D, page, width, _CODES.get(q.dtype, -1), pages, max_q,
                         min(width * page, _MAX_KV) if max_kv is None else max_kv, path, wait_polls, 0.0 if scale is None else scale, *_heads(q, "q"), *_heads(o, "o"), k_cache.data_ptr(),
                         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), sb,
-                        kv_lens.data_ptr(), cu_seqlens.data_ptr(), 0 if status is None else _status_word(status))
+                        kv_lens.data_ptr(), cu_seqlens.data_ptr(), 0 if status is None else _status_word(status, device))
     L = lib()
     need = L.cgdr_cache_attend_workspace_size(block)
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = L.cgdr_cache_attend(block, workspace.data_ptr() if need else None, need, _current(q.get_device()))
+    st = L.cgdr_cache_attend(block, workspace.data_ptr() if need else None, need, _current(device))
     if st:
         raise CgdrError(st, "cgdr_cache_attend")
     return o
