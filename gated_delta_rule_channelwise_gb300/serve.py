@@ -417,7 +417,7 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     bf16) packs the query tokens of all requests, ``cu_seqlens [B+1]`` says whose they are; they are the last of
     the ``kv_lens[b]`` cached tokens, each sees the tokens up to itself, and a row that sees nothing is zero.
     ``block_table [B,width]``, ``kv_lens``, ``cu_seqlens`` int32 as :func:`cache_plan` leaves them.  Query head h
-    reads key-value head h / (Hq/Hkv); ``scale`` defaults to 1/sqrt(D).
+    reads key-value head h / (Hq/Hkv); ``scale``, above 0, defaults to 1/sqrt(D).
 
     ``max_q`` and ``max_kv`` bound the requests' query and cached tokens on the host (default for max_kv: what
     the table holds); what exceeds them is cut off and reported in ``status`` (``ERR_CAPACITY``), and pages
@@ -429,6 +429,8 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     if stream is not None:
         return _on(stream, cache_attend, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o,
                    max_q=max_q, max_kv=max_kv, scale=scale, path=path, workspace=workspace, status=status, wait_polls=wait_polls)
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be above 0, got %s" % scale)    # the library would take its default
     pages, Hkv, page, D = _check_cache(k_cache, v_cache, k_scale, v_scale)
     device = q.get_device()
     if not (device == block_table.get_device() == kv_lens.get_device() == cu_seqlens.get_device() == k_cache.get_device()
