@@ -62,7 +62,42 @@ def test_attend_nan_scale_reaches_only_the_rows_that_see_its_page(dtype, D, path
     assert torch.isfinite(o[:80]).all() and torch.isnan(o[80:90]).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_attend_more_pages_than_a_block_holds_at_a_time(dtype):
+    """29 requests that share 325 pages of 16 tokens: 928 units with a block each, which looks up 320 pages, then the rest."""
+    B, page, kv, Hkv, D = 29, 16, 5200, 32, 32
+    q, kc, vc, ks, vs, table, _, _ = attend_case(53, [9 * B], [kv], Hkv, Hkv, D, page, dtype)
+    lens = torch.full((B,), kv, dtype=torch.int32, device="cuda")
+    case = (q, kc, vc, ks, vs, table.expand(B, -1).contiguous(), lens, offsets([9] * B))
+    assert cg.cache_attend_workspace_size(B, 9 * B, Hkv, Hkv, D, page, table.shape[1], max_q=9, max_kv=kv, dtype=dtype) == 0
+    check_attend(case, dtype)
+
+
+@pytest.mark.parametrize("path", [cg.ATTEND_AUTO, cg.ATTEND_ROWS, cg.ATTEND_TILES])
+def test_attend_one_prompt_among_many_single_tokens_bf16(path):
+    q_lens = [1] * 20 + [600] + [0, 1] * 10
+    kv_lens = [(37 * i) % 300 for i in range(20)] + [700] + [5, 129] * 10
+    check_attend(attend_case(54, q_lens, kv_lens, 8, 2, 128, 32, BF), BF, path=path)
+
+
 # ------------------------------------------------------------------------------------ scan
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [16, 64])
+@pytest.mark.parametrize("lens", [[5000], [3000, 0, 1701, 40]])
+def test_scan_many_chunks(dtype, N, lens):
+    """Sequences of dozens of chunks.  The states here forget within some 300 tokens (rates of 0.4 a unit of time
+    and more, steps of 0.03 and more in all but a few), so the bound for 300 tokens holds for any number."""
+    g = gen(12 + N)
+    n, B, cu = sum(lens), len(lens), offsets(lens)
+    s = scan_inputs(g, n, B, 24, N, 1, dtype, True)
+    assert cg.scan_workspace_size(B, 0, 24, N, n_tokens=n, dtype=dtype) > 20 * 4 * 24 * N
+    want, new = scan_ref(s, ref.spans_of(0, 0, cu))
+    o = cg.scan_prefill(s["x"], s["dt"], s["A_log"], s["Bm"], s["Cm"], s["state"], D=s["D"], z=s["z"], dt_bias=s["dt_bias"],
+                        cu_seqlens=cu)
+    close(o, want, 1e-4 * rms(want), dtype)
+    close(s["state"], new, 1e-4 * rms(new))
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
