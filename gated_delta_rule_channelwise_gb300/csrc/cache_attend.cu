@@ -22,8 +22,9 @@
 // p' = 2^(s + log2 vs - M), with its own running maximum M of s + log2 vs, so that p' lies in (0, 1]
 // whatever the scales are and fits fp16; the denominator adds p' / vs (of pages of zeros, which have
 // no logarithm, see kZero).  M follows the maximum loosely:
-// it is only looked for, over the lanes, when some score passes it by more than 2^7, which after the
-// first step is rare, and a vote otherwise.  p' is carried times 2^8: it stays below 2^15 even so,
+// it is only looked for, over the lanes, when some score passes it by more than 2^7, which in a tile whose
+// rows are all in use is rare after the first step, and a vote otherwise.  (Unused rows of a tile keep M at kLowest and
+// pass it in every step, so a tile that is not full looks each time; their results go nowhere.)  p' is carried times 2^8: it stays below 2^15 even so,
 // and keeps fp16's relative accuracy down to 2^-22 of the largest (2^-33 of it is where it ends).
 //
 // A unit is (request, row tile, key-value head), its cost the 128-token steps of its cache.  Where units are

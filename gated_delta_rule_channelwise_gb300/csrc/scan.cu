@@ -16,7 +16,7 @@
 // Measured: one sequence of 4,000 tokens, 4,096 bf16 channels, N = 16, gated: 132 us for 262 M exponentials done
 // twice, which are 57 us of their unit; the schedulers issue in 49 % of the cycles with the 12 warps that
 // 160 registers a thread leave an SM (16 warps with fewer registers: 138 us).  Three sequences of 1 to 16,411 tokens,
-// 24,618 in all, of 1,000 fp32 channels: 200 us.  A step of 64 x 4,096 channels: 8.1 us for 35.9 MB.
+// 24,618 in all, of 1,000 fp32 channels: 200 us.  A step of 64 x 4,096 channels: 8.8 us for 35.9 MB.
 #include "serve.cuh"
 
 namespace cgdr {
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(ScanShape<N>::NT, N == 128 ? 3 : 6) scan_kerne
 }
 
 // One token a sequence: a thread reads, updates and writes four states.  Bound by the state's bytes: 64 x 4,096 channels
-// take 8.1 us, and 17.4 in the kernel above, which stages tiles of tokens.
+// take 8.8 us (8.6 with rates that may be infinite), and 17.4 in the kernel above, which stages tiles of tokens.
 constexpr int kStepThreads = 128;
 template <typename T> __device__ __forceinline__ float4 four(const T *p);
 template <> __device__ __forceinline__ float4 four<float>(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }

@@ -5,7 +5,7 @@ block of its C entry point and runs it on the current CUDA stream (or ``stream``
 :func:`~gated_delta_rule_channelwise_gb300.decode`, every step runs in the library's kernels and
 there is no CPU fallback.  The tensors of a call share one device, the current one.  Outputs that
 are not given, and workspaces, come from torch's caching allocator; with ``stream`` they are
-allocated on that stream.
+allocated on that stream.  An output may not overlap an input, other than what is updated in place.
 
 * :func:`conv_prefill`, :func:`conv_decode` -- short causal convolution with its state.
 * :func:`scan_prefill`, :func:`scan_decode` -- selective state space scan.
@@ -389,8 +389,8 @@ def cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, status=None
     """Quantise ``k, v [n,Hkv,D]`` (fp32 or bf16) into the cache: ``k_cache, v_cache`` int8
     ``[pages,Hkv,page,D]``, ``k_scale, v_scale`` fp32 ``[pages,Hkv]``, all updated in place.  Token i goes to
     ``slots[i]`` (int64, as :func:`cache_plan` gives them: tokens of a page consecutive and ascending; below 0:
-    nowhere).  A page's scale of a head is the largest magnitude in it / 127; where new values raise it, what
-    the page holds is rounded to the larger scale.  A token at a page's offset 0 starts the page afresh.  A
+    nowhere).  A page's scale of a head is the largest magnitude in it times 1/127 (in fp32); where new values
+    raise it, what the page holds is rounded to the larger scale.  A token at a page's offset 0 starts the page afresh.  A
     slot outside the cache is skipped and reported in ``status`` (``ERR_BOUNDS``)."""
     if stream is not None:
         return _on(stream, cache_append, k, v, slots, k_cache, v_cache, k_scale, v_scale, status=status)
@@ -425,6 +425,8 @@ def cache_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu
     o ``[n,Hq,D]``, like q.  ``path`` forces one of the two kernels for this call (``ATTEND_ROWS``,
     ``ATTEND_TILES``; the latter covers bf16 with D = 128).  ``workspace``: a buffer of
     :func:`cache_attend_workspace_size` bytes (for dense q and o) or more keeps the call free of allocations.
+    The choice goes by ``max_q`` and ``max_kv`` as if every request had them: a long prompt among many single
+    tokens over long caches takes less time in a call of its own.
     ``wait_polls``: polls of a bounded device wait (0: the default; ``ERR_TIMEOUT`` in ``status`` when one gives up)."""
     if stream is not None:
         return _on(stream, cache_attend, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, o,

@@ -130,10 +130,10 @@ cgdr_status cgdr_cache_plan(const cgdr_plan_args *args, void *stream);
  *
  * Append: packed token i of k and v goes to slots[i] (page * page_size + offset; below 0: nowhere).
  * Tokens that go to one page are consecutive and ascend, as cgdr_cache_plan lays them out.  Per
- * (page, head) the scale becomes max(old, amax / 127) over the new values, with old = 0 where the
- * first new token enters the page at offset 0 (what a page held for an earlier request plays no
- * part); where it grows, the values already in the page are rounded to it.  To nearest, ties to
- * even; all divisions as IEEE has them.  A NaN or an infinity makes the scale of its page and head
+ * (page, head) the scale becomes max(old, amax * r) over the new values, r = 1/127 rounded to fp32 (one
+ * unit in the last place from the quotient at most), with old = 0 where the first new token enters the
+ * page at offset 0 (what a page held for an earlier request plays no part); where it grows, the values
+ * already in the page are rounded to it.  To nearest, ties to even, of the IEEE quotient by the scale.  A NaN or an infinity makes the scale of its page and head
  * non-finite, and with it every value of that page and head.
  * A slot outside the cache is skipped and reported as CGDR_ERR_BOUNDS.
  */
@@ -157,15 +157,18 @@ cgdr_status cgdr_cache_append(const cgdr_append_args *args, void *stream);
  * head h reads key-value head h / (Hq/Hkv).  softmax(scale q.k) v, softmax and sums in fp32; a row
  * that sees nothing (kv_lens[b] < q_len) is zero.  `max_q` and `max_kv` bound q_len and kv_lens on
  * the host (they size the launch): what exceeds them, or the table's width * page, is cut off and
- * reported as CGDR_ERR_CAPACITY.  Table entries past a request's pages are not read; a page
+ * reported as CGDR_ERR_CAPACITY, rows of o beyond max_q stay as they are.  Table entries past a request's pages are not read; a page
  * outside [0, num_pages) is left out of the sums and reported as CGDR_ERR_BOUNDS.
  * Where rows are few, key-value positions are split over CTAs; `workspace` (16-byte aligned) holds the parts.
  * A wait that gives up reports CGDR_ERR_TIMEOUT in *status; the rows of its CTA are then undefined.
  * bf16: products of fp16 operands (int8 values are exact in fp16, queries are scaled by a power of
- * two per row first).  fp32: both queries and probabilities in two fp16 parts.
+ * two per row first).  fp32: both queries and probabilities in two fp16 parts.  A page's v scale below 2^-100 counts as
+ * zero; a NaN in a scale reaches the rows that see its page, and no others.
  */
 typedef enum cgdr_attend_path {
-    CGDR_ATTEND_AUTO = 0,           /* per call: whichever of the two needs less time by what they measured */
+    CGDR_ATTEND_AUTO = 0,           /* per call: whichever of the two measured less time where every request has max_q
+                                       query tokens and max_kv cached ones; a long prompt among many single tokens
+                                       over long caches takes less in a call of its own */
     CGDR_ATTEND_ROWS = 1,           /* row tiles of 8 or 16; a CTA a tile, or the cache split evenly over all SMs */
     CGDR_ATTEND_TILES = 2           /* tensor memory, row tiles of 128, the cache in parts where they are few (bf16,
                                        D = 128, o in 16-byte rows; elsewhere ROWS) */
