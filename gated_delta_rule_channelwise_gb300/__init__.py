@@ -276,7 +276,8 @@ def prefill(q, k, v, state, o=None, *, g=None, beta=None, a=None, b=None, A_log=
     if o is None:
         o = torch.empty(v.shape, dtype=torch.float32, device=v.device)
     _check_status(status)
-    _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias, status, workspace)
+    _check_types(q, k, v, state, o, g, beta, a, b, A_log, dt_bias, status,
+                 workspace if workspace is not None and workspace.is_cuda else None)
     A = make_args(q, k, v, state, o, T=q.shape[1], g=g, beta=beta, a=a, b=b, A_log=A_log, dt_bias=dt_bias,
                   l2norm=l2norm, q_scale=q_scale, eps=eps, chunk=chunk, path=path, wait_polls=wait_polls,
                   status=status)
@@ -284,6 +285,8 @@ def prefill(q, k, v, state, o=None, *, g=None, beta=None, a=None, b=None, A_log=
     need = int(L.cgdr_prefill_workspace_size(ctypes.byref(A)))
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if need > 0:                                      # one that is not needed may be anything
+        _need_cuda(workspace)
     ws_ptr = workspace.data_ptr() if (workspace is not None and need > 0) else 0
     ws_bytes = workspace.numel() * workspace.element_size() if (workspace is not None and need > 0) else 0
     _check(L.cgdr_prefill(ctypes.byref(A), ctypes.c_void_p(ws_ptr), ctypes.c_size_t(ws_bytes),

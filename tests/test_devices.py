@@ -117,3 +117,21 @@ def test_plan_into_buffers_of_another_device():
     out._buffer.index = 1
     with pytest.raises(ValueError, match="one device"):
         fn(*args, out=out)
+
+
+@pytest.mark.parametrize("need", [0, 4])
+def test_prefill_looks_at_a_workspace_only_where_it_needs_one(monkeypatch, need):
+    """A host tensor (an empty one, say) is fine for a kernel that needs none, and refused where its address would be used."""
+    class Library:
+        cgdr_prefill_workspace_size = staticmethod(lambda args: need)
+        cgdr_prefill = staticmethod(lambda *args: cg.OK)
+
+    monkeypatch.setattr(cg, "lib", Library)
+    monkeypatch.setattr(cg, "_stream_handle", lambda stream: None)
+    fn, args, kw = prefill(lambda *a, **k: at(0, *a, **k))
+    kw["workspace"] = torch.zeros(8)
+    if need:
+        with pytest.raises(ValueError, match="CUDA device"):
+            fn(*args, **kw)
+    else:
+        assert fn(*args, **kw) is kw["o"]
