@@ -17,6 +17,8 @@ Public calls (same names as the C ABI without the ``cgdr_`` prefix):
 * the operators around the delta rule (``include/cgdr_serve.h``, :mod:`.serve`): :func:`conv_prefill`,
   :func:`conv_decode`, :func:`scan_prefill`, :func:`scan_decode`, :func:`cache_plan`, :func:`cache_append`,
   :func:`cache_attend`.
+* the operators around a layer's state (``include/cgdr_layer.h``, :mod:`.layer`): :func:`rms_norm`, :func:`rms_norm_fp8`,
+  :func:`fp8_quantize`, :func:`fp8_quantize_weight`, :func:`fp8_matmul`, :func:`rotary`, :func:`rotary_frequencies`.
 
 The prefill kernel is chosen per call (``path=``, one of the ``PREFILL_*``
 codes; ``PREFILL_AUTO`` by default): the choice travels in the argument
@@ -39,6 +41,7 @@ F32, BF16 = 0, 1
 GATE_CHANNEL, GATE_GDN = 0, 1
 PREFILL_AUTO, PREFILL_PER_HEAD, PREFILL_CLUSTER, PREFILL_SIMT, PREFILL_RECURRENT, PREFILL_COOP = range(6)
 ATTEND_AUTO, ATTEND_ROWS, ATTEND_TILES = range(3)
+MATMUL_AUTO, MATMUL_FEW, MATMUL_TILES = range(3)
 
 
 class CgdrArgs(ctypes.Structure):
@@ -81,7 +84,7 @@ _SIGNATURES = [
     ("cgdr_prefill_path_for", ctypes.c_int, [ctypes.POINTER(CgdrArgs)]),
 ]
 
-#: The same for include/cgdr_serve.h, whose argument blocks are packed bytes (serve.py).
+#: The same for include/cgdr_serve.h and include/cgdr_layer.h, whose argument blocks are packed bytes (serve.py, layer.py).
 SIGNATURES = [
     ("cgdr_conv", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
     ("cgdr_scan_workspace_size", ctypes.c_size_t, [ctypes.c_char_p]),
@@ -90,6 +93,10 @@ SIGNATURES = [
     ("cgdr_cache_append", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
     ("cgdr_cache_attend_workspace_size", ctypes.c_size_t, [ctypes.c_char_p]),
     ("cgdr_cache_attend", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    ("cgdr_norm", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_quantize", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_matmul", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
+    ("cgdr_rotary", ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
 ]
 
 
@@ -325,26 +332,28 @@ def validate(A: CgdrArgs, for_prefill: bool) -> int:
     return int(lib().cgdr_validate(ctypes.byref(A), 1 if for_prefill else 0))
 
 
-# The operators around the delta rule: serve.py needs torch, which importing the package does not, so it is imported with
-# the first of them that is asked for.
+# The operators around the delta rule: serve.py and layer.py need torch, which importing the package does not, so each is
+# imported with the first of its names that is asked for.
 _SERVE = ("conv_prefill", "conv_decode", "scan_prefill", "scan_decode", "scan_workspace_size", "CachePlan", "cache_plan",
           "cache_append", "cache_attend", "cache_attend_workspace_size")
+_LAYER = ("rms_norm", "rms_norm_fp8", "fp8_quantize", "fp8_quantize_weight", "fp8_matmul", "rotary", "rotary_frequencies")
+_LATE = {**dict.fromkeys((*_SERVE, "serve"), "serve"), **dict.fromkeys((*_LAYER, "layer"), "layer")}
 
 
 def __getattr__(name):
-    if name != "serve" and name not in _SERVE:
+    if name not in _LATE:
         raise AttributeError("module %r has no attribute %r" % (__name__, name))
-    module = importlib.import_module(__name__ + ".serve")
-    value = module if name == "serve" else getattr(module, name)
+    module = importlib.import_module(__name__ + "." + _LATE[name])
+    value = module if name == _LATE[name] else getattr(module, name)
     globals()[name] = value
     return value
 
 
 def __dir__():
-    return sorted({*globals(), *_SERVE, "serve"})
+    return sorted({*globals(), *_LATE})
 
 
 __all__ = ["decode", "prefill", "prefill_noalloc", "prefill_workspace_size", "workspace_status", "validate",
            "status_string", "make_args", "prefill_path_for",
-           *(_SERVE if importlib.util.find_spec("torch") else ()),
+           *((*_SERVE, *_LAYER) if importlib.util.find_spec("torch") else ()),
            "CgdrArgs", "CgdrError", "lib", "LIB_PATH"]

@@ -1,0 +1,102 @@
+// What the two kernels of the 8-bit matrix product share: parameters, copies, products, bounded waits.
+#pragma once
+
+#include "layer.cuh"
+#include "tc05.cuh"
+
+namespace cgdr {
+
+struct MatmulParams {
+    CUtensorMap mx, mw;                               // first: 64-byte aligned
+    int n, N, K, blocks;                              // blocks of 128 along K
+    const float *xs, *ws;
+    void *o;
+    int64_t o_st, eo;                                 // and its footprint (index-checking build)
+    int o_f32;
+    int *status;
+    uint32_t polls;
+    int inject;
+};
+
+bool matmul_few(const cgdr_matmul_args &a);           // whether the kernel for few rows takes the call
+cgdr_status launch_matmul_few(const cgdr_matmul_args &a, MatmulParams &p, cudaStream_t s);
+cgdr_status launch_matmul_tiles(const cgdr_matmul_args &a, MatmulParams &p, cudaStream_t s);
+// A tensor map of [rows, K] bytes with boxes of 128 bytes by `box` rows, swizzled by 128 bytes.
+bool encode_rows(CUtensorMap &m, const void *base, int64_t K, int64_t rows, int64_t stride, int box);
+
+constexpr uint32_t kMatmulPolls = 1u << 18;           // of a wait, before it gives up (args.wait_polls, 0)
+constexpr int kBlockK = 128;                          // bytes of a row in a stage: the values of a scale
+
+namespace fp8 {
+
+using namespace tc05;
+
+// D[128 x N] (+)= A[128 x 32] B[N x 32]^T, e4m3 both, fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// A block of K: four products of 32.
+template <int N>
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem) {
+    const uint64_t ad = smem_desc(a_smem), bd = smem_desc(b_smem);
+#pragma unroll
+    for (int k = 0; k < kBlockK / 32; ++k) mma_e4m3(d_tmem, ad + 2 * k, bd + 2 * k, idesc_e4m3(N), k > 0);
+}
+
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *m, int k, int row, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(k), "r"(row), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 32 columns of this thread's lane: asked for, and (later) there.
+__device__ __forceinline__ void ask32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void ask16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// All loads asked for so far are there; their registers pass through, so that no use of them moves up.
+__device__ __forceinline__ void there() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// The slow part of a wait: until the phase is over, another wait has given up, or this one does.
+__device__ __forceinline__ bool keep_waiting(uint32_t bar, uint32_t parity, volatile int *stop, int *status, uint32_t polls) {
+    for (uint32_t it = 0; it < polls; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*stop) return false;
+    }
+    *stop = 1;
+    if (status != nullptr) atomicExch(status, (int)CGDR_ERR_TIMEOUT);
+    return false;
+}
+
+}  // namespace fp8
+}  // namespace cgdr
