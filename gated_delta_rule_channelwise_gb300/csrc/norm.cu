@@ -1,12 +1,18 @@
 // Root-mean-square norm with the residual's addition (cgdr_norm), and the 8-bit quantisers (cgdr_quantize).
+//
+// All of it is bound by memory.  4,001 rows of 4,096 bf16 with residual, in 8 bits (115 MB): 21.0 us, 17.0 at the copy rate.
+// 128,000 heads of 128 bf16 out of packed rows (66 MB): 13.4 us, 9.7.  64 rows of 4,096: 2.3 us, a launch.  4,001 rows of 4,096 bf16
+// into 8 bits (50 MB): 10.0 us, 7.3; a weight of 12288 x 4096 (151 MB): 25.0 us, 22.2.  Consecutive launches are 1.5 to 2 us apart, which
+// these times include.
 #include "layer.cuh"
 
 namespace cgdr {
 namespace {
 
 struct NormParams {
-    int64_t rows;                                     // n * H
+    uint32_t rows;                                    // n * H
     int H, C, shift;                                  // 2^shift threads to a row
+    uint64_t by_head;                                 // 2^64 / H, rounded up: row / H is the high word of the product
     float eps;
     const void *x;  int64_t x_st, x_sh;
     void *r;        int64_t r_st, r_sh;
@@ -14,107 +20,161 @@ struct NormParams {
     void *o;        int64_t o_st, o_sh;
     uint8_t *y8;    int64_t y8_st;
     float *scale;
-    int64_t ex, er, eo, ey;                               // footprints (index-checking build)
+    int64_t ex, er, eo, ey;                           // footprints (index-checking build)
     int *status;
 };
 
-// A row is held by 2^shift threads, kVecs vectors of eight values a thread: one pass over the data.  The 16 lanes
-// of a half warp hold 128 consecutive values, so a group's largest magnitude takes four shuffles.
-template <typename T, int kVecs, bool kResidual, bool k8>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
-    __shared__ float s_sum[32];
+// sum_i h_i^2 of a row, then h_i / sqrt(sum / C + eps) w_i.  A row is held by 2^shift threads, kVecs vectors of eight values a thread: one pass over the data.  The 16 lanes
+// of a half warp hold 128 consecutive values, so a group's largest magnitude takes four shuffles.  A block stays and takes row after
+// row, kRows at a time, with the weights in registers and the next rows on their way while it works on these (but for the longest
+// rows, whose 1024 threads have no registers left for that): with a block for each row the first case takes 24.9 us, and 22.5 the
+// second, which was bound by instructions, too, before values went in pairs.
+constexpr int blocks_of(int vecs, int threads) { return threads > 256 ? 1 : vecs > 2 ? 2 : 4; }   // resident on an SM
+
+template <typename T, int kVecs, int kRows, int kThreads, bool kResidual, bool k8>
+__global__ void __launch_bounds__(kThreads, blocks_of(kVecs, kThreads)) norm_kernel(const NormParams p) {
+    constexpr bool kKeep = kThreads < 1024;
+    __shared__ float s_sum[2][kRows][32];
     const int tid = threadIdx.x, per = 1 << p.shift, t = tid & (per - 1);
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> p.shift) + (tid >> p.shift);
-    const bool live = row < p.rows;
-    const int64_t i = p.H == 1 ? row : row / p.H, h = p.H == 1 ? 0 : row % p.H;
-    const int64_t x0 = i * p.x_st + h * p.x_sh, r0 = i * p.r_st + h * p.r_sh;
-    const int nv = p.C / 8;
-
-    Eight<T> xv[kVecs], rv[kVecs];
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
+    const uint32_t heads = p.H, side = blockDim.x >> p.shift, stride = gridDim.x * kRows * side;
+    const float share = 1.f / (float)p.C;
+    f32x2 w[kVecs][4];
+    auto weights = [&](int j) {
         const int c = (t + (j << p.shift)) * 8;
-        xv[j].clear();
-        rv[j].clear();
-        if (live && c < p.C) {
-            if (range_in_bounds(x0 + c, 8, p.ex, p.status, nullptr)) xv[j].load(static_cast<const T *>(p.x) + x0 + c);
-            if (kResidual && range_in_bounds(r0 + c, 8, p.er, p.status, nullptr)) rv[j].fetch(static_cast<T *>(p.r) + r0 + c);
-        }
-    }
-    float f[kVecs][8], sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        const int c = (t + (j << p.shift)) * 8;
-        xv[j].unpack(f[j]);
-        if (kResidual) {
-            float g[8];
-            rv[j].unpack(g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[j][e] += g[e];
-            if (live && c < p.C && range_in_bounds(r0 + c, 8, p.er, p.status, nullptr)) Eight<T>::store(static_cast<T *>(p.r) + r0 + c, f[j]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(f[j][e], f[j][e], sum);
-    }
-    for (int o = min(per, 32) >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (per > 32) {                                   // always in the same order
-        if ((tid & 31) == 0) s_sum[tid >> 5] = sum;
-        __syncthreads();
-        sum = 0.f;
-        for (int w = 0; w < per / 32; ++w) sum += s_sum[((tid >> p.shift) << (p.shift - 5)) + w];
-    }
-    const float by = __frsqrt_rn(sum / (float)p.C + p.eps);
-
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        const int v = t + (j << p.shift), c = v * 8;
-        const bool in = live && v < nv;
-        float w[8];
-        if (p.weight != nullptr && in) {
+        for (int e = 0; e < 4; ++e) w[j][e] = both(1.f);
+        if (p.weight != nullptr && c < p.C) {
             Eight<float> raw;
             raw.load(p.weight + c);
-            raw.unpack(w);
+            raw.unpack(w[j]);
+        }
+    };
+    wait_for_inputs();
+    if (kKeep)
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) weights(j);
+    Eight<T> xv[kRows][kVecs], rv[kRows][kVecs];
+    auto offset = [&](uint32_t row, int64_t st, int64_t sh) {
+        const uint32_t i = heads == 1 ? row : (uint32_t)__umul64hi(row, p.by_head);
+        return (int64_t)i * st + (int64_t)(row - i * heads) * sh;
+    };
+    auto ask = [&](uint32_t first) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const uint32_t row = first + k * side;
+            const int64_t x0 = offset(row, p.x_st, p.x_sh), r0 = kResidual ? offset(row, p.r_st, p.r_sh) : 0;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int c = (t + (j << p.shift)) * 8;
+                xv[k][j].clear();
+                rv[k][j].clear();
+                if (row < p.rows && c < p.C) {
+                    if (range_in_bounds(x0 + c, 8, p.ex, p.status, nullptr)) xv[k][j].load(static_cast<const T *>(p.x) + x0 + c);
+                    if (kResidual && range_in_bounds(r0 + c, 8, p.er, p.status, nullptr)) rv[k][j].fetch(static_cast<T *>(p.r) + r0 + c);
+                }
+            }
+        }
+    };
+    uint32_t first = blockIdx.x * kRows * side + (tid >> p.shift), last = blockIdx.x * kRows * side;
+    if (kKeep) ask(first);
+    for (int round = 0; last < p.rows; first += stride, last += stride, round ^= 1) {
+        if (!kKeep) ask(first);
+        f32x2 f[kRows][kVecs][4];
+        float sum[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const uint32_t row = first + k * side;
+            const int64_t r0 = kResidual ? offset(row, p.r_st, p.r_sh) : 0;
+            f32x2 sums = both(0.f);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int c = (t + (j << p.shift)) * 8;
+                xv[k][j].unpack(f[k][j]);
+                if (kResidual) {
+                    f32x2 g[4];
+                    rv[k][j].unpack(g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[k][j][e] = add2(f[k][j][e], g[e]);
+                    if (row < p.rows && c < p.C && range_in_bounds(r0 + c, 8, p.er, p.status, nullptr)) Eight<T>::store(static_cast<T *>(p.r) + r0 + c, f[k][j]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sums = fma2(f[k][j][e], f[k][j][e], sums);
+            }
+            const float2 v = split(sums);
+            sum[k] = v.x + v.y;
+        }
+        if (kKeep) ask(first + stride);
+        for (int o = min(per, 32) >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+        if (per > 32) {                               // always in the same order
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+                if ((tid & 31) == 0) s_sum[round][k][tid >> 5] = sum[k];
+            __syncthreads();                          // (the other buffer is written before the next one of these)
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                sum[k] = 0.f;
+                for (int i = 0; i < per / 32; ++i) sum[k] += s_sum[round][k][((tid >> p.shift) << (p.shift - 5)) + i];
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[j][e] = in ? f[j][e] * by * (p.weight != nullptr ? w[e] : 1.f) : 0.f;
-        if (k8) {
-            const float scale = scale_of(top_of_group(top_of(f[j])));
-            if (in && range_in_bounds(row * p.y8_st + c, 8, p.ey, p.status, nullptr)) {
-                *reinterpret_cast<uint2 *>(p.y8 + row * p.y8_st + c) = e4m3x8(f[j], __frcp_rn(scale));
-                if (v % 16 == 0) p.scale[row * ((p.C + kGroup - 1) / kGroup) + c / kGroup] = scale;
+        for (int k = 0; k < kRows; ++k) {
+            const uint32_t row = first + k * side;
+            const f32x2 by = both(__frsqrt_rn(sum[k] * share + p.eps));
+            const int64_t o0 = k8 ? row * p.y8_st : offset(row, p.o_st, p.o_sh);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int v = t + (j << p.shift), c = v * 8;
+                const bool in = row < p.rows && c < p.C;
+                f32x2 y[4];
+                if (!kKeep) weights(j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(f[k][j][e], by), w[j][e]);
+                if (k8) {
+                    const float scale = scale_of(top_of_group(in ? top_of(y) : 0.f));
+                    if (in && range_in_bounds(o0 + c, 8, p.ey, p.status, nullptr)) {
+                        *reinterpret_cast<uint2 *>(p.y8 + o0 + c) = e4m3x8(y, __frcp_rn(scale));
+                        if (v % 16 == 0) p.scale[(int64_t)row * ((p.C + kGroup - 1) / kGroup) + c / kGroup] = scale;
+                    }
+                } else if (in && range_in_bounds(o0 + c, 8, p.eo, p.status, nullptr)) {
+                    Eight<T>::store(static_cast<T *>(p.o) + o0 + c, y);
+                }
             }
-        } else {
-            const int64_t at = i * p.o_st + h * p.o_sh + c;
-            if (in && range_in_bounds(at, 8, p.eo, p.status, nullptr)) Eight<T>::store(static_cast<T *>(p.o) + at, f[j]);
         }
     }
 }
 
-template <typename T, int kVecs>
+template <typename T, int kVecs, int kRows, int kThreads, bool kResidual, bool k8>
+cgdr_status launch_rows(const NormParams &p, cudaStream_t s) {
+    const int per = 1 << p.shift, threads = per < 256 ? 256 : per, sms = device_sms();
+    if (sms <= 0) return CGDR_ERR_CUDA;
+    const uint32_t rows = kRows * (threads >> p.shift), need = (p.rows + rows - 1) / rows, most = sms * blocks_of(kVecs, kThreads);
+    return launch_early(norm_kernel<T, kVecs, kRows, kThreads, kResidual, k8>, need < most ? need : most, threads, 0, s, 0, p);
+}
+
+template <typename T, int kVecs, int kRows, int kThreads>
 cgdr_status launch_norm(const NormParams &p, cudaStream_t s) {
-    const int per = 1 << p.shift, threads = per < 256 ? 256 : per, rows = threads / per;
-    const int64_t blocks = (p.rows + rows - 1) / rows;
-    if (blocks > INT32_MAX) return CGDR_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks);
     if (p.r != nullptr)
-        p.y8 != nullptr ? norm_kernel<T, kVecs, true, true><<<grid, threads, 0, s>>>(p) : norm_kernel<T, kVecs, true, false><<<grid, threads, 0, s>>>(p);
-    else
-        p.y8 != nullptr ? norm_kernel<T, kVecs, false, true><<<grid, threads, 0, s>>>(p) : norm_kernel<T, kVecs, false, false><<<grid, threads, 0, s>>>(p);
-    return launched();
+        return p.y8 != nullptr ? launch_rows<T, kVecs, kRows, kThreads, true, true>(p, s) : launch_rows<T, kVecs, kRows, kThreads, true, false>(p, s);
+    return p.y8 != nullptr ? launch_rows<T, kVecs, kRows, kThreads, false, true>(p, s) : launch_rows<T, kVecs, kRows, kThreads, false, false>(p, s);
 }
 
 template <typename T>
 cgdr_status launch_vecs(NormParams &p, cudaStream_t s) {
-    const int nv = p.C / 8;
-    int vecs = 1;
     auto shift_for = [&](int v) {
         int sh = 4;
-        while ((v << sh) < nv) ++sh;
+        while ((v * 8 << sh) < p.C) ++sh;
         return sh;
     };
-    while (vecs < 4 && shift_for(vecs) > 7) vecs *= 2;
-    p.shift = shift_for(vecs);
-    return vecs == 1 ? launch_norm<T, 1>(p, s) : vecs == 2 ? launch_norm<T, 2>(p, s) : launch_norm<T, 4>(p, s);
+    // Vectors of a thread.  4,096 columns: 21 us with two, 27 with one (512 threads a row).  128: 13.4 with two rows at a time, 14.7 with one.
+    p.shift = shift_for(p.C <= 2048 ? 1 : p.C <= 4096 ? 2 : 4);
+    return p.C <= 512     ? launch_norm<T, 1, 2, 256>(p, s)
+           : p.C <= 2048  ? launch_norm<T, 1, 1, 256>(p, s)
+           : p.C <= 4096  ? launch_norm<T, 2, 1, 256>(p, s)
+           : p.C <= 8192  ? launch_norm<T, 4, 1, 256>(p, s)
+           : p.C <= 16384 ? launch_norm<T, 4, 1, 512>(p, s)
+                          : launch_norm<T, 4, 1, 1024>(p, s);
 }
 
 cgdr_status check(const cgdr_norm_args *a) {
@@ -148,15 +208,16 @@ struct QuantizeParams {
 };
 
 constexpr int kQThreads = 256;
-constexpr int kQGroups = 4;                           // groups of a half warp
+constexpr int kQGroups = 2;                           // groups of a half warp
 
-// Rows: a half warp takes a group of 128 values, several at a time.
+// Rows: a half warp takes two groups of 128 values at a time (10.0 us in the first case above; one 11.8, four 11.3).
 template <typename T>
-__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const QuantizeParams p) {
+__global__ void __launch_bounds__(kQThreads, 8) quantize_rows_kernel(const QuantizeParams p) {
     const int lane = threadIdx.x & 15, c = lane * 8;
     const int64_t units = (int64_t)p.n * p.groups, u0 = ((int64_t)blockIdx.x * kQGroups) * (kQThreads / 16) + threadIdx.x / 16;
     Eight<T> v[kQGroups];
     int64_t at[kQGroups];
+    wait_for_inputs();
 #pragma unroll
     for (int j = 0; j < kQGroups; ++j) {
         const int64_t u = u0 + j * (kQThreads / 16);
@@ -173,7 +234,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const Quantize
     }
 #pragma unroll
     for (int j = 0; j < kQGroups; ++j) {
-        float f[8];
+        f32x2 f[4];
         v[j].unpack(f);
         const float scale = scale_of(top_of_group(top_of(f)));
         if (at[j] >= 0 && range_in_bounds(at[j], 8, p.ey, p.status, nullptr)) {
@@ -187,10 +248,11 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const Quantize
 template <typename T>
 __global__ void __launch_bounds__(kQThreads) quantize_blocks_kernel(const QuantizeParams p) {
     constexpr int kRows = kGroup / (kQThreads / 16);
-    __shared__ uint32_t s_top[kQThreads / 32];
+    __shared__ float s_top[kQThreads / 32];
     const int tid = threadIdx.x, lane = tid & 15, part = tid / 16;
     const int block = blockIdx.x / p.groups, group = blockIdx.x % p.groups, c = group * kGroup + lane * 8;
     Eight<T> v[kRows];
+    wait_for_inputs();
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
         const int row = block * kGroup + part + j * (kQThreads / 16);
@@ -198,24 +260,25 @@ __global__ void __launch_bounds__(kQThreads) quantize_blocks_kernel(const Quanti
         v[j].clear();
         if (row < p.n && c < p.C && range_in_bounds(from, 8, p.ex, p.status, nullptr)) v[j].load(static_cast<const T *>(p.x) + from);
     }
-    uint32_t top = 0;
+    float top = 0.f;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-        float f[8];
+        f32x2 f[4];
         v[j].unpack(f);
-        top = max(top, top_of(f));
+        top = top_of(f, top);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
+    // of what is not below 0 the bits order as integers do, a NaN's above all
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     if ((tid & 31) == 0) s_top[tid >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kQThreads / 32; ++w) top = max(top, s_top[w]);
+    for (int w = 0; w < kQThreads / 32; w += 2) top = max3_nan(top, s_top[w], s_top[w + 1]);
     const float scale = scale_of(top), inverse = __frcp_rn(scale);
     if (tid == 0) p.scale[blockIdx.x] = scale;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
         const int row = block * kGroup + part + j * (kQThreads / 16);
-        float f[8];
+        f32x2 f[4];
         v[j].unpack(f);
         if (row < p.n && c < p.C && range_in_bounds(row * p.y8_st + c, 8, p.ey, p.status, nullptr))
             *reinterpret_cast<uint2 *>(p.y8 + row * p.y8_st + c) = e4m3x8(f, inverse);
@@ -239,11 +302,9 @@ template <typename T>
 cgdr_status launch_quantize(const QuantizeParams &p, int block_rows, cudaStream_t s) {
     if (block_rows == 1) {
         const int64_t units = (int64_t)p.n * p.groups, per = (kQThreads / 16) * kQGroups;
-        quantize_rows_kernel<T><<<(unsigned)((units + per - 1) / per), kQThreads, 0, s>>>(p);
-    } else {
-        quantize_blocks_kernel<T><<<(unsigned)(groups_of(p.n) * (int64_t)p.groups), kQThreads, 0, s>>>(p);
+        return launch_early(quantize_rows_kernel<T>, (unsigned)((units + per - 1) / per), kQThreads, 0, s, 0, p);
     }
-    return launched();
+    return launch_early(quantize_blocks_kernel<T>, (unsigned)(groups_of(p.n) * (int64_t)p.groups), kQThreads, 0, s, 0, p);
 }
 
 }  // namespace
@@ -253,21 +314,29 @@ extern "C" cgdr_status cgdr_norm(const cgdr_norm_args *a, void *stream) {
     using namespace cgdr;
     const cgdr_status st = check(a);
     if (st != CGDR_OK || a->n == 0) return st;
-    NormParams p{};
-    p.rows = (int64_t)a->n * a->H; p.H = a->H; p.C = a->C;
-    p.eps = a->eps < 0.f ? 1e-6f : a->eps;
-    p.x = a->x; p.x_st = a->x_st; p.x_sh = a->x_sh;
-    p.r = a->residual; p.r_st = a->r_st; p.r_sh = a->r_sh;
-    p.weight = a->weight;
-    p.o = a->o; p.o_st = a->o_st; p.o_sh = a->o_sh;
-    p.y8 = static_cast<uint8_t *>(a->y8); p.y8_st = a->y8_st; p.scale = a->y_scale;
-    p.ey = extent3(1, 0, a->n, a->y8_st, a->C);
-    p.ex = extent3(a->n, a->x_st, a->H, a->x_sh, a->C);
-    p.er = extent3(a->n, a->r_st, a->H, a->r_sh, a->C);
-    p.eo = extent3(a->n, a->o_st, a->H, a->o_sh, a->C);
-    p.status = a->status;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return a->dtype == CGDR_BF16 ? launch_vecs<__nv_bfloat16>(p, s) : launch_vecs<float>(p, s);
+    const int most = INT32_MAX / a->H;                // tokens of a launch: rows are numbered in 32 bits
+    const int esz = esize(a->dtype);
+    auto from = [&](const void *base, int64_t at) { return const_cast<char *>(static_cast<const char *>(base)) + at; };
+    for (int64_t t = 0; t < a->n; t += most) {
+        const int n = a->n - t < most ? (int)(a->n - t) : most;
+        NormParams p{};
+        p.rows = (uint32_t)n * a->H; p.H = a->H; p.C = a->C;
+        p.by_head = ~0ull / a->H + 1;
+        p.eps = a->eps < 0.f ? 1e-6f : a->eps;
+        p.x = from(a->x, t * a->x_st * esz); p.x_st = a->x_st; p.x_sh = a->x_sh; p.ex = extent3(n, a->x_st, a->H, a->x_sh, a->C);
+        if (a->residual) p.r = from(a->residual, t * a->r_st * esz);
+        p.r_st = a->r_st; p.r_sh = a->r_sh; p.er = extent3(n, a->r_st, a->H, a->r_sh, a->C);
+        p.weight = a->weight;
+        if (a->o) p.o = from(a->o, t * a->o_st * esz);
+        p.o_st = a->o_st; p.o_sh = a->o_sh; p.eo = extent3(n, a->o_st, a->H, a->o_sh, a->C);
+        if (a->y8) { p.y8 = static_cast<uint8_t *>(a->y8) + t * a->y8_st; p.scale = a->y_scale + t * groups_of(a->C); }
+        p.y8_st = a->y8_st; p.ey = extent3(1, 0, n, a->y8_st, a->C);
+        p.status = a->status;
+        const cgdr_status done = a->dtype == CGDR_BF16 ? launch_vecs<__nv_bfloat16>(p, s) : launch_vecs<float>(p, s);
+        if (done != CGDR_OK) return done;
+    }
+    return CGDR_OK;
 }
 
 extern "C" cgdr_status cgdr_quantize(const cgdr_quantize_args *a, void *stream) {
