@@ -2,7 +2,8 @@
 
     python examples/hybrid_decoder.py
 
-Random weights, torch for the projections, and the library for everything that carries state: the
+Random weights, torch for the projections of the recurrent layers, and the library for the norms, for the attention layers'
+rotary positions and (with ``eight_bit``) 8-bit projections, and for everything that carries state: the
 short causal convolution in front of the recurrent layers, the channelwise gated delta rule, the
 selective scan, and a paged 8-bit cache whose block tables are built on the GPU.  Requests of
 different lengths are packed into one step; a step of prompts and a step of single tokens take the
@@ -27,11 +28,12 @@ class HybridDecoder:
     """``layers`` of "delta", "scan" and "attend" over a width of heads x 128; serves ``B`` requests."""
 
     def __init__(self, layers=("delta", "scan", "attend", "delta"), heads=4, kv_heads=2, vocab=512, states=16, taps=4,
-                 B=3, pages=64, page=64, table_width=16, seed=0, device="cuda"):
+                 B=3, pages=64, page=64, table_width=16, seed=0, device="cuda", eight_bit=False):
         g = torch.Generator(device=device)
         g.manual_seed(seed)
         self.kinds, self.H, self.Hkv, self.d = layers, heads, kv_heads, 128
-        self.C, self.N, self.W, self.B, self.page = heads * 128, states, taps, B, page
+        self.C, self.N, self.W, self.B, self.page, self.eight_bit = heads * 128, states, taps, B, page, eight_bit
+        self.freq, self.turn_scale = cg.rotary_frequencies(128, device=device)
         C = self.C
 
         def weight(n_in, n_out):
@@ -52,6 +54,8 @@ class HybridDecoder:
                          D=torch.ones(C, device=device), dt_bias=rand(C) * 4 - 6)
             else:
                 p.update(qkv=weight(C, C + 2 * kv_heads * 128))
+                if eight_bit:                         # rows of w are outputs
+                    p.update(qkv=cg.fp8_quantize_weight(p["qkv"].t().contiguous()), out=cg.fp8_quantize_weight(p["out"].t().contiguous()))
             self.layers.append(p)
         # what the requests keep: conv rows and recurrent states, caches, one block table for all attention layers
         zeros = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype, device=device)
@@ -70,11 +74,6 @@ class HybridDecoder:
         self.free_pages, self.free_count = torch.arange(pages, **i32), torch.full((1,), pages, **i32)
         self.status = torch.zeros(1, **i32)
 
-    @staticmethod
-    def norm(x):
-        f = x.float()
-        return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-6)).to(BF)
-
     def step(self, tokens, lens):
         """``tokens``: the new ids of all requests, packed; ``lens``: how many of each (known on the host, as
         the ids are).  Returns the logits of every new token."""
@@ -84,10 +83,13 @@ class HybridDecoder:
         plan = cg.cache_plan(self.table, self.lens, new, self.free_pages, self.free_count, n, self.page,
                              num_pages=self.free_pages.numel(), status=self.status)
         self.lens, self.free_count = plan.kv_lens, plan.free_count
-        x = self.embedding[tokens]
+        x, y = self.embedding[tokens], None           # the residual stream, and what the last layer adds to it
         for p, s in zip(self.layers, self.state):
-            x = x + getattr(self, "_" + p["kind"])(p, s, self.norm(x), plan, lens, longest, single) @ p["out"]
-        return self.norm(x) @ self.head
+            norm = cg.rms_norm_fp8 if self.eight_bit and p["kind"] == "attend" else cg.rms_norm
+            h = norm(x, None) if y is None else norm(y, None, residual=x)
+            y = getattr(self, "_" + p["kind"])(p, s, h, plan, lens, longest, single)
+            y = cg.fp8_matmul(*cg.fp8_quantize(y), *p["out"]) if self.eight_bit and p["kind"] == "attend" else y @ p["out"]
+        return cg.rms_norm(y, None, residual=x) @ self.head
 
     def _conv(self, x, taps, state, plan, single):
         return cg.conv_decode(x, taps, state) if single else cg.conv_prefill(x, taps, state, cu_seqlens=plan.cu_seqlens)
@@ -120,21 +122,22 @@ class HybridDecoder:
         return cg.scan_prefill(u, x @ p["dt"], p["A_log"], Bm, Cm, s["h"], cu_seqlens=plan.cu_seqlens, **kw)
 
     def _attend(self, p, s, x, plan, lens, longest, single):
-        q, k, v = (x @ p["qkv"]).split([self.C, self.Hkv * self.d, self.Hkv * self.d], -1)
-        q, k, v = (t.unflatten(-1, (-1, self.d)) for t in (q, k, v))
+        row = cg.fp8_matmul(*x, *p["qkv"]) if self.eight_bit else x @ p["qkv"]
+        q, k, v = (t.unflatten(-1, (-1, self.d)) for t in row.split([self.C, self.Hkv * self.d, self.Hkv * self.d], -1))
+        cg.rotary(q, k, plan.positions, self.freq, scale=self.turn_scale)
         cg.cache_append(k, v, plan.slots, s["k"], s["v"], s["ks"], s["vs"], status=self.status)
         return cg.cache_attend(q, s["k"], s["v"], s["ks"], s["vs"], self.table, self.lens, plan.cu_seqlens, max_q=longest,
                                status=self.status).flatten(1)
 
 
-def compare(lens=(70, 1, 133), tail=5, seed=0):
+def compare(lens=(70, 1, 133), tail=5, seed=0, eight_bit=False):
     """Largest logit difference, over the logits' RMS, between whole sequences in one step and prompts
     followed by ``tail`` steps of single tokens."""
     B = len(lens)
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
     ids = [torch.randint(0, 512, (l + tail,), generator=g, device="cuda") for l in lens]
-    whole, parts = HybridDecoder(B=B), HybridDecoder(B=B)
+    whole, parts = HybridDecoder(B=B, eight_bit=eight_bit), HybridDecoder(B=B, eight_bit=eight_bit)
     full = whole.step(torch.cat(ids), [l + tail for l in lens]).split([l + tail for l in lens])
     got = [parts.step(torch.cat([t[:l] for t, l in zip(ids, lens)]), list(lens)).split(list(lens))]
     for k in range(tail):

@@ -9,7 +9,7 @@
 // 128 x 256 x 128 takes 910 cycles: the products 512 (measured alone), the sums 64 pairs of multiply-adds for each of 8 warps. Measured,
 // and no better: two threads that issue, two that copy (169, 174), tiles of 160 columns with three sums (177), sums by 512 threads' block
 // with scales through shared memory (173), a pair of CTAs on one product (185), stores by copies (177).  Without the sums' work
-// it takes 147, without the stores, too, 125.
+// it takes 147.
 #include "fp8.cuh"
 
 namespace cgdr {
@@ -220,7 +220,8 @@ cgdr_status check(const cgdr_matmul_args *a) {
     if ((int64_t)groups_of(a->n) * groups_of(a->N) > INT32_MAX / 2) return CGDR_ERR_UNSUPPORTED;
     if (a->n == 0 || a->N == 0) return CGDR_OK;
     if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->o) return CGDR_ERR_INVALID_ARG;
-    if (a->n > 1 && a->o_st < a->N) return CGDR_ERR_INVALID_ARG;
+    if (a->n > 1 && (a->o_st < a->N || a->x_st < a->K)) return CGDR_ERR_INVALID_ARG;
+    if (a->N > 1 && a->w_st < a->K) return CGDR_ERR_INVALID_ARG;
     if (!aligned_to(a->x, 16) || !aligned_to(a->w, 16) || !aligned_to(a->o, 16) || !aligned_to(a->x_scale, 4) || !aligned_to(a->w_scale, 4) ||
         !aligned_to(a->status, 4))
         return CGDR_ERR_ALIGNMENT;

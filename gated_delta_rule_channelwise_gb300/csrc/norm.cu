@@ -186,14 +186,14 @@ cgdr_status check(const cgdr_norm_args *a) {
     if (a->n == 0) return CGDR_OK;
     if (!a->x || (a->y8 && !a->y_scale)) return CGDR_ERR_INVALID_ARG;
     if (a->y8 && !disjoint(a->n, a->y8_st, 1, 0, a->C)) return CGDR_ERR_INVALID_ARG;
-    if ((a->residual && !disjoint(a->n, a->r_st, a->H, a->r_sh, a->C)) || (a->o && !disjoint(a->n, a->o_st, a->H, a->o_sh, a->C)))
+    if ((a->residual && !disjoint(a->n, a->residual_st, a->H, a->residual_sh, a->C)) || (a->o && !disjoint(a->n, a->o_st, a->H, a->o_sh, a->C)))
         return CGDR_ERR_INVALID_ARG;
     const int esz = esize(a->dtype);
     if (!aligned_to(a->x, 16) || !aligned_to(a->residual, 16) || !aligned_to(a->weight, 16) || !aligned_to(a->o, 16) ||
         !aligned_to(a->y8, 16) || !aligned_to(a->y_scale, 4) || !aligned_to(a->status, 4))
         return CGDR_ERR_ALIGNMENT;
     if (!row_stride_ok(a->x_st, esz) || !row_stride_ok(a->x_sh, esz)) return CGDR_ERR_ALIGNMENT;
-    if (a->residual && (!row_stride_ok(a->r_st, esz) || !row_stride_ok(a->r_sh, esz))) return CGDR_ERR_ALIGNMENT;
+    if (a->residual && (!row_stride_ok(a->residual_st, esz) || !row_stride_ok(a->residual_sh, esz))) return CGDR_ERR_ALIGNMENT;
     if (a->o && (!row_stride_ok(a->o_st, esz) || !row_stride_ok(a->o_sh, esz))) return CGDR_ERR_ALIGNMENT;
     if (a->y8 && !row_stride_ok(a->y8_st, 1)) return CGDR_ERR_ALIGNMENT;
     return CGDR_OK;
@@ -325,8 +325,8 @@ extern "C" cgdr_status cgdr_norm(const cgdr_norm_args *a, void *stream) {
         p.by_head = ~0ull / a->H + 1;
         p.eps = a->eps < 0.f ? 1e-6f : a->eps;
         p.x = from(a->x, t * a->x_st * esz); p.x_st = a->x_st; p.x_sh = a->x_sh; p.ex = extent3(n, a->x_st, a->H, a->x_sh, a->C);
-        if (a->residual) p.r = from(a->residual, t * a->r_st * esz);
-        p.r_st = a->r_st; p.r_sh = a->r_sh; p.er = extent3(n, a->r_st, a->H, a->r_sh, a->C);
+        if (a->residual) p.r = from(a->residual, t * a->residual_st * esz);
+        p.r_st = a->residual_st; p.r_sh = a->residual_sh; p.er = extent3(n, a->residual_st, a->H, a->residual_sh, a->C);
         p.weight = a->weight;
         if (a->o) p.o = from(a->o, t * a->o_st * esz);
         p.o_st = a->o_st; p.o_sh = a->o_sh; p.eo = extent3(n, a->o_st, a->H, a->o_sh, a->C);

@@ -22,7 +22,7 @@ import math
 import torch
 
 from . import MATMUL_AUTO, CgdrError, _need_cuda, lib
-from . import serve as _serve
+from . import serve as _serve  # noqa: F401 (its notion of the current device: _serve._here)
 from .serve import _CODES, _F32, _I32, Block, _address, _current, _fits, _i, _on, _on_device, _p, _refuse, _status_word, _strided
 
 _E4M3, _F64 = torch.float8_e4m3fn, torch.float64
@@ -34,10 +34,6 @@ MATMUL = Block(*_i("n N K o_dtype path wait_polls"), *_strided("x", "st"), *_p("
                *_strided("o", "st"), *_p("status"))
 ROTARY = Block(*_i("n Hq Hk D half dtype interleaved"), ("scale", "f"), *_strided("q", "st", "sh"), *_strided("k", "st", "sh"),
                *_p("positions freq status"))
-
-
-def _here():
-    return _serve._here()
 
 
 def _groups(n):
@@ -60,7 +56,7 @@ _NONE = (0, 0, 0)
 
 def _norm(x, weight, residual, eps, o, y, y_scale, status):
     device = x.get_device()
-    if not (device >= 0 and device == _here() and _on_device(weight, device) and _on_device(residual, device) and _on_device(o, device)
+    if not (device >= 0 and device == _serve._here() and _on_device(weight, device) and _on_device(residual, device) and _on_device(o, device)
             and _on_device(y, device) and _on_device(y_scale, device)):
         _need_cuda(x, weight, residual, o, y, y_scale)
     dtype, shape = x.dtype, x.shape
@@ -94,7 +90,7 @@ def rms_norm(x, weight, o=None, *, residual=None, eps=1e-6, status=None, stream=
         raise ValueError("x must be [n, C] or [n, H, C]")
     _check_eps(eps)
     if o is None:
-        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        o = torch.empty(x.shape, dtype=x.dtype, device=x.device)    # dense, whatever x's strides are
     _norm(x, weight, residual, eps, o, None, None, status)
     return o
 
@@ -102,8 +98,9 @@ def rms_norm(x, weight, o=None, *, residual=None, eps=1e-6, status=None, stream=
 def _rows_of(shape, dtype, device, step):
     """New rows, each of a multiple of ``step`` values (16 bytes)."""
     n, C = shape
-    o = torch.empty((n, C + -C % step), dtype=dtype, device=device)
-    return o[:, :C] if C % step else o
+    if C % step == 0:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty((n, C + -C % step), dtype=dtype, device=device)[:, :C]
 
 
 def _eight(shape, y, y_scale, device, rows=1):
@@ -140,7 +137,7 @@ def _quantize(x, rows, y, y_scale, status):
         raise ValueError("%s must be a matrix" % ("x" if rows == 1 else "w"))
     y, y_scale = _eight(x.shape, y, y_scale, x.device, rows)
     device = x.get_device()
-    if not (device >= 0 and device == y.get_device() == y_scale.get_device() == _here()):
+    if not (device >= 0 and device == y.get_device() == y_scale.get_device() == _serve._here()):
         _need_cuda(x, y, y_scale)
     address, st, _ = _tokens(x, "x" if rows == 1 else "w")
     block = QUANTIZE.pack(x.shape[0], x.shape[1], _CODES.get(x.dtype, -1), rows, address, st, *_tokens(y, "y")[:2], y_scale.data_ptr(),
@@ -177,7 +174,7 @@ def fp8_matmul(x, x_scale, w, w_scale, o=None, *, dtype=torch.bfloat16, path=MAT
     if stream is not None:
         return _on(stream, fp8_matmul, x, x_scale, w, w_scale, o, dtype=dtype, path=path, status=status, wait_polls=wait_polls)
     device = x.get_device()
-    if not (device >= 0 and device == x_scale.get_device() == w.get_device() == w_scale.get_device() == _here() and _on_device(o, device)):
+    if not (device >= 0 and device == x_scale.get_device() == w.get_device() == w_scale.get_device() == _serve._here() and _on_device(o, device)):
         _need_cuda(x, x_scale, w, w_scale, o)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [n, K] and w [N, K]")
@@ -212,7 +209,7 @@ def rotary(q, k, positions, freq, *, interleaved=False, scale=1.0, status=None, 
     if stream is not None:
         return _on(stream, rotary, q, k, positions, freq, interleaved=interleaved, scale=scale, status=status)
     device = q.get_device()
-    if not (device >= 0 and device == positions.get_device() == freq.get_device() == _here() and _on_device(k, device)):
+    if not (device >= 0 and device == positions.get_device() == freq.get_device() == _serve._here() and _on_device(k, device)):
         _need_cuda(q, k, positions, freq)
     if q.dim() != 3 or freq.dim() != 1 or (k is not None and k.dim() != 3):
         raise ValueError("q must be [n, Hq, D], k [n, Hk, D] and freq [R / 2]")

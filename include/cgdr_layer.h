@@ -41,7 +41,7 @@ typedef struct cgdr_norm_args {
     int32_t dtype;                  /* cgdr_dtype of x, residual and o */
     float eps;                      /* < 0 selects 1e-6 */
     const void *x;  int64_t x_st, x_sh;         /* [n,H,C] */
-    void *residual; int64_t r_st, r_sh;         /* [n,H,C] or NULL; in place */
+    void *residual; int64_t residual_st, residual_sh;         /* [n,H,C] or NULL; in place */
     const float *weight;                        /* [C], 16-byte aligned, or NULL for ones */
     void *o;        int64_t o_st, o_sh;         /* [n,H,C], or NULL with y8 */
     void *y8;       int64_t y8_st;              /* [n,C], or NULL with o */
@@ -71,14 +71,14 @@ cgdr_status cgdr_quantize(const cgdr_quantize_args *args, void *stream);
  * o = x w^T of 8-bit operands, x [n,K] with x_scale [n,KB], w [N,K] with w_scale [NB,KB]; KB and NB
  * are K and N over 128, rounded up:
  *     o[i,j] = sum_b x_scale[i,b] w_scale[j/128,b] sum_{k of block b} x[i,k] w[j,k]
- * Products are exact, sums are fp32.  A NaN or an infinity reaches the outputs of its row of x, or of its rows
+ * Products are exact, sums are fp32.  Rows of x and of w may not overlap (they are described to the copy engine).  A NaN or an infinity reaches the outputs of its row of x, or of its rows
  * of w, and no others.  `path` says which kernel runs (they agree up to the order of sums).  A wait that gives
  * up reports CGDR_ERR_TIMEOUT in *status; the outputs of its CTA (or cluster) are then undefined.
  */
 typedef enum cgdr_matmul_path {
     CGDR_MATMUL_AUTO = 0,           /* per call: whichever of the two measured less time */
     CGDR_MATMUL_FEW = 1,            /* few rows of x: 128 rows of w a CTA, K in parts over a cluster */
-    CGDR_MATMUL_TILES = 2           /* tiles of 128 rows of x */
+    CGDR_MATMUL_TILES = 2           /* tiles of 128 rows of x by 128 or 256 rows of w */
 } cgdr_matmul_path;
 
 typedef struct cgdr_matmul_args {
