@@ -95,12 +95,11 @@ def rms_norm(x, weight, o=None, *, residual=None, eps=1e-6, status=None, stream=
     return o
 
 
-def _rows_of(shape, dtype, device, step):
-    """New rows, each of a multiple of ``step`` values (16 bytes)."""
-    n, C = shape
-    if C % step == 0:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return torch.empty((n, C + -C % step), dtype=dtype, device=device)[:, :C]
+def _rows_of(n, C, dtype, device, step):
+    """New rows, each beginning at a multiple of ``step`` values (16 bytes): dense, or with the least stride that gives that (one
+    allocation either way; a view of padded rows would cost as much again)."""
+    return torch.empty((n, C), dtype=dtype, device=device) if C % step == 0 else \
+        torch.empty_strided((n, C), (C + -C % step, 1), dtype=dtype, device=device)
 
 
 def _eight(shape, y, y_scale, device, rows=1):
@@ -108,11 +107,13 @@ def _eight(shape, y, y_scale, device, rows=1):
     n, C = shape
     scales = (_groups(n) if rows > 1 else n, _groups(C))
     if y is None:
-        y = _rows_of(shape, _E4M3, device, 16)
+        y = _rows_of(n, C, _E4M3, device, 16)
+    elif y.dtype != _E4M3 or y.shape != shape:
+        _refuse([("y", y, _E4M3)], [("y", y, shape)], [])
     if y_scale is None:
         y_scale = torch.empty(scales, dtype=_F32, device=device)
-    if not (y.dtype == _E4M3 and y.shape == (n, C) and _fits(y_scale, _F32, scales)):
-        _refuse([("y", y, _E4M3), ("y_scale", y_scale, _F32)], [("y", y, (n, C)), ("y_scale", y_scale, scales)], [("y_scale", y_scale)])
+    elif not _fits(y_scale, _F32, scales):
+        _refuse([("y_scale", y_scale, _F32)], [("y_scale", y_scale, scales)], [("y_scale", y_scale)])
     return y, y_scale
 
 
@@ -168,7 +169,7 @@ def fp8_matmul(x, x_scale, w, w_scale, o=None, *, dtype=torch.bfloat16, path=MAT
     """``o = x w^T`` of 8-bit operands: ``x [n,K]`` with ``x_scale [n, ceil(K/128)]`` (as :func:`fp8_quantize` and
     :func:`rms_norm_fp8` leave them) and ``w [N,K]`` with ``w_scale [ceil(N/128), ceil(K/128)]``
     (:func:`fp8_quantize_weight`).  Any n, N and K; rows of x, w and o are 16-byte aligned (new outputs of all these calls
-    are views of padded rows where the sizes do not give that).  Products are exact, sums fp32.  Returns o ``[n,N]``, the given one (fp32 or bf16) or a new one of
+    have strides that give that).  Products are exact, sums fp32.  Returns o ``[n,N]``, the given one (fp32 or bf16) or a new one of
     ``dtype``.  ``path`` forces one of the two kernels for this call (``MATMUL_FEW``, ``MATMUL_TILES``).
     ``wait_polls``: polls of a bounded device wait (0: the default; ``ERR_TIMEOUT`` in ``status`` when one gives up)."""
     if stream is not None:
@@ -182,7 +183,7 @@ def fp8_matmul(x, x_scale, w, w_scale, o=None, *, dtype=torch.bfloat16, path=MAT
     N = w.shape[0]
     blocks = _groups(K)
     if o is None:
-        o = _rows_of((n, N), dtype, x.device, 8 if dtype == torch.bfloat16 else 4)
+        o = _rows_of(n, N, dtype, x.device, 8 if dtype == torch.bfloat16 else 4)
     if not (x.dtype == _E4M3 and w.dtype == _E4M3 and w.shape[1] == K and o.shape == (n, N) and _fits(x_scale, _F32, (n, blocks))
             and _fits(w_scale, _F32, (_groups(N), blocks))):
         _refuse([("x", x, _E4M3), ("w", w, _E4M3), ("x_scale", x_scale, _F32), ("w_scale", w_scale, _F32)],
