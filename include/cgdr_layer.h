@@ -71,7 +71,8 @@ cgdr_status cgdr_quantize(const cgdr_quantize_args *args, void *stream);
  * o = x w^T of 8-bit operands, x [n,K] with x_scale [n,KB], w [N,K] with w_scale [NB,KB]; KB and NB
  * are K and N over 128, rounded up:
  *     o[i,j] = sum_b x_scale[i,b] w_scale[j/128,b] sum_{k of block b} x[i,k] w[j,k]
- * Products are exact, sums are fp32.  Rows of x and of w may not overlap (they are described to the copy engine).  A NaN or an infinity reaches the outputs of its row of x, or of its rows
+ * Products are exact, sums are fp32; x_scale w_scale is formed first, in fp32, so scales whose product overflows give
+ * infinities or NaN.  Rows of x and of w may not overlap (they are described to the copy engine).  A NaN or an infinity reaches the outputs of its row of x, or of its rows
  * of w, and no others.  `path` says which kernel runs (they agree up to the order of sums).  A wait that gives
  * up reports CGDR_ERR_TIMEOUT in *status; the outputs of its CTA (or cluster) are then undefined.
  */
