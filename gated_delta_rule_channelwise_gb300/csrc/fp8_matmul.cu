@@ -4,12 +4,15 @@
 // The scales change with every block of K, so a block's product (four instructions of K = 32) is a sum of its own in
 // tensor memory, which 256 threads take from there, scale and add up in registers: a thread has a row of x and half of the
 // tile's columns, so that both scales are one number to it.  Two such sums fit tensor memory: one is formed while the other
-// is taken.  One warp copies operands ahead, one thread issues the products.
-// 4,001 x 12,288 x 4,096: 167 us, 2,415 TFLOP/s, 1.28 times what a large bf16 product reaches, 0.64 of twice that.  A block of
-// 128 x 256 x 128 takes 910 cycles: the products 512 (measured alone), the sums 64 pairs of multiply-adds for each of 8 warps. Measured,
-// and no better: two threads that issue, two that copy (169, 174), tiles of 160 columns with three sums (177), sums by 512 threads' block
-// with scales through shared memory (173), a pair of CTAs on one product (185), stores by copies (177).  Without the sums' work
-// it takes 147.
+// is taken.  One thread copies operands ahead.  Two issue the products, a block each in turn: the waits, four instructions and two
+// commits of a block take one thread 600 to 700 cycles, longer than the products of 128 columns run (256; 512 rows by 4,096 x 4,096
+// take 15.2 us with one such thread, 12.4 with two).
+// 4,001 x 12,288 x 4,096: 162 us, 2,480 TFLOP/s, 1.31 times what a large bf16 product reaches, 0.66 of twice that.  A block of
+// 128 x 256 x 128 takes 750 cycles there (the slope along K), the products alone 512, the sums alone 560; a tile begins and ends in 4,000 more,
+// of which most is 64 KB of results on their way while every SM stores.  Measured, and no better: tiles of 160 columns with three
+// sums (177), or of 256 as four sums of 128 (173), sums by 512 threads (188), loads of 32 columns at a time (165), a pair of CTAs on one product (185), w's half copied to
+// both of a pair (162), results stored by other warps or by copies during the next tile (162 to 177: their buffer costs a stage of operands).  With neither
+// the sums' work nor the copies it takes 137.
 #include "fp8.cuh"
 
 namespace cgdr {
@@ -19,14 +22,22 @@ using namespace fp8;
 
 constexpr int kRows = 128;
 constexpr int kSum = 256;                             // threads that add up
+constexpr int kIssue = 2;                             // threads that issue products
 constexpr int kThreads = kSum + 128;                  // and the warps that copy, multiply and hold tensor memory
 constexpr int kRegsSum = 224, kRegsRest = 56;         // 2 x 224 + 56 = 3 x 168, what the block is launched with
 constexpr int kOutBytes = 32 * 128;                   // of a warp: 32 rows of 128 bytes
+
+#ifdef CGDR_DEBUG_CHECKS
+constexpr bool kInside = false;                       // every store is tested
+#else
+constexpr bool kInside = true;
+#endif
 
 template <int BN> struct Shape {
     static constexpr int stages = BN == 256 ? 4 : 6, sums = 512 / BN;
     static constexpr int a = kRows * kBlockK, b = BN * kBlockK, stage = a + b;
     static constexpr int out = stages * stage, bars = out + kSum / 32 * kOutBytes;
+    static_assert(stages % kIssue == 0 && sums % kIssue == 0, "each of the issuing threads has its own");
     enum { full, empty = full + stages, ready = empty + stages, taken = ready + sums, drain = taken + sums, never, count };
     static constexpr int bytes = bars + count * 8 + 1024;    // and the room to align to 1024 bytes
 };
@@ -54,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
             mbar_init(bar(S::ready + i), 1);
             mbar_init(bar(S::taken + i), kSum / 32);
         }
-        mbar_init(bar(S::drain), 1);
+        mbar_init(bar(S::drain), kIssue);
         mbar_init(bar(S::never), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -77,13 +88,21 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
         const uint32_t out = base + S::out + warp * kOutBytes;
         uint32_t at = 0;                              // sums taken so far
         bool go = true;
+        const float *xs, *ws;
+        float xn, wn;                                 // scales of the next block
+        auto scales_of = [&](int tile) {
+            const int row = tile % tiles_m * kRows + r, c = tile / tiles_m * BN + half * kCols;
+            xs = p.xs + (int64_t)min(row, p.n - 1) * p.blocks;
+            ws = p.ws + (int64_t)min(c / kBlockK, (p.N - 1) / kBlockK) * p.blocks;
+            xn = __ldg(xs);
+            wn = __ldg(ws);
+        };
+        scales_of(blockIdx.x);
         for (int tile = blockIdx.x; tile < tiles && go; tile += gridDim.x) {
-            const int m0 = tile % tiles_m * kRows, c0 = tile / tiles_m * BN + half * kCols, row = m0 + r;
-            const float *xs = p.xs + (int64_t)min(row, p.n - 1) * p.blocks, *ws = p.ws + (int64_t)min(c0 / kBlockK, (p.N - 1) / kBlockK) * p.blocks;
+            const int m0 = tile % tiles_m * kRows, c0 = tile / tiles_m * BN + half * kCols;
             f32x2 acc[kCols / 2];
 #pragma unroll
             for (int c = 0; c < kCols / 2; ++c) acc[c] = both(0.f);
-            float xn = __ldg(xs), wn = __ldg(ws);
             for (int b = 0; b < p.blocks; ++b, ++at) {
                 const f32x2 s = both(xn * wn);
                 if (b + 1 < p.blocks) {
@@ -114,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
                 }
             }
             if (!go) break;
+            if (tile + gridDim.x < tiles) scales_of(tile + gridDim.x);
             // a warp's 32 rows leave through shared memory, 128 bytes of each at a time
             const int osz = p.o_f32 ? 4 : 2;
 #pragma unroll
@@ -141,21 +161,30 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
                                  "r"(w[3]) : "memory");
                 }
                 __syncwarp();
+                const int to = m0 + 32 * (warp & 3) + (lane >> 3), n = 16 / osz, col = c0 + part * 32 + (lane & 7) * n;
+                const int64_t e0 = (int64_t)to * p.o_st + col;
+                unsigned char *dst = static_cast<unsigned char *>(p.o) + e0 * osz;
+                uint4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int rr = 4 * i + (lane >> 3), c = lane & 7, to = m0 + 32 * (warp & 3) + rr;
-                    uint4 v;
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(out + rr * 128 + ((c ^ (rr & 7)) << 4)));
-                    const int n = 16 / osz, col = c0 + part * 32 + c * n;
-                    const int64_t e0 = (int64_t)to * p.o_st + col;
-                    if (to >= p.n || col >= p.N || !range_in_bounds(e0, min(n, p.N - col), p.eo, p.status, nullptr)) continue;
-                    unsigned char *dst = static_cast<unsigned char *>(p.o) + e0 * osz;
-                    if (col + n <= p.N) *reinterpret_cast<uint4 *>(dst) = v;
-                    else {
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                        for (int e = 0; e < p.N - col; ++e) {
-                            if (p.o_f32) reinterpret_cast<uint32_t *>(dst)[e] = e == 0 ? w[0] : e == 1 ? w[1] : w[2];
-                            else reinterpret_cast<uint16_t *>(dst)[e] = (uint16_t)((e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3]) >> (16 * (e & 1)));
+                    const int rr = 4 * i + (lane >> 3);
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w) : "r"(out + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)));
+                }
+                if (kInside && m0 + 32 * (warp & 3) + 32 <= p.n && c0 + part * 32 + 8 * n <= p.N) {      // all of it
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(dst + 4 * i * p.o_st * osz) = v[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (to + 4 * i >= p.n || col >= p.N || !range_in_bounds(e0 + 4 * i * p.o_st, min(n, p.N - col), p.eo, p.status, nullptr)) continue;
+                        unsigned char *row = dst + 4 * i * p.o_st * osz;
+                        if (col + n <= p.N) *reinterpret_cast<uint4 *>(row) = v[i];
+                        else {
+                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                            for (int e = 0; e < p.N - col; ++e) {
+                                if (p.o_f32) reinterpret_cast<uint32_t *>(row)[e] = e == 0 ? w[0] : e == 1 ? w[1] : w[2];
+                                else reinterpret_cast<uint16_t *>(row)[e] = (uint16_t)((e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3]) >> (16 * (e & 1)));
+                            }
                         }
                     }
                 }
@@ -182,26 +211,24 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
             if (!go)                                  // what is on its way has to land before the block ends
                 for (uint32_t u = at > S::stages ? at - S::stages : 0; u < at; ++u)
                     keep_waiting(bar(S::full + u % S::stages), (u / S::stages) & 1, &s_never, nullptr, kMatmulPolls);
-        } else if (warp == kSum / 32 + 1 && lane == 0) {
-            // ---------------------------------------------------------------- products
-            uint32_t at = 0;
+        } else if (warp <= kSum / 32 + kIssue && lane == 0) {
+            // ---------------------------------------------------------------- products: two threads, a block of K each in turn
+            const uint32_t total = (uint32_t)((tiles - blockIdx.x + gridDim.x - 1) / gridDim.x) * p.blocks;    // blocks of K of all tiles
+            const uint32_t first = warp - kSum / 32 - 1;
+            uint32_t st = first, sum = first, st_phase = 0, sum_phase = 1;    // (a sum's first use waits for the phase before the first, which counts as over)
             bool go = true;
-            for (int tile = blockIdx.x; tile < tiles && go; tile += gridDim.x) {
-                for (int b = 0; b < p.blocks; ++b, ++at) {
-                    const int st = at % S::stages, sum = at % S::sums;
-                    if (at >= S::sums) go = wait(S::taken + sum, (at / S::sums - 1) & 1);
-                    if (go) go = wait(S::full + st, (at / S::stages) & 1);
-                    if (!go) break;
-                    fence_after_sync();
-                    mma_block<BN>(tmem + sum * BN, base + st * S::stage, base + st * S::stage + S::a);
-                    commit(bar(S::empty + st));
-                    commit(bar(S::ready + sum));
-                }
+            for (uint32_t at = first; at < total; at += kIssue) {
+                go = wait(S::full + st, st_phase) && wait(S::taken + sum, sum_phase);
+                if (!go) break;
+                fence_after_sync();
+                mma_block<BN>(tmem + sum * BN, base + st * S::stage, base + st * S::stage + S::a);
+                commit(bar(S::ready + sum));
+                commit(bar(S::empty + st));
+                if ((st += kIssue) >= S::stages) { st -= S::stages; st_phase ^= 1; }
+                if ((sum += kIssue) >= S::sums) { sum -= S::sums; sum_phase ^= 1; }
             }
-            if (!go) {                                // and what was issued has to end
-                commit(bar(S::drain));
-                keep_waiting(bar(S::drain), 0, &s_never, nullptr, kMatmulPolls);
-            }
+            commit(bar(S::drain));                    // and what both have issued has to end
+            keep_waiting(bar(S::drain), 0, &s_never, nullptr, kMatmulPolls);
         }
     }
     __syncwarp();
@@ -252,11 +279,11 @@ bool encode_rows(CUtensorMap &m, const void *base, int64_t K, int64_t rows, int6
 }
 
 cgdr_status launch_matmul_tiles(const cgdr_matmul_args &a, MatmulParams &p, cudaStream_t s) {
-    // A tile of 256 columns takes 15.8 us for K = 4096, one of 128 11.9 (14.4 where it is the only one): 2000 rows of 12288 x 4096 95 us and
-    // 131, 512 rows of 4096 x 4096 17.3 and 15.2.
+    // A tile of 256 columns takes 14.7 us of K = 4096 where there are many, one of 128 9.1: 1500 rows of 4096 x 4096 (2 rounds of the SMs against
+    // 3) 32.8 us and 30.2, 2500 (3 against 5) 46.7 and 48.1, 600 (1 against 2) 17.8 and 21.2.
     const int64_t sms = device_sms() > 0 ? device_sms() : 152, rows = (a.n + kRows - 1) / kRows;
     const int64_t wide = (rows * ((a.N + 255) / 256) + sms - 1) / sms, narrow = (rows * groups_of(a.N) + sms - 1) / sms;
-    return 4 * wide <= 3 * narrow ? launch<256>(a, p, s) : launch<128>(a, p, s);
+    return 5 * wide <= 3 * narrow ? launch<256>(a, p, s) : launch<128>(a, p, s);
 }
 
 }  // namespace cgdr

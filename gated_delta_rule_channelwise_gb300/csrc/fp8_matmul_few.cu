@@ -265,17 +265,18 @@ template <int BT> cgdr_status launch(const cgdr_matmul_args &a, MatmulParams &p,
 
 }  // namespace
 
-// This kernel, where its tiles are few enough to be split (or at least to run all at once), unless K is so short that there is
-// little to split.  Here / the better of the two tile widths there, us:
-//   4096 x 4096:   n = 128 10.2 / 14.5,  256 13.3 / 14.7,  384 20.4 / 14.7
-//   12288 x 4096:  n = 64 15.4 / 16.4,   128 21.5 / 16.5
-//   4096 x 12288:  n = 128 18.7 / 36.5,  256 28.3 / 36.9,  384 46.8 / 37.4
-//   1000 x 4096:   n = 512 9.9 / 14.3,   1000 13.3 / 14.4, 2000 20.7 / 14.8
-//   512 x 512:     n = 16 3.8 / 4.1,     64 5.2 / 4.2
+// This kernel, where its tiles are few enough to be split, unless K is so short that there is little to split; where K is
+// long, also where they just run all at once.  Here / the better of the two tile widths there, us:
+//   4096 x 4096:   n = 64 10.2 / 11.5,   128 10.1 / 11.8,  256 13.2 / 11.8,  320 19.9 / 11.9
+//   12288 x 4096:  n = 32 13.6 / 14.8,   64 15.4 / 14.8,   128 21.5 / 15.1
+//   4096 x 12288:  n = 128 18.9 / 29.7,  192 22.5 / 28.3,  256 28.3 / 28.9,  320 48.5 / 28.2
+//   1000 x 4096:   n = 512 9.9 / 11.6,   640 11.1 / 11.7,  1000 13.3 / 11.9
+//   512 x 512:     n = 16 3.8 / 4.1,     64 5.7 / 4.0
 bool matmul_few(const cgdr_matmul_args &a) {
     if (a.path != CGDR_MATMUL_AUTO) return a.path == CGDR_MATMUL_FEW;
     const int64_t sms = device_sms() > 0 ? device_sms() : 152, tiles = (int64_t)((a.n + 63) / 64) * groups_of(a.N);
-    return a.n <= 16 ? tiles <= 19 * sms / 10 : tiles <= 19 * sms / 20 && groups_of(a.K) > 8;
+    if (a.n <= 16) return tiles <= 19 * sms / 10;
+    return groups_of(a.K) > 8 && tiles <= (a.n <= 32 || groups_of(a.K) > 64 ? 19 : 12) * sms / 20;
 }
 
 // 16, 32 or 64 rows of x a tile.  (128 of them take an SM for one CTA: 13.1 us against 10.1 for 128 rows of 4096 x 4096.)
