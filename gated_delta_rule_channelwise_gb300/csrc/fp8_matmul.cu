@@ -7,12 +7,12 @@
 // is taken.  One thread copies operands ahead.  Two issue the products, a block each in turn: the waits, four instructions and two
 // commits of a block take one thread 600 to 700 cycles, longer than the products of 128 columns run (256; 512 rows by 4,096 x 4,096
 // take 15.2 us with one such thread, 12.4 with two).
-// 4,001 x 12,288 x 4,096: 162 us, 2,480 TFLOP/s, 1.31 times what a large bf16 product reaches, 0.66 of twice that.  A block of
-// 128 x 256 x 128 takes 750 cycles there (the slope along K), the products alone 512, the sums alone 560; a tile begins and ends in 4,000 more,
-// of which most is 64 KB of results on their way while every SM stores.  Measured, and no better: tiles of 160 columns with three
-// sums (177), or of 256 as four sums of 128 (173), sums by 512 threads (188), loads of 32 columns at a time (165), a pair of CTAs on one product (185), w's half copied to
-// both of a pair (162), results stored by other warps or by copies during the next tile (162 to 177: their buffer costs a stage of operands).  With neither
-// the sums' work nor the copies it takes 137.
+// 4,001 x 12,288 x 4,096: 163 us, 2,460 TFLOP/s, 1.31 times what a large bf16 product reaches, 0.65 of twice that.  A block of
+// 128 x 256 x 128 takes 750 cycles there (the slope along K), the products alone 512, the sums alone 560; a tile begins and ends in
+// 4,000 more, of which most is 64 KB of results on their way while every SM stores.  Measured, and no better: tiles of 160 columns with
+// three sums (177), or of 256 as four sums of 128 (173), sums by 512 threads (188), loads of 32 columns at a time (165), a pair of CTAs on
+// one product (185), w's half copied to both of a pair (162), results stored by other warps or by copies during the next tile (162 to
+// 177: their buffer costs a stage of operands), a last round of half tiles (163).  With neither the sums' work nor the copies it takes 137.
 #include "fp8.cuh"
 
 namespace cgdr {
