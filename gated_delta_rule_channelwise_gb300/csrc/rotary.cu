@@ -149,6 +149,7 @@ cgdr_status check(const cgdr_rotary_args *a) {
     if (a->n == 0) return CGDR_OK;
     if (!disjoint(a->n, a->q_st, a->Hq, a->q_sh, a->D) || !disjoint(a->n, a->k_st, a->Hk, a->k_sh, a->D)) return CGDR_ERR_INVALID_ARG;
     if (!a->q || (a->Hk > 0 && !a->k) || !a->positions || !a->freq) return CGDR_ERR_INVALID_ARG;
+    if (a->Hk > 0 && a->k == a->q) return CGDR_ERR_INVALID_ARG;     // turned twice
     const int esz = esize(a->dtype);
     if (!aligned_to(a->q, 16) || !aligned_to(a->positions, 4) || !aligned_to(a->freq, 8) || !aligned_to(a->status, 4)) return CGDR_ERR_ALIGNMENT;
     if (!row_stride_ok(a->q_st, esz) || !row_stride_ok(a->q_sh, esz)) return CGDR_ERR_ALIGNMENT;

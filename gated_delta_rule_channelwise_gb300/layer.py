@@ -41,11 +41,11 @@ def _groups(n):
 
 
 def _tokens(t, name):
-    """(pointer, token stride, head stride) of [n, C] or [n, H, C]."""
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    """(pointer, token stride, head stride) of [n, C] or [n, H, C]; of one token or head its stride says nothing, and 0 stands for it."""
+    st, shape = t.stride(), t.shape
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError("%s: innermost dimension must be contiguous" % name)
-    return (t.data_ptr(), st[0], st[1]) if len(st) == 3 else (t.data_ptr(), st[0], 0)
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if len(st) == 3 and shape[1] > 1 else 0
 
 
 _NONE = (0, 0, 0)

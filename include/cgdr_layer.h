@@ -71,9 +71,10 @@ cgdr_status cgdr_quantize(const cgdr_quantize_args *args, void *stream);
  * o = x w^T of 8-bit operands, x [n,K] with x_scale [n,KB], w [N,K] with w_scale [NB,KB]; KB and NB
  * are K and N over 128, rounded up:
  *     o[i,j] = sum_b x_scale[i,b] w_scale[j/128,b] sum_{k of block b} x[i,k] w[j,k]
- * Products are exact, sums are fp32; x_scale w_scale is formed first, in fp32, so scales whose product overflows give
- * infinities or NaN.  Rows of x and of w may not overlap (they are described to the copy engine).  A NaN or an infinity reaches the outputs of its row of x, or of its rows
- * of w, and no others.  `path` says which kernel runs (they agree up to the order of sums).  A wait that gives
+ * Products are exact, sums are fp32; x_scale w_scale is formed first, in fp32, so scales whose product
+ * overflows give infinities or NaN.  Rows of x and of w may not overlap (they are described to the copy
+ * engine).  A NaN or an infinity reaches the outputs of its row of x, or of its rows of w, and no others.
+ * `path` says which kernel runs (they agree up to the order of sums).  A wait that gives
  * up reports CGDR_ERR_TIMEOUT in *status; the outputs of its CTA (or cluster) are then undefined.
  */
 typedef enum cgdr_matmul_path {
@@ -113,7 +114,7 @@ typedef struct cgdr_rotary_args {
     int32_t interleaved;
     float scale;
     void *q;  int64_t q_st, q_sh;   /* [n,Hq,D]; in place */
-    void *k;  int64_t k_st, k_sh;   /* [n,Hk,D] or NULL; in place */
+    void *k;  int64_t k_st, k_sh;   /* [n,Hk,D] or NULL; in place; not q */
     const int32_t *positions;       /* [n] */
     const double *freq;             /* [half], radians a position */
     int32_t *status;                /* reserved for the index-checking build */

@@ -75,7 +75,7 @@ INV, UNS, ALN = cg.ERR_INVALID_ARG, cg.ERR_UNSUPPORTED, cg.ERR_ALIGNMENT
     ("matmul", MATMUL, dict(o=P + 8), ALN), ("matmul", MATMUL, dict(status=P + 2), ALN), ("matmul", MATMUL, dict(x_st=128), INV), ("matmul", MATMUL, dict(w_st=0), INV),
     ("rotary", ROTARY, dict(n=-1), INV), ("rotary", ROTARY, dict(Hq=0), INV), ("rotary", ROTARY, dict(half=0), INV), ("rotary", ROTARY, dict(half=33), INV),
     ("rotary", ROTARY, dict(q=0), INV), ("rotary", ROTARY, dict(k=0), INV), ("rotary", ROTARY, dict(positions=0), INV), ("rotary", ROTARY, dict(freq=0), INV),
-    ("rotary", ROTARY, dict(q_sh=0), INV), ("rotary", ROTARY, dict(k_st=64), INV),                                         # heads that overlap
+    ("rotary", ROTARY, dict(k=P), INV), ("rotary", ROTARY, dict(q_sh=0), INV), ("rotary", ROTARY, dict(k_st=64), INV),                                         # heads that overlap
     ("rotary", ROTARY, dict(D=1024, half=512, q_sh=1024, q_st=4096, k_sh=1024, k_st=2048), UNS), ("rotary", ROTARY, dict(dtype=2), UNS),
     ("rotary", ROTARY, dict(Hk=70000, k_st=70000 * 64), UNS), ("rotary", ROTARY, dict(q=P + 2), ALN), ("rotary", ROTARY, dict(q_st=260), ALN),
     ("rotary", ROTARY, dict(freq=P + 4), ALN), ("rotary", ROTARY, dict(k_sh=65, k_st=200), ALN),

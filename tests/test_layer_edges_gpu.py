@@ -179,3 +179,35 @@ def test_given_outputs_and_refusals():
         cg.rms_norm(rand(44, 64, 8).t(), None)
     with pytest.raises(TypeError, match="float64"):
         cg.rotary(rand(1, 4, 1, 64), None, torch.zeros(4, dtype=torch.int32, device="cuda"), torch.ones(32, device="cuda"))
+
+
+def test_one_token_of_any_stride():
+    """The strides of a dimension of size 1 say nothing: a row made of a column is a row."""
+    def row(t):                                       # the same values, with the strides of a transposed column
+        assert t.shape[0] == 1
+        r = t.reshape(-1, 1).clone().t()
+        assert r.stride() == (1, 1)
+        return r
+
+    x, w = rand(71, 1, 264, dtype=BF), 1 + 0.1 * rand(72, 264)
+    assert torch.equal(cg.rms_norm(row(x), w), cg.rms_norm(x, w))
+    r, s = row(x), x.clone()
+    o = row(torch.zeros_like(x))
+    cg.rms_norm(row(x), w, o, residual=r)
+    assert torch.equal(o, cg.rms_norm(x, w, residual=s)) and torch.equal(r, s)
+    for call in (cg.fp8_quantize, cg.fp8_quantize_weight):
+        (a, s), (b, t) = call(x), call(row(x))
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and torch.equal(s, t)
+    x8, xs = cg.fp8_quantize(x)
+    narrow = row(x8.view(torch.uint8)).view(E4M3)
+    for path in PATHS:
+        want = cg.fp8_matmul(x8, xs, x8, xs, path=path)
+        assert torch.equal(cg.fp8_matmul(narrow, xs, narrow, xs, path=path), want)
+    pos, (freq, _) = torch.tensor([12345], dtype=torch.int32, device="cuda"), cg.rotary_frequencies(64)
+    q = x[:, :256].reshape(1, 4, 64).clone()
+    odd = torch.empty_strided((1, 4, 64), (7, 64, 1), dtype=BF, device="cuda").copy_(q)
+    cg.rotary(q, None, pos, freq)
+    cg.rotary(odd, None, pos, freq)
+    assert torch.equal(odd, q)
+    one = torch.empty_strided((5, 1, 64), (64, 3, 1), dtype=BF, device="cuda").copy_(rand(74, 5, 1, 64, dtype=BF))
+    assert torch.equal(cg.rms_norm(one, None), cg.rms_norm(one.reshape(5, 1, 64).contiguous(), None))
