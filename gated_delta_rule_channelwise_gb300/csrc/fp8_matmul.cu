@@ -4,15 +4,15 @@
 // The scales change with every block of K, so a block's product (four instructions of K = 32) is a sum of its own in
 // tensor memory, which 256 threads take from there, scale and add up in registers: a thread has a row of x and half of the
 // tile's columns, so that both scales are one number to it.  Two such sums fit tensor memory: one is formed while the other
-// is taken.  One thread copies operands ahead.  Two issue the products, a block each in turn: the waits, four instructions and two
-// commits of a block take one thread 600 to 700 cycles, longer than the products of 128 columns run (256; 512 rows by 4,096 x 4,096
-// take 15.2 us with one such thread, 12.4 with two).
-// 4,001 x 12,288 x 4,096: 163 us, 2,460 TFLOP/s, 1.31 times what a large bf16 product reaches, 0.65 of twice that.  A block of
-// 128 x 256 x 128 takes 750 cycles there (the slope along K), the products alone 512, the sums alone 560; a tile begins and ends in
-// 4,000 more, of which most is 64 KB of results on their way while every SM stores.  Measured, and no better: tiles of 160 columns with
-// three sums (177), or of 256 as four sums of 128 (173), sums by 512 threads (188), loads of 32 columns at a time (165), a pair of CTAs on
-// one product (185), w's half copied to both of a pair (162), results stored by other warps or by copies during the next tile (162 to
-// 177: their buffer costs a stage of operands), a last round of half tiles (163).  With neither the sums' work nor the copies it takes 137.
+// is taken.  One warp copies operands ahead, one issues the products.
+// 4,001 x 12,288 x 4,096: 154 us, 2,610 TFLOP/s, 1.39 times what a large bf16 product reaches, 0.69 of twice that.  A block of
+// 128 x 256 x 128 takes 710 cycles there (the slope along K; without copies 680), the products alone 512, the sums alone 560, and a sum that is
+// handed over and back waits 390; a tile begins and ends in 4,000 more, of which most is 64 KB of results on their way while every SM stores.
+// A block of 128 columns is bound by its operands' way from L2.  Measured, and no better: two warps that issue (155), four sums of 128 columns
+// (156), a look at the next sum ahead of its wait (158), w's half copied to both of a pair of CTAs (154), results stored by other warps during the
+// next tile (154: the buffer costs a stage of operands), 128 columns with every other block for each half of the sums' threads (10 % slower).
+// While one lane issued, behind a branch (163): three sums of 160 columns (177), 512 threads for the sums (188), a pair of CTAs on one product (185), a
+// last round of half tiles (163).
 #include "fp8.cuh"
 
 namespace cgdr {
@@ -22,7 +22,6 @@ using namespace fp8;
 
 constexpr int kRows = 128;
 constexpr int kSum = 256;                             // threads that add up
-constexpr int kIssue = 2;                             // threads that issue products
 constexpr int kThreads = kSum + 128;                  // and the warps that copy, multiply and hold tensor memory
 constexpr int kRegsSum = 224, kRegsRest = 56;         // 2 x 224 + 56 = 3 x 168, what the block is launched with
 constexpr int kOutBytes = 32 * 128;                   // of a warp: 32 rows of 128 bytes
@@ -37,7 +36,6 @@ template <int BN> struct Shape {
     static constexpr int stages = BN == 256 ? 4 : 6, sums = 512 / BN;
     static constexpr int a = kRows * kBlockK, b = BN * kBlockK, stage = a + b;
     static constexpr int out = stages * stage, bars = out + kSum / 32 * kOutBytes;
-    static_assert(stages % kIssue == 0 && sums % kIssue == 0, "each of the issuing threads has its own");
     enum { full, empty = full + stages, ready = empty + stages, taken = ready + sums, drain = taken + sums, never, count };
     static constexpr int bytes = bars + count * 8 + 1024;    // and the room to align to 1024 bytes
 };
@@ -65,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
             mbar_init(bar(S::ready + i), 1);
             mbar_init(bar(S::taken + i), kSum / 32);
         }
-        mbar_init(bar(S::drain), kIssue);
+        mbar_init(bar(S::drain), 1);
         mbar_init(bar(S::never), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -193,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-        if (warp == kSum / 32 && lane == 0) {
+        if (warp == kSum / 32) {
             // ---------------------------------------------------------------- copies
             uint32_t at = 0;
             bool go = true;
@@ -201,34 +199,34 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
                 const int m0 = tile % tiles_m * kRows, n0 = tile / tiles_m * BN;
                 for (int b = 0; b < p.blocks; ++b, ++at) {
                     const int st = at % S::stages;
-                    if (at >= S::stages) go = wait(S::empty + st, (at / S::stages - 1) & 1);
+                    if (at >= S::stages) go = __all_sync(0xffffffffu, wait(S::empty + st, (at / S::stages - 1) & 1));
                     if (!go) break;
-                    expect(bar(S::full + st), S::stage);
-                    copy_box(base + st * S::stage, &p.mx, b * kBlockK, m0, bar(S::full + st));
-                    copy_box(base + st * S::stage + S::a, &p.mw, b * kBlockK, n0, bar(S::full + st));
+                    copy_boxes(base + st * S::stage, S::a, S::stage, &p.mx, m0, &p.mw, n0, b * kBlockK, bar(S::full + st));
                 }
             }
             if (!go)                                  // what is on its way has to land before the block ends
                 for (uint32_t u = at > S::stages ? at - S::stages : 0; u < at; ++u)
                     keep_waiting(bar(S::full + u % S::stages), (u / S::stages) & 1, &s_never, nullptr, kMatmulPolls);
-        } else if (warp <= kSum / 32 + kIssue && lane == 0) {
-            // ---------------------------------------------------------------- products: two threads, a block of K each in turn
-            const uint32_t total = (uint32_t)((tiles - blockIdx.x + gridDim.x - 1) / gridDim.x) * p.blocks;    // blocks of K of all tiles
-            const uint32_t first = warp - kSum / 32 - 1;
-            uint32_t st = first, sum = first, st_phase = 0, sum_phase = 1;    // (a sum's first use waits for the phase before the first, which counts as over)
+        } else if (warp == kSum / 32 + 1) {
+            // ---------------------------------------------------------------- products
+            uint32_t at = 0;
             bool go = true;
-            for (uint32_t at = first; at < total; at += kIssue) {
-                go = wait(S::full + st, st_phase) && wait(S::taken + sum, sum_phase);
-                if (!go) break;
-                fence_after_sync();
-                mma_block<BN>(tmem + sum * BN, base + st * S::stage, base + st * S::stage + S::a);
-                commit(bar(S::ready + sum));
-                commit(bar(S::empty + st));
-                if ((st += kIssue) >= S::stages) { st -= S::stages; st_phase ^= 1; }
-                if ((sum += kIssue) >= S::sums) { sum -= S::sums; sum_phase ^= 1; }
+            for (int tile = blockIdx.x; tile < tiles && go; tile += gridDim.x) {
+                for (int b = 0; b < p.blocks; ++b, ++at) {
+                    const int st = at % S::stages, sum = at % S::sums;
+                    go = wait(S::full + st, (at / S::stages) & 1) && (at < S::sums || wait(S::taken + sum, (at / S::sums - 1) & 1));
+                    go = __all_sync(0xffffffffu, go);
+                    if (!go) break;
+                    fence_after_sync();
+                    mma_block<BN>(tmem + sum * BN, base + st * S::stage, base + st * S::stage + S::a);
+                    commit_warp(bar(S::ready + sum));
+                    commit_warp(bar(S::empty + st));
+                }
             }
-            commit(bar(S::drain));                    // and what both have issued has to end
-            keep_waiting(bar(S::drain), 0, &s_never, nullptr, kMatmulPolls);
+            if (!go) {                                // and what was issued has to end
+                commit_warp(bar(S::drain));
+                keep_waiting(bar(S::drain), 0, &s_never, nullptr, kMatmulPolls);
+            }
         }
     }
     __syncwarp();
@@ -279,8 +277,8 @@ bool encode_rows(CUtensorMap &m, const void *base, int64_t K, int64_t rows, int6
 }
 
 cgdr_status launch_matmul_tiles(const cgdr_matmul_args &a, MatmulParams &p, cudaStream_t s) {
-    // A tile of 256 columns takes 14.7 us of K = 4096 where there are many, one of 128 9.1: 1500 rows of 4096 x 4096 (2 rounds of the SMs against
-    // 3) 32.8 us and 30.2, 2500 (3 against 5) 46.7 and 48.1, 600 (1 against 2) 17.8 and 21.2.
+    // A tile of 256 columns takes 14.0 us of K = 4096 where there are many, one of 128 8.9: 1500 rows of 4096 x 4096 (2 rounds of the SMs against
+    // 3) 31.1 us and 30.2, 2500 (3 against 5) 44.9 and 47.7, 600 (1 against 2) 16.7 and 21.0.
     const int64_t sms = device_sms() > 0 ? device_sms() : 152, rows = (a.n + kRows - 1) / kRows;
     const int64_t wide = (rows * ((a.N + 255) / 256) + sms - 1) / sms, narrow = (rows * groups_of(a.N) + sms - 1) / sms;
     return 5 * wide <= 3 * narrow ? launch<256>(a, p, s) : launch<128>(a, p, s);

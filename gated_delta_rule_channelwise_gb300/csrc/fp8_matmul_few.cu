@@ -5,7 +5,7 @@
 // are sent to one CTA of the cluster, which adds them in their order: no workspace, and no order of arrival in a result.
 // Block by block of K as in the tiles kernel: a product in tensor memory, taken from there, scaled and added up in registers, a
 // thread a row of w.
-// One row by 12288 x 4096 (50.4 MB) takes 12.6 us, 64 rows 14.5: the bytes at the copy rate are 7.4 and 7.7.  The copies
+// One row by 12288 x 4096 (50.4 MB) takes 11.8 us, 64 rows 13.7: the bytes at the copy rate are 7.4 and 7.7.  The copies
 // end after 9.5 us of these, the parts meet in 0.4 and 1.6 (they pass between shared memories at 17 bytes a clock), 2 are the launch.  A cluster
 // barrier after the parts have been read cost 0.9, sends of 4 bytes instead of 16 another 0.4.
 #include "fp8.cuh"
@@ -190,35 +190,32 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::residents) matmul_few_ker
             }
         }
     } else if (warp == kSum / 32) {
-        if (lane == 0) {
-            bool go = true;
-            int at = 0;
-            for (; at < b1 - b0; ++at) {
-                const int st = at % S::stages;
-                if (at >= S::stages) go = wait(S::empty + st, (at / S::stages - 1) & 1);
-                if (!go) break;
-                expect(bar(S::full + st), S::stage);
-                copy_box(base + st * S::stage, &p.mw, (b0 + at) * kBlockK, n0, bar(S::full + st));
-                copy_box(base + st * S::stage + S::a, &p.mx, (b0 + at) * kBlockK, t0, bar(S::full + st));
-            }
-            if (!go)                                  // what is on its way has to land before the block ends
-                for (int u = at > S::stages ? at - S::stages : 0; u < at; ++u)
-                    keep_waiting(bar(S::full + u % S::stages), (u / S::stages) & 1, &s_never, nullptr, kMatmulPolls);
+        bool go = true;
+        int at = 0;
+        for (; at < b1 - b0; ++at) {
+            const int st = at % S::stages;
+            if (at >= S::stages) go = __all_sync(0xffffffffu, wait(S::empty + st, (at / S::stages - 1) & 1));
+            if (!go) break;
+            copy_boxes(base + st * S::stage, S::a, S::stage, &p.mw, n0, &p.mx, t0, (b0 + at) * kBlockK, bar(S::full + st));
         }
-    } else if (lane == 0) {
+        if (!go)                                      // what is on its way has to land before the block ends
+            for (int u = at > S::stages ? at - S::stages : 0; u < at; ++u)
+                keep_waiting(bar(S::full + u % S::stages), (u / S::stages) & 1, &s_never, nullptr, kMatmulPolls);
+    } else {
         bool go = true;
         for (int at = 0; at < b1 - b0; ++at) {
             const int st = at % S::stages, sum = at % S::sums;
             if (at >= S::sums) go = wait(S::taken + sum, (at / S::sums - 1) & 1);
             if (go) go = wait(S::full + st, (at / S::stages) & 1);
+            go = __all_sync(0xffffffffu, go);
             if (!go) break;
             fence_after_sync();
             mma_block<BT>(tmem + sum * BT, base + st * S::stage, base + st * S::stage + S::a);
-            commit(bar(S::empty + st));
-            commit(bar(S::ready + sum));
+            commit_warp(bar(S::empty + st));
+            commit_warp(bar(S::ready + sum));
         }
         if (!go) {                                    // and what was issued has to end
-            commit(bar(S::drain));
+            commit_warp(bar(S::drain));
             keep_waiting(bar(S::drain), 0, &s_never, nullptr, kMatmulPolls);
         }
     }
@@ -267,10 +264,10 @@ template <int BT> cgdr_status launch(const cgdr_matmul_args &a, MatmulParams &p,
 
 // This kernel, where its tiles are few enough to be split, unless K is so short that there is little to split; where K is
 // long, also where they just run all at once.  Here / the better of the two tile widths there, us:
-//   4096 x 4096:   n = 64 10.2 / 11.5,   128 10.1 / 11.8,  256 13.2 / 11.8,  320 19.9 / 11.9
-//   12288 x 4096:  n = 32 13.6 / 14.8,   64 15.4 / 14.8,   128 21.5 / 15.1
-//   4096 x 12288:  n = 128 18.9 / 29.7,  192 22.5 / 28.3,  256 28.3 / 28.9,  320 48.5 / 28.2
-//   1000 x 4096:   n = 512 9.9 / 11.6,   640 11.1 / 11.7,  1000 13.3 / 11.9
+//   4096 x 4096:   n = 64 10.1 / 11.3,   128 10.2 / 11.4,  256 13.2 / 11.5,  320 20.1 / 11.8
+//   12288 x 4096:  n = 32 13.3 / 14.0,   64 15.0 / 14.2,   128 21.1 / 14.8
+//   4096 x 12288:  n = 128 18.0 / 29.3,  192 22.0 / 28.4,  256 27.7 / 28.5,  320 48.5 / 28.3
+//   1000 x 4096:   n = 512 10.0 / 11.4,  640 11.2 / 11.5,  1000 13.3 / 11.8
 //   512 x 512:     n = 16 3.8 / 4.1,     64 5.7 / 4.0
 bool matmul_few(const cgdr_matmul_args &a) {
     if (a.path != CGDR_MATMUL_AUTO) return a.path == CGDR_MATMUL_FEW;
