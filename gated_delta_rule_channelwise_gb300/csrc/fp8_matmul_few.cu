@@ -232,20 +232,24 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::residents) matmul_few_ker
     if (s_stop) asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Parts of K: as many as let all CTAs be resident at once, two on an SM.  Clusters of more than four leave more of them empty,
-// and a part has two blocks at least.  Measured, us:
+// Parts of K: as many as let all CTAs be resident at once, two on an SM.  Clusters of more than four leave more of them empty
+// and take longer to meet, so they need a third of the SMs to spare or parts of eight blocks; every part has two blocks at least.  Measured, us:
 //   N x K, n            parts 1     2     3     4     5     6     8
-//   4096 x 4096, 1       13.5   9.0   7.8   7.3   7.7   7.7   7.2
-//   4096 x 4096, 256     17.4  13.3  19.1  18.5  23.2  23.8  29.4
-//   12288 x 4096, 64     20.0  16.1  15.4  19.5  19.6  23.8  24.8
-//   1000 x 4096, 384     16.8  11.0  10.6   9.7   9.4  13.8  14.9
-//   4096 x 12288, 64     41.5  24.7  19.5  17.2  17.1  15.8  15.5
-//   2048 x 1024, 64       8.1   6.5   6.1   5.5   5.6   5.5   6.6
+//   4096 x 4096, 1       10.1   7.3   6.8   6.5   6.9   7.0   6.7
+//   4096 x 4096, 64      15.6  10.7   9.8   8.8   9.1   9.6  10.2
+//   4096 x 4096, 128     15.7  10.8  11.0  10.2  14.9  15.5  16.3
+//   12288 x 4096, 64     18.2  15.0  15.0  19.0  19.4  23.6  24.8
+//   1000 x 4096, 64      15.1   9.7   8.4   7.3   7.0   6.7   6.4
+//   1000 x 4096, 128     15.2   9.7   8.4   7.4   7.1   6.8   7.6
+//   1000 x 4096, 384     15.7  10.3  10.5   9.5   9.2  13.6  14.6
+//   4096 x 12288, 64     37.2  21.7  18.1  16.0  16.6  15.1  15.1
+//   2048 x 1024, 64       7.8   6.1   6.0   5.5   5.4   5.5   6.4
 int split_of(int64_t tiles, int blocks) {
     const int64_t sms = device_sms() > 0 ? device_sms() : 152;
     int64_t split = 19 * sms / (10 * tiles);
     if (split > 4 && split * tiles > 17 * sms / 10) split = 17 * sms / (10 * tiles) > 4 ? 17 * sms / (10 * tiles) : 4;
     if (split > kMaxSplit) split = kMaxSplit;
+    if (split > 4 && split * tiles > 2 * sms / 3 && split * 8 > blocks) split = 2 * sms / (3 * tiles) > 4 ? 2 * sms / (3 * tiles) : 4;
     if (split > blocks / 2) split = blocks / 2;
     return split < 1 ? 1 : (int)split;
 }
@@ -264,7 +268,7 @@ template <int BT> cgdr_status launch(const cgdr_matmul_args &a, MatmulParams &p,
 
 // This kernel, where its tiles are few enough to be split, unless K is so short that there is little to split; where K is
 // long, also where they just run all at once.  Here / the better of the two tile widths there, us:
-//   4096 x 4096:   n = 64 10.1 / 11.3,   128 10.2 / 11.4,  256 13.2 / 11.5,  320 20.1 / 11.8
+//   4096 x 4096:   n = 64 8.8 / 11.2,    128 10.2 / 11.4,  256 13.2 / 11.5,  320 20.1 / 11.8
 //   12288 x 4096:  n = 32 13.3 / 14.0,   64 15.0 / 14.2,   128 21.1 / 14.8
 //   4096 x 12288:  n = 128 18.0 / 29.3,  192 22.0 / 28.4,  256 27.7 / 28.5,  320 48.5 / 28.3
 //   1000 x 4096:   n = 512 10.0 / 11.4,  640 11.2 / 11.5,  1000 13.3 / 11.8
