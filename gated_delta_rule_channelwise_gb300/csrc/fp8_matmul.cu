@@ -8,9 +8,10 @@
 // 4,001 x 12,288 x 4,096: 154 us, 2,610 TFLOP/s, 1.39 times what a large bf16 product reaches, 0.69 of twice that.  A block of
 // 128 x 256 x 128 takes 710 cycles there (the slope along K; without copies 680), the products alone 512, the sums alone 560, and a sum that is
 // handed over and back waits 390; a tile begins and ends in 4,000 more, of which most is 64 KB of results on their way while every SM stores.
-// A block of 128 columns is bound by its operands' way from L2.  Measured, and no better: two warps that issue (155), four sums of 128 columns
+// A block of 128 columns takes 460 to 490, of which issuing takes 400 and its operands' way from L2 425.  Measured, and no better: two warps that issue (155), four sums of 128 columns
 // (156), a look at the next sum ahead of its wait (158), w's half copied to both of a pair of CTAs (154), results stored by other warps during the
-// next tile (154: the buffer costs a stage of operands), 128 columns with every other block for each half of the sums' threads (10 % slower).
+// next tile (154: the buffer costs a stage of operands), 128 columns with every other block for each half of the sums' threads (10 % slower), one barrier for a
+// sum that is there and operands that are not needed any more (the same).
 // While one lane issued, behind a branch (163): three sums of 160 columns (177), 512 threads for the sums (188), a pair of CTAs on one product (185), a
 // last round of half tiles (163).
 #include "fp8.cuh"
