@@ -5,7 +5,7 @@
 // tensor memory, which 256 threads take from there, scale and add up in registers: a thread has a row of x and half of the
 // tile's columns, so that both scales are one number to it.  Two such sums fit tensor memory: one is formed while the other
 // is taken.  One warp copies operands ahead, one issues the products.
-// 4,001 x 12,288 x 4,096: 154 us, 2,610 TFLOP/s, 1.39 times what a large bf16 product reaches, 0.69 of twice that.  A block of
+// 4,001 x 12,288 x 4,096: 154 to 158 us (the GPU is near its power limit), 2,580 TFLOP/s, 0.68 of twice what a large bf16 product reaches.  A block of
 // 128 x 256 x 128 takes 710 cycles there (the slope along K; without copies 680), the products alone 512, the sums alone 560, and a sum that is
 // handed over and back waits 390; a tile begins and ends in 4,000 more, of which most is 64 KB of results on their way while every SM stores.
 // A block of 128 columns takes 460 to 490, of which issuing takes 400 and its operands' way from L2 425.  Measured, and no better: two warps that issue (155), four sums of 128 columns
