@@ -103,5 +103,29 @@ __device__ __forceinline__ bool keep_waiting(uint32_t bar, uint32_t parity, vola
     return false;
 }
 
+// What a block leaves must be over, whichever wait gave up and whichever warp had issued all that it had to: its memory and its tensor
+// memory go to the next block.  The copying warp waits for its last uses of every stage, the issuing one for all its products.  Both
+// are over before the last sums are taken in any other case, so these waits cost nothing there.
+template <int kStages>
+__device__ __forceinline__ void copies_land(uint32_t first_bar, uint32_t issued) {
+    for (uint32_t u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
+        mbar_wait(first_bar + 8 * (u % kStages), (u / kStages) & 1, kMatmulPolls);
+}
+__device__ __forceinline__ void products_end(uint32_t bar) {
+    commit_warp(bar);
+    mbar_wait(bar, 0, kMatmulPolls);
+}
+// Index-checking build, one thread, after every warp has come to its end: CGDR_ERR_BOUNDS if that did not hold.
+template <int kStages>
+__device__ __forceinline__ void check_over(uint32_t full, uint32_t issued, uint32_t drain, int *status) {
+#ifdef CGDR_DEBUG_CHECKS
+    bool over = mbar_try_wait(drain, 0);
+    for (uint32_t u = issued > kStages ? issued - kStages : 0; u < issued; ++u) over = over && mbar_try_wait(full + 8 * (u % kStages), (u / kStages) & 1);
+    in_bounds(over ? 0 : -1, 1, status, nullptr);
+#else
+    (void)full; (void)issued; (void)drain; (void)status;
+#endif
+}
+
 }  // namespace fp8
 }  // namespace cgdr

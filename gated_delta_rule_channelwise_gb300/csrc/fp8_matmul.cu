@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
     constexpr int kCols = BN / 2;                     // of a thread
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_stop, s_never;          // a wait gave up: everybody leaves; (never set)
+    __shared__ volatile int s_stop;                   // a wait gave up: everybody leaves
+    __shared__ uint32_t s_issued;                     // copies of this block (index-checking build)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     auto bar = [&](int i) { return base + S::bars + 8 * i; };
@@ -55,7 +56,6 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
 
     if (tid == 0) {
         s_stop = 0;
-        s_never = 0;
         for (int i = 0; i < S::stages; ++i) {
             mbar_init(bar(S::full + i), 1);
             mbar_init(bar(S::empty + i), 1);
@@ -205,9 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
                     copy_boxes(base + st * S::stage, S::a, S::stage, &p.mx, m0, &p.mw, n0, b * kBlockK, bar(S::full + st));
                 }
             }
-            if (!go)                                  // what is on its way has to land before the block ends
-                for (uint32_t u = at > S::stages ? at - S::stages : 0; u < at; ++u)
-                    keep_waiting(bar(S::full + u % S::stages), (u / S::stages) & 1, &s_never, nullptr, kMatmulPolls);
+            copies_land<S::stages>(bar(S::full), at);
+            if (lane == 0) s_issued = at;
         } else if (warp == kSum / 32 + 1) {
             // ---------------------------------------------------------------- products
             uint32_t at = 0;
@@ -224,15 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
                     commit_warp(bar(S::empty + st));
                 }
             }
-            if (!go) {                                // and what was issued has to end
-                commit_warp(bar(S::drain));
-                keep_waiting(bar(S::drain), 0, &s_never, nullptr, kMatmulPolls);
-            }
+            products_end(bar(S::drain));
         }
     }
     __syncwarp();
     fence_before_sync();
     __syncthreads();
+    if (tid == 0) check_over<S::stages>(bar(S::full), s_issued, bar(S::drain), p.status);
     if (warp == kThreads / 32 - 1) {
         fence_after_sync();
         tmem_dealloc(tmem, 512);

@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::residents) matmul_few_ker
     using S = Shape<BT>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_stop, s_never;
+    __shared__ volatile int s_stop;
+    __shared__ uint32_t s_issued;                     // copies of this CTA (index-checking build)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     auto bar = [&](int i) { return base + S::bars + 8 * i; };
@@ -58,7 +59,6 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::residents) matmul_few_ker
 
     if (tid == 0) {
         s_stop = 0;
-        s_never = 0;
         for (int i = 0; i < S::stages; ++i) {
             mbar_init(bar(S::full + i), 1);
             mbar_init(bar(S::empty + i), 1);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::residents) matmul_few_ker
         }
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         named_bar_sync<1, kSum>();
-        for (int t = warp; t < have && go; t += kSum / 32) {
+        for (int t = warp; t < have; t += kSum / 32) {   // (after a wait that gave up, too, whatever is there: so every part arrives)
             const int to = t / slice;
             if (to == rank) continue;
             const float4 x = *reinterpret_cast<const float4 *>(smem_raw + (base - smem_u32(smem_raw)) + (t * kRows + 4 * lane) * 4);
@@ -198,9 +198,8 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::residents) matmul_few_ker
             if (!go) break;
             copy_boxes(base + st * S::stage, S::a, S::stage, &p.mw, n0, &p.mx, t0, (b0 + at) * kBlockK, bar(S::full + st));
         }
-        if (!go)                                      // what is on its way has to land before the block ends
-            for (int u = at > S::stages ? at - S::stages : 0; u < at; ++u)
-                keep_waiting(bar(S::full + u % S::stages), (u / S::stages) & 1, &s_never, nullptr, kMatmulPolls);
+        copies_land<S::stages>(bar(S::full), at);
+        if (lane == 0) s_issued = at;
     } else {
         bool go = true;
         for (int at = 0; at < b1 - b0; ++at) {
@@ -214,22 +213,23 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::residents) matmul_few_ker
             commit_warp(bar(S::empty + st));
             commit_warp(bar(S::ready + sum));
         }
-        if (!go) {                                    // and what was issued has to end
-            commit_warp(bar(S::drain));
-            keep_waiting(bar(S::drain), 0, &s_never, nullptr, kMatmulPolls);
-        }
+        products_end(bar(S::drain));
     }
     __syncwarp();
     if (warp >= kSum / 32) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     fence_before_sync();
     __syncthreads();
+    if (tid == 0) check_over<S::stages>(bar(S::full), s_issued, bar(S::drain), p.status);
     if (warp == kThreads / 32 - 1) {
         fence_after_sync();
         tmem_dealloc(tmem, S::columns);
     }
     // Every part has arrived, so nobody touches this CTA's shared memory any more, unless a wait gave up: then it stays until
-    // the others have left or given up, too.
-    if (s_stop) asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // the others have left or given up, too, and their parts, which they have sent by then, are here.
+    if (s_stop) {
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        mbar_wait(bar(S::met), 0, kMatmulPolls);
+    }
 }
 
 // Parts of K: as many as let all CTAs be resident at once, two on an SM.  Clusters of more than four leave more of them empty
