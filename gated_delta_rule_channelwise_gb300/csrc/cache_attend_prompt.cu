@@ -109,7 +109,7 @@ __device__ __noinline__ bool keep_waiting(uint32_t bar, uint32_t parity, volatil
 __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const AttendParams p) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_stop, s_never;          // a wait gave up: everybody leaves; (never set)
+    __shared__ volatile int s_stop;                   // a wait gave up: everybody leaves
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // the last rows, which see the most, first: what runs at the end is short
     const int b = blockIdx.y, hk = blockIdx.x, part = blockIdx.z % p.splits, pairs = gridDim.z / p.splits,
@@ -128,7 +128,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
     if (tid == 0) {
         s_stop = 0;
         mbar_init(bar(kQFull), tiles * kSoft / 32);
-        s_never = 0;
         for (int i = 0; i < 4; ++i) mbar_init(bar(kDrain + i), 1);
         mbar_init(bar(kNever), 1);
         for (int i = 0; i < 2; ++i) {
@@ -458,15 +457,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_prompt_kernel(const 
                     commit(bar(kVFree + (i & 1)));
                 }
             }
-            if (!go) {                                // what was issued has to end before its memory is given up
-                commit(bar(kDrain + which));
-                keep_waiting(bar(kDrain + which), 0, &s_never, nullptr, kPolls);
-            }
+            // What was issued has to end before its memory is given up, whichever wait gave up: the softmax threads may have left
+            // when everything had been issued.  (In any other case they wait for these products themselves.)
+            commit(bar(kDrain + which));
+            mbar_wait(bar(kDrain + which), 0, kPolls);
         }
     }
     __syncwarp();
     fence_before_sync();
     __syncthreads();
+#ifdef CGDR_DEBUG_CHECKS
+    if (tid < 4 && (tid & 1) < tiles && steps > 0) in_bounds(mbar_try_wait(bar(kDrain + tid), 0) ? 0 : -1, 1, p.status, nullptr);
+#endif
     if (warp == kThreads / 32 - 1) {
         fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
