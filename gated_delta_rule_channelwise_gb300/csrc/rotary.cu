@@ -1,7 +1,8 @@
 // Rotary positions (cgdr_rotary): pairs of channels of every head turned by their token's angle, in place.
 //
 // A frequency is kept as a 64-bit fraction of a turn, so that position * frequency modulo a turn is one integer
-// product, exact whatever the position; the nearest quarter turn is taken off before the remainder becomes fp32.
+// product, exact whatever the position; the nearest quarter turn is taken off and all that remains becomes fp32, so that the sine of a
+// slow pair has fp32's bits, too.
 // Bound by memory: 4,000 tokens of 32 + 8 heads of 128 bf16 (82 MB read and written) take 16.7 us, 12.1 at the copy rate; 4,011 tokens of 24 + 24
 // heads of 96 fp32, half of each turned (74 MB, in pieces of 192 bytes) 18.8, 10.9; 64 tokens 2.2, a launch.
 #include "layer.cuh"
@@ -41,7 +42,7 @@ __device__ __forceinline__ uint64_t fraction_of(double freq) {
 __device__ __forceinline__ float2 turn_of(int position, double freq, float scale) {
     const uint64_t phase = (uint64_t)position * fraction_of(freq);
     const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
-    const float rest = (float)(int32_t)((int64_t)(phase - ((uint64_t)quarter << 62)) >> 32) * 0x1p-31f;   // half turns, |rest| <= 1/4
+    const float rest = __ll2float_rn((int64_t)(phase - ((uint64_t)quarter << 62))) * 0x1p-63f;            // half turns, |rest| <= 1/4
     float s, c;
     sincospif(rest, &s, &c);
     const float cs = quarter & 1 ? s : c, sn = quarter & 1 ? c : s;

@@ -104,8 +104,9 @@ cgdr_status cgdr_matmul(const cgdr_matmul_args *args, void *stream);
  * pairs, in place.  Pair i of token t turns by a = positions[t] * freq[i]:
  *     (u, v) <- scale * (u cos a - v sin a, v cos a + u sin a)
  * u and v are channels i and i + half, or 2 i and 2 i + 1 (interleaved).  a is formed modulo a turn in 64
- * bits, so positions up to 2^31 lose nothing; cos, sin and the products are fp32.  Tokens with a position
- * below 0 stay as they are.
+ * bits, so positions up to 2^31 lose nothing; cos, sin and the products are fp32.  Of frequencies of 6e-12 and
+ * more (2^24 steps of 2^-64 turns) cos and sin are good to fp32's relative rounding, however small they are.  Tokens
+ * with a position below 0 stay as they are.
  */
 typedef struct cgdr_rotary_args {
     int32_t n, Hq, Hk, D;           /* Hk may be 0 */
