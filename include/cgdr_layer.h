@@ -34,7 +34,8 @@ extern "C" {
  *     h = x + residual;  residual <- h (rounded to its type)
  *     y = h / sqrt(mean(h^2) + eps) * weight
  * h, the mean and y in fp32; y is formed from h as it was before it was rounded.  The output is o, in
- * dtype, or y8 with its scales.  Squares that overflow fp32 (magnitudes above 1.8e19) make a row zero.
+ * dtype, or y8 with its scales.  The squares of a row are added up before they are divided by C: a row whose sum(h^2)
+ * overflows fp32 (3.4e38: one value above 1.8e19, or C = 4096 values above 2.9e17 each) becomes zero.
  */
 typedef struct cgdr_norm_args {
     int32_t n, H, C;                /* C a multiple of 8, at most 32768; H == 1 with y8 */
