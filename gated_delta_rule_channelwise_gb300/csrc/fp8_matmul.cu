@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
             const int row = tile % tiles_m * kRows + r, c = tile / tiles_m * BN + half * kCols;
             xs = p.xs + (int64_t)min(row, p.n - 1) * p.blocks;
             ws = p.ws + (int64_t)min(c / kBlockK, (p.N - 1) / kBlockK) * p.blocks;
-            xn = __ldg(xs);
-            wn = __ldg(ws);
+            xn = *xs;
+            wn = *ws;
         };
         scales_of(blockIdx.x);
         for (int tile = blockIdx.x; tile < tiles && go; tile += gridDim.x) {
@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tiles_kernel(const __grid_
             for (int b = 0; b < p.blocks; ++b, ++at) {
                 const f32x2 s = both(xn * wn);
                 if (b + 1 < p.blocks) {
-                    xn = __ldg(xs + b + 1);
-                    wn = __ldg(ws + b + 1);
+                    xn = xs[b + 1];
+                    wn = ws[b + 1];
                 }
                 const int sum = at % S::sums;
                 go = __all_sync(0xffffffffu, p.inject ? wait(S::never, 0) : wait(S::ready + sum, (at / S::sums) & 1));

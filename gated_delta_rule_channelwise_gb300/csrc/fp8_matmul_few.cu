@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, Shape<BT>::residents) matmul_few_ker
                 for (int e = tid; e < kAhead * BT; e += kSum) {
                     const int t = e / kAhead, k = e % kAhead;
                     float s = 0.f;
-                    if (b + k < b1 && t0 + t < p.n) s = __ldg(p.xs + (int64_t)(t0 + t) * p.blocks + b + k) * __ldg(ws + b + k);
+                    if (b + k < b1 && t0 + t < p.n) s = p.xs[(int64_t)(t0 + t) * p.blocks + b + k] * ws[b + k];
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + S::scales + (k * BT + t) * 4), "f"(s) : "memory");
                 }
                 named_bar_sync<1, kSum>();

@@ -19,7 +19,8 @@ inline bool disjoint(int64_t n, int64_t st, int64_t H, int64_t sh, int64_t d) {
 }
 
 // These kernels may be set up while the one before them in the stream ends: every thread waits for its results before it
-// touches global memory.
+// touches global memory.  What they read may be written while they are already there, so it is not read-only for as long as they live, as
+// the read-only path (__ldg) asks: they read with ordinary loads, which stay behind the wait.  (No case was slower by that.)
 __device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>
 cgdr_status launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, A &&...args) {
@@ -45,8 +46,7 @@ cgdr_status launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 template <typename T> struct Eight;
 template <> struct Eight<__nv_bfloat16> {
     uint4 r;
-    __device__ __forceinline__ void load(const void *p) { r = __ldg(static_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void fetch(const void *p) { r = *static_cast<const uint4 *>(p); }    // of what the call writes, too
+    __device__ __forceinline__ void load(const void *p) { r = *static_cast<const uint4 *>(p); }
     __device__ __forceinline__ void clear() { r = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void unpack(f32x2 (&f)[4]) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -66,10 +66,6 @@ template <> struct Eight<__nv_bfloat16> {
 template <> struct Eight<float> {
     ulonglong2 a, b;
     __device__ __forceinline__ void load(const void *p) {
-        a = __ldg(static_cast<const ulonglong2 *>(p));
-        b = __ldg(static_cast<const ulonglong2 *>(p) + 1);
-    }
-    __device__ __forceinline__ void fetch(const void *p) {
         a = static_cast<const ulonglong2 *>(p)[0];
         b = static_cast<const ulonglong2 *>(p)[1];
     }

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(kVecs, kThreads)) norm_ker
                 rv[k][j].clear();
                 if (row < p.rows && c < p.C) {
                     if (range_in_bounds(x0 + c, 8, p.ex, p.status, nullptr)) xv[k][j].load(static_cast<const T *>(p.x) + x0 + c);
-                    if (kResidual && range_in_bounds(r0 + c, 8, p.er, p.status, nullptr)) rv[k][j].fetch(static_cast<T *>(p.r) + r0 + c);
+                    if (kResidual && range_in_bounds(r0 + c, 8, p.er, p.status, nullptr)) rv[k][j].load(static_cast<T *>(p.r) + r0 + c);
                 }
             }
         }

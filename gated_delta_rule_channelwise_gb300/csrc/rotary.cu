@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams 
     const int tokens = kThreads >> p.shift, t0 = blockIdx.x * tokens, mine = threadIdx.x >> p.shift, t = t0 + mine;
     const int l = threadIdx.x & ((1 << p.shift) - 1), lane = l / p.units, unit = l - lane * p.units;
     wait_for_inputs();
-    const bool live = t < p.n && lane < p.rows && __ldg(p.positions + t) >= 0;
+    const bool live = t < p.n && lane < p.rows && p.positions[t] >= 0;
     constexpr int64_t kStep = kInterleaved ? 2 * V : V;
     const int64_t far = kInterleaved ? V : p.half;
     T *q = static_cast<T *>(p.q) + t * p.q_st + kStep * unit, *k = static_cast<T *>(p.k) + t * p.k_st + kStep * unit;
@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams 
         }
         if (first == lane) {                          // the first round, which every thread takes
             for (int e = threadIdx.x; e < tokens * p.half; e += kThreads) {
-                const int i = e / p.half, position = t0 + i < p.n ? __ldg(p.positions + t0 + i) : 0;
-                const float2 turn = turn_of(position, __ldg(p.freq + e - i * p.half), p.scale);
+                const int i = e / p.half, position = t0 + i < p.n ? p.positions[t0 + i] : 0;
+                const float2 turn = turn_of(position, p.freq[e - i * p.half], p.scale);
                 s_cos[e] = turn.x;
                 s_sin[e] = turn.y;
             }
