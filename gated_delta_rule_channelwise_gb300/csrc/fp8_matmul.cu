@@ -242,7 +242,7 @@ cgdr_status check(const cgdr_matmul_args *a) {
     if (!dtype_ok(a->o_dtype) || a->n > kMaxTokens || a->N > kMaxTokens || a->K > kMaxTokens) return CGDR_ERR_UNSUPPORTED;
     if ((int64_t)groups_of(a->n) * groups_of(a->N) > INT32_MAX / 2) return CGDR_ERR_UNSUPPORTED;
     if (a->n == 0 || a->N == 0) return CGDR_OK;
-    if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->o) return CGDR_ERR_INVALID_ARG;
+    if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->o || a->o == a->x || a->o == a->w) return CGDR_ERR_INVALID_ARG;
     if (a->n > 1 && (a->o_st < a->N || a->x_st < a->K)) return CGDR_ERR_INVALID_ARG;
     if (a->N > 1 && a->w_st < a->K) return CGDR_ERR_INVALID_ARG;
     if (!aligned_to(a->x, 16) || !aligned_to(a->w, 16) || !aligned_to(a->o, 16) || !aligned_to(a->x_scale, 4) || !aligned_to(a->w_scale, 4) ||

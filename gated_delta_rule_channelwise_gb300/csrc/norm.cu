@@ -188,6 +188,9 @@ cgdr_status check(const cgdr_norm_args *a) {
     if (a->y8 && !disjoint(a->n, a->y8_st, 1, 0, a->C)) return CGDR_ERR_INVALID_ARG;
     if ((a->residual && !disjoint(a->n, a->residual_st, a->H, a->residual_sh, a->C)) || (a->o && !disjoint(a->n, a->o_st, a->H, a->o_sh, a->C)))
         return CGDR_ERR_INVALID_ARG;
+    // In place: a thread reads what it holds of a row before it writes it, and no other row is there.
+    if (a->o == a->x && ((a->n > 1 && a->o_st != a->x_st) || (a->H > 1 && a->o_sh != a->x_sh))) return CGDR_ERR_INVALID_ARG;
+    if (a->y8 == a->x || (a->residual && (a->residual == a->x || a->residual == a->o || a->residual == a->y8))) return CGDR_ERR_INVALID_ARG;
     const int esz = esize(a->dtype);
     if (!aligned_to(a->x, 16) || !aligned_to(a->residual, 16) || !aligned_to(a->weight, 16) || !aligned_to(a->o, 16) ||
         !aligned_to(a->y8, 16) || !aligned_to(a->y_scale, 4) || !aligned_to(a->status, 4))
@@ -292,7 +295,7 @@ cgdr_status check(const cgdr_quantize_args *a) {
         return CGDR_ERR_UNSUPPORTED;
     if ((int64_t)a->n * groups_of(a->C) > INT32_MAX) return CGDR_ERR_UNSUPPORTED;
     if (a->n == 0) return CGDR_OK;
-    if (!a->x || !a->y8 || !a->y_scale || !disjoint(a->n, a->y8_st, 1, 0, a->C)) return CGDR_ERR_INVALID_ARG;
+    if (!a->x || !a->y8 || !a->y_scale || a->y8 == a->x || !disjoint(a->n, a->y8_st, 1, 0, a->C)) return CGDR_ERR_INVALID_ARG;
     if (!aligned_to(a->x, 16) || !aligned_to(a->y8, 16) || !aligned_to(a->y_scale, 4) || !aligned_to(a->status, 4))
         return CGDR_ERR_ALIGNMENT;
     return row_stride_ok(a->x_st, esize(a->dtype)) && row_stride_ok(a->y8_st, 1) ? CGDR_OK : CGDR_ERR_ALIGNMENT;

@@ -4,7 +4,7 @@ Python side of ``include/cgdr_layer.h``, in the manner of :mod:`.serve`: each ca
 the argument block of its C entry point and runs it on the current CUDA stream (or ``stream``).  Every step runs
 in the library's kernels and there is no CPU fallback.  The tensors of a call share one device, the current one.  Outputs that are
 not given come from torch's caching allocator; no call needs a workspace.  An output may not overlap an input, other than
-what is updated in place.
+what is updated in place and the o of :func:`rms_norm`, which may be x.
 
 * :func:`rms_norm`, :func:`rms_norm_fp8` -- root-mean-square norm with the residual's addition, the latter in 8 bits.
 * :func:`fp8_quantize`, :func:`fp8_quantize_weight` -- rows and weights in 8 bits.
@@ -83,7 +83,8 @@ def rms_norm(x, weight, o=None, *, residual=None, eps=1e-6, status=None, stream=
     """Root-mean-square norm of the rows of ``x [n,C]`` or ``[n,H,C]`` (fp32 or bf16, C a multiple of 8, at most 32768):
     ``h = x + residual``, ``o = h / sqrt(mean(h^2) + eps) * weight``.  ``weight [C]`` is fp32 (None: ones).  ``residual``, like x, is
     optional and updated in place: it becomes h, rounded; o is formed from h in fp32.  x, residual and o may be strided in
-    tokens and heads; rows are 16-byte aligned.  Returns o, like x."""
+    tokens and heads; rows are 16-byte aligned.  o may be x: the norm in place, of heads in a packed row for
+    instance.  Returns o, like x."""
     if stream is not None:
         return _on(stream, rms_norm, x, weight, o, residual=residual, eps=eps, status=status)
     if x.dim() not in (2, 3):

@@ -7,7 +7,8 @@
  * dimension contiguous, asynchronous on `stream`, launched on the calling thread's current device,
  * every buffer owned by the caller, nothing allocated, no workspace, arguments checked on the host
  * before any launch, no C++ exception across the ABI.  No input may alias an output other than the
- * buffers that are named as updated in place.  Rows need 16-byte aligned base pointers and strides
+ * buffers that are named as updated in place and the norm's o, which may be x; equal addresses are
+ * refused, overlaps of other kinds are not looked for.  Rows need 16-byte aligned base pointers and strides
  * of a multiple of 16 bytes; rows that a call writes may not overlap.
  *
  * 8 bits: e4m3 values (sign, four exponent bits, three of mantissa, no infinity, largest 448) with
@@ -44,7 +45,7 @@ typedef struct cgdr_norm_args {
     const void *x;  int64_t x_st, x_sh;         /* [n,H,C] */
     void *residual; int64_t residual_st, residual_sh;         /* [n,H,C] or NULL; in place */
     const float *weight;                        /* [C], 16-byte aligned, or NULL for ones */
-    void *o;        int64_t o_st, o_sh;         /* [n,H,C], or NULL with y8 */
+    void *o;        int64_t o_st, o_sh;         /* [n,H,C], or NULL with y8; may be x, with its strides */
     void *y8;       int64_t y8_st;              /* [n,C], or NULL with o */
     float *y_scale;                             /* [n, ceil(C/128)] dense */
     int32_t *status;                            /* reserved for the index-checking build */
