@@ -88,7 +88,7 @@ class HybridDecoder:
             norm = cg.rms_norm_fp8 if self.eight_bit and p["kind"] == "attend" else cg.rms_norm
             h = norm(x, None) if y is None else norm(y, None, residual=x)
             y = getattr(self, "_" + p["kind"])(p, s, h, plan, lens, longest, single)
-            y = cg.fp8_matmul(*cg.fp8_quantize(y), *p["out"]) if self.eight_bit and p["kind"] == "attend" else y @ p["out"]
+            y = cg.fp8_matmul(*cg.fp8_quantize(y), *p["out"], status=self.status) if self.eight_bit and p["kind"] == "attend" else y @ p["out"]
         return cg.rms_norm(y, None, residual=x) @ self.head
 
     def _conv(self, x, taps, state, plan, single):
@@ -122,7 +122,7 @@ class HybridDecoder:
         return cg.scan_prefill(u, x @ p["dt"], p["A_log"], Bm, Cm, s["h"], cu_seqlens=plan.cu_seqlens, **kw)
 
     def _attend(self, p, s, x, plan, lens, longest, single):
-        row = cg.fp8_matmul(*x, *p["qkv"]) if self.eight_bit else x @ p["qkv"]
+        row = cg.fp8_matmul(*x, *p["qkv"], status=self.status) if self.eight_bit else x @ p["qkv"]
         q, k, v = (t.unflatten(-1, (-1, self.d)) for t in row.split([self.C, self.Hkv * self.d, self.Hkv * self.d], -1))
         cg.rotary(q, k, plan.positions, self.freq, scale=self.turn_scale)
         cg.cache_append(k, v, plan.slots, s["k"], s["v"], s["ks"], s["vs"], status=self.status)

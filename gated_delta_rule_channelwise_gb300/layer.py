@@ -172,7 +172,8 @@ def fp8_matmul(x, x_scale, w, w_scale, o=None, *, dtype=torch.bfloat16, path=MAT
     (:func:`fp8_quantize_weight`).  Any n, N and K; rows of x, w and o are 16-byte aligned (new outputs of all these calls
     have strides that give that).  Products are exact, sums fp32.  Returns o ``[n,N]``, the given one (fp32 or bf16) or a new one of
     ``dtype``.  ``path`` forces one of the two kernels for this call (``MATMUL_FEW``, ``MATMUL_TILES``).
-    ``wait_polls``: polls of a bounded device wait (0: the default; ``ERR_TIMEOUT`` in ``status`` when one gives up)."""
+    ``wait_polls``: polls of a bounded device wait (0: the default).  When one gives up o is undefined and ``status`` holds
+    ``ERR_TIMEOUT``; without ``status`` nothing says so."""
     if stream is not None:
         return _on(stream, fp8_matmul, x, x_scale, w, w_scale, o, dtype=dtype, path=path, status=status, wait_polls=wait_polls)
     device = x.get_device()
