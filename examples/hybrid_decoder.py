@@ -89,7 +89,7 @@ class HybridDecoder:
             h = norm(x, None) if y is None else norm(y, None, residual=x)
             y = getattr(self, "_" + p["kind"])(p, s, h, plan, lens, longest, single)
             y = cg.fp8_matmul(*cg.fp8_quantize(y), *p["out"], status=self.status) if self.eight_bit and p["kind"] == "attend" else y @ p["out"]
-        return cg.rms_norm(y, None, residual=x) @ self.head
+        return (cg.rms_norm(x, None) if y is None else cg.rms_norm(y, None, residual=x)) @ self.head
 
     def _conv(self, x, taps, state, plan, single):
         return cg.conv_decode(x, taps, state) if single else cg.conv_prefill(x, taps, state, cu_seqlens=plan.cu_seqlens)
