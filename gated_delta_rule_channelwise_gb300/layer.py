@@ -243,6 +243,8 @@ def rotary_frequencies(R, base=10000.0, *, scaling=None, factor=1.0, length=4096
         raise ValueError("R must be even and above 0, got %s" % R)
     if not (base > 0 and factor >= 1 and length > 0 and fast > slow > 0):
         raise ValueError("base, length and slow must be above 0, factor at least 1 and fast above slow")
+    if scaling == "ramp" and base <= 1:
+        raise ValueError("the ramp needs frequencies that fall: base must be above 1, got %s" % base)
     if scaling == "base" and R > 2:
         base = base * factor ** (R / (R - 2))
     i = torch.arange(0, R, 2, dtype=_F64)
