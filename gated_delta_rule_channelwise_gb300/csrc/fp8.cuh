@@ -24,7 +24,9 @@ cgdr_status launch_matmul_tiles(const cgdr_matmul_args &a, MatmulParams &p, cuda
 // A tensor map of [rows, K] bytes with boxes of 128 bytes by `box` rows, swizzled by 128 bytes.
 bool encode_rows(CUtensorMap &m, const void *base, int64_t K, int64_t rows, int64_t stride, int box);
 
-constexpr uint32_t kMatmulPolls = 1u << 18;           // of a wait, before it gives up (args.wait_polls, 0)
+// Polls of a wait, before it gives up (args.wait_polls, 0).  The longest wait of a call that goes well is for a few blocks of K, or for the
+// other parts of a cluster, which began together: microseconds.
+constexpr uint32_t kMatmulPolls = 1u << 18;
 constexpr int kBlockK = 128;                          // bytes of a row in a stage: the values of a scale
 
 namespace fp8 {

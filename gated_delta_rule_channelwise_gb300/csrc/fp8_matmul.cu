@@ -8,12 +8,7 @@
 // 4,001 x 12,288 x 4,096: 154 to 158 us (the GPU is near its power limit), 2,580 TFLOP/s, 0.68 of twice what a large bf16 product reaches.  A block of
 // 128 x 256 x 128 takes 710 cycles there (the slope along K; without copies 680), the products alone 512, the sums alone 560, and a sum that is
 // handed over and back waits 390; a tile begins and ends in 4,000 more, of which most is 64 KB of results on their way while every SM stores.
-// A block of 128 columns takes 460 to 490, of which issuing takes 400 and its operands' way from L2 425.  Measured, and no better: two warps that issue (155), four sums of 128 columns
-// (156), a look at the next sum ahead of its wait (158), w's half copied to both of a pair of CTAs (154), results stored by other warps during the
-// next tile (154: the buffer costs a stage of operands), 128 columns with every other block for each half of the sums' threads (10 % slower), one barrier for a
-// sum that is there and operands that are not needed any more (the same).
-// While one lane issued, behind a branch (163): three sums of 160 columns (177), 512 threads for the sums (188), a pair of CTAs on one product (185), a
-// last round of half tiles (163).
+// A block of 128 columns takes 460 to 490, of which issuing takes 400 and its operands' way from L2 425.
 #include "fp8.cuh"
 
 namespace cgdr {
@@ -276,7 +271,7 @@ bool encode_rows(CUtensorMap &m, const void *base, int64_t K, int64_t rows, int6
 
 cgdr_status launch_matmul_tiles(const cgdr_matmul_args &a, MatmulParams &p, cudaStream_t s) {
     // A tile of 256 columns takes 14.0 us of K = 4096 where there are many, one of 128 8.9: 1500 rows of 4096 x 4096 (2 rounds of the SMs against
-    // 3) 31.1 us and 30.2, 2500 (3 against 5) 44.9 and 47.7, 600 (1 against 2) 16.7 and 21.0.
+    // 3) 31.1 us and 30.2, 2500 (3 against 5) 44.9 and 47.7, 600 (1 against 2) 16.7 and 21.0 (each forced; what is taken now takes 30.0, 44.5 and 16.6).
     const int64_t sms = device_sms() > 0 ? device_sms() : 152, rows = (a.n + kRows - 1) / kRows;
     const int64_t wide = (rows * ((a.N + 255) / 256) + sms - 1) / sms, narrow = (rows * groups_of(a.N) + sms - 1) / sms;
     return 5 * wide <= 3 * narrow ? launch<256>(a, p, s) : launch<128>(a, p, s);

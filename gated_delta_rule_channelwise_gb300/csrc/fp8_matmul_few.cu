@@ -5,7 +5,7 @@
 // are sent to one CTA of the cluster, which adds them in their order: no workspace, and no order of arrival in a result.
 // Block by block of K as in the tiles kernel: a product in tensor memory, taken from there, scaled and added up in registers, a
 // thread a row of w.
-// One row by 12288 x 4096 (50.4 MB) takes 11.8 us, 64 rows by 4096 x 12288 15.0: the bytes at the copy rate are 7.4 and 7.6, the launch is
+// One row by 12288 x 4096 (50.4 MB) takes 11.7 us, 64 rows by 4096 x 12288 14.2: the bytes at the copy rate are 7.4 and 7.6, the launch is
 // 2, and the parts meet in 0.4 and 1.6 (they pass between shared memories at 17 bytes a clock).  A cluster barrier after the parts have been read
 // cost 0.9, sends of 4 bytes instead of 16 another 0.4.
 #include "fp8.cuh"
@@ -268,11 +268,11 @@ template <int BT> cgdr_status launch(const cgdr_matmul_args &a, MatmulParams &p,
 
 // This kernel, where its tiles are few enough to be split, unless K is so short that there is little to split; where K is
 // long, also where they just run all at once.  Here / the better of the two tile widths there, us:
-//   4096 x 4096:   n = 64 8.8 / 11.2,    128 10.2 / 11.4,  256 13.2 / 11.5,  320 20.1 / 11.8
-//   12288 x 4096:  n = 32 13.3 / 14.0,   64 15.0 / 14.2,   128 21.1 / 14.8
-//   4096 x 12288:  n = 128 18.0 / 29.3,  192 22.0 / 28.4,  256 27.7 / 28.5,  320 48.5 / 28.3
-//   1000 x 4096:   n = 512 10.0 / 11.4,  640 11.2 / 11.5,  1000 13.3 / 11.8
-//   512 x 512:     n = 16 3.8 / 4.1,     64 5.7 / 4.0
+//   4096 x 4096:   n = 64 8.5 / 11.1,    128 10.0 / 11.2,  256 12.8 / 11.3,  320 19.3 / 11.5
+//   12288 x 4096:  n = 32 12.6 / 13.5,   64 14.1 / 13.6,   128 20.3 / 13.9
+//   4096 x 12288:  n = 64 14.3 / 26.8,   128 17.8 / 28.6,  192 21.3 / 28.0,  256 27.0 / 28.2,  320 46.6 / 28.1
+//   1000 x 4096:   n = 512 10.0 / 11.4,  640 10.9 / 11.5,  1000 12.6 / 11.5
+//   512 x 512:     n = 16 3.4 / 3.6,     64 4.9 / 3.5
 bool matmul_few(const cgdr_matmul_args &a) {
     if (a.path != CGDR_MATMUL_AUTO) return a.path == CGDR_MATMUL_FEW;
     const int64_t sms = device_sms() > 0 ? device_sms() : 152, tiles = (int64_t)((a.n + 63) / 64) * groups_of(a.N);

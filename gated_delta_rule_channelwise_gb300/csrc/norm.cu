@@ -2,7 +2,9 @@
 //
 // All of it is bound by memory.  4,001 rows of 4,096 bf16 with residual, in 8 bits (115 MB): 21.0 us, 17.0 at the copy rate.
 // 128,000 heads of 128 bf16 out of packed rows (66 MB): 13.4 us, 9.7.  64 rows of 4,096: 2.3 us, a launch.  4,001 rows of 4,096 bf16
-// into 8 bits (50 MB): 10.0 us, 7.3; a weight of 12288 x 4096 (151 MB): 25.0 us, 22.2.  Consecutive launches are 1.5 to 2 us apart, which
+// into 8 bits (50 MB): 10.0 us, 7.3; a weight of 12288 x 4096 (151 MB): 25.0 us, 22.2.  4,001 rows of 4,096 fp32 with residual (262 MB):
+// 50.8 us, 38.6; in 8 bits (213 MB) 38.4, 31.4.  Those forms, and others of fp32 with residual, spill 50 to 90 bytes a thread: the residency below was
+// fitted on bf16, whose forms spill nothing.  Consecutive launches are 1.5 to 2 us apart, which
 // these times include.
 #include "layer.cuh"
 

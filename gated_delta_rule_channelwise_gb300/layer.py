@@ -22,7 +22,7 @@ import math
 import torch
 
 from . import MATMUL_AUTO, CgdrError, _need_cuda, lib
-from . import serve as _serve  # noqa: F401 (its notion of the current device: _serve._here)
+from . import serve as _serve
 from .serve import _CODES, _F32, _I32, Block, _address, _current, _fits, _i, _on, _on_device, _p, _refuse, _status_word, _strided
 
 _E4M3, _F64 = torch.float8_e4m3fn, torch.float64
